@@ -63,6 +63,10 @@ typedef enum {
 #define NVFP4_DEV_BAD_SCALE 2       /* s_pre not in [FLT_MIN, FLT_MAX] or a   */
                                     /* non-finite s_post                       */
 #define NVFP4_DEV_BAD_AMAX 4        /* a global amax is NaN, Inf or negative  */
+#define NVFP4_DEV_BAD_INDEX 8       /* a length, position, slot or page index  */
+                                    /* out of range (nothing is read or        */
+                                    /* written there)                          */
+#define NVFP4_DEV_NO_PAGES 16       /* fewer free pages than the requests need */
 
 /* nvfp4_config.blocks */
 #define NVFP4_BLOCKS_ROW 1  /* 1x16 blocks along the last dimension            */
@@ -367,6 +371,176 @@ NVFP4_API nvfp4_status nvfp4_requant_transpose(const nvfp4_config* src, const nv
 NVFP4_API nvfp4_status nvfp4_mx_quantize(const nvfp4_config* cfg, const void* x, int64_t slices,
                                          int64_t rows, int64_t cols, const nvfp4_out* row,
                                          const nvfp4_out* col, int32_t* status, void* stream);
+
+/* ---- attention with the KV cache held in NVFP4 ---------------------------
+ * The pages describe the number format and its two-level scale; a cache in
+ * that format and the operators around it have no counterpart there.
+ *
+ * The cache is paged. A page holds page_size token slots of every KV head;
+ * slot number = page * page_size + offset. K and V rows are NVFP4 row
+ * encodings: blocks of 16 along head_dim, E4M3 block scales, one FP32 outer
+ * scale per KV head and tensor, g = amax / (6 M) as everywhere in this
+ * library. The amax values are fixed when the cache is set up (calibrated:
+ * tokens arrive over time and share them); larger values saturate. */
+typedef struct {
+  uint8_t* k_codes;      /* [pages][kv_heads][page_size][head_dim/2]           */
+  uint8_t* k_scales;     /* [pages][kv_heads][page_size][head_dim/16]          */
+  uint8_t* v_codes;      /* as k_codes                                         */
+  uint8_t* v_scales;     /* as k_scales                                        */
+  const float* k_amax;   /* fp32 [kv_heads]                                    */
+  const float* v_amax;   /* fp32 [kv_heads]                                    */
+  int64_t pages;
+  int32_t kv_heads;
+  int32_t page_size;     /* token slots per page, a multiple of 16             */
+  int32_t head_dim;      /* 64 or 128                                          */
+  int32_t four_over_six; /* 1: appended blocks choose between max->6 and       */
+                         /* max->4 (MSE rule), M = 256; 0: M = 448             */
+} nvfp4_kv_cache;
+
+/* bf16 rows of heads: token t, head h, element d at ptr[t*stride + h*head_dim
+ * + d]. stride (in elements, a multiple of 8) may exceed heads * head_dim: a
+ * view of a packed projection output. ptr 16-byte aligned. */
+typedef struct {
+  void* ptr;
+  int64_t stride;
+} nvfp4_rows;
+
+/* Block tables and slot maps from request lengths, in one launch. Request b
+ * has cached_len[b] tokens in the cache and gets new_len[b] more (int32
+ * [requests]). With held = ceil(cached/page_size) and total =
+ * ceil((cached + new)/page_size), entries held .. total-1 of row b of
+ * block_table (int32 [requests][table_cols]) receive the next pages of
+ * free_pages (int32 [free_count]), requests in order; other entries are left
+ * as they are. Written besides:
+ *   seq_len   int32 [requests]      cached + new
+ *   q_start   int32 [requests + 1]  first row of each request among the new
+ *                                   tokens (exclusive prefix sum of new_len)
+ *   slots     int64 [tokens]        cache slot of each new token
+ *   positions int32 [tokens]        its position in its request
+ *   pages_used int32 [1]            pages taken from free_pages
+ * Rows past the last new token (a batch padded to `tokens`) get slot -1 and
+ * position 0. free_pages is only read: the caller drops the first pages_used
+ * entries. The call can be repeated with the same result.
+ * Data errors: NVFP4_DEV_BAD_INDEX for a negative length, more pages than
+ * table_cols or more new tokens than `tokens` (the excess gets no slot);
+ * NVFP4_DEV_NO_PAGES when free_pages runs out (table entry and slots -1).
+ * Errors: NULL pointers, negative sizes, page_size < 1, requests, tokens,
+ * table_cols or free_count above 2^31 - 1, misaligned pointers. */
+NVFP4_API nvfp4_status nvfp4_kv_plan(const int32_t* cached_len, const int32_t* new_len,
+                                     int64_t requests, int32_t* block_table, int64_t table_cols,
+                                     int32_t page_size, const int32_t* free_pages,
+                                     int64_t free_count, int64_t tokens, int32_t* seq_len,
+                                     int32_t* q_start, int64_t* slots, int32_t* positions,
+                                     int32_t* pages_used, int32_t* status, void* stream);
+
+/* RMS norm of every query and key head and the rotation of its positions in
+ * the same pass. */
+typedef struct {
+  int64_t tokens;
+  int32_t q_heads;
+  int32_t kv_heads;          /* either may be 0: the other alone               */
+  int32_t head_dim;          /* 64 or 128                                      */
+  int32_t rotary_dim;        /* elements 0 .. rotary_dim-1 are rotated; a       */
+                             /* multiple of 16, at most head_dim               */
+  int32_t interleaved;       /* 0: pairs (i, i + rotary_dim/2); 1: (2i, 2i + 1) */
+  float eps;
+  const void* q_weight;      /* bf16 [head_dim]; NULL: queries are not normed  */
+  const void* k_weight;      /* bf16 [head_dim]; NULL: keys are not normed     */
+  const int32_t* positions;  /* int32 [tokens]                                 */
+  const float* cos_sin;      /* fp32 [max_pos][rotary_dim]: rotary_dim/2        */
+                             /* cosines, then as many sines                    */
+  int64_t max_pos;
+} nvfp4_qk_config;
+
+/* Per token and head, in fp32 with one rounding to bf16 at the end:
+ *   y = x * rsqrt(mean(x^2) + eps) * w     (y = x without a weight)
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for every rotated pair of y.
+ * Outputs may be the inputs themselves (same ptr and stride).
+ * A position outside [0, max_pos) sets NVFP4_DEV_BAD_INDEX; position 0 stands
+ * in for it.
+ * Errors: NULL required pointers, sizes out of range, strides below
+ * heads * head_dim or not a multiple of 8, eps negative or not finite
+ * (NVFP4_ERR_ENUM), misalignment. */
+NVFP4_API nvfp4_status nvfp4_qk_norm_rope(const nvfp4_qk_config* cfg, nvfp4_rows q, nvfp4_rows k,
+                                          nvfp4_rows q_out, nvfp4_rows k_out, int32_t* status,
+                                          void* stream);
+
+/* Its gradient: gq_out, gk_out are the loss's gradients of the outputs, q and
+ * k the forward's inputs. With u the gradient rotated back, r = rsqrt(mean(x^2)
+ * + eps): gw = sum over tokens and heads of u x r, gx = r (w u - x r^2
+ * mean(w u x)); without a weight gx = u.
+ * gq_weight, gk_weight: fp32 [head_dim], overwritten, required iff the weight
+ * is given (NULL otherwise). They are summed in a fixed order: the same inputs
+ * give the same bits on the same device. gq may be gq_out, gk may be gk_out.
+ * workspace: device memory, >= nvfp4_qk_norm_rope_ws_bytes() bytes, 16-byte
+ * aligned, ALL ZERO before its first use; every call leaves its counters zero
+ * again. It serves one call at a time. May be NULL when no weight is given.
+ * Errors: as nvfp4_qk_norm_rope, plus those of the workspace (as
+ * nvfp4_amax_ws). */
+NVFP4_API size_t nvfp4_qk_norm_rope_ws_bytes(void);
+NVFP4_API nvfp4_status nvfp4_qk_norm_rope_bwd(const nvfp4_qk_config* cfg, nvfp4_rows gq_out,
+                                              nvfp4_rows gk_out, nvfp4_rows q, nvfp4_rows k,
+                                              nvfp4_rows gq, nvfp4_rows gk, float* gq_weight,
+                                              float* gk_weight, void* workspace, size_t ws_bytes,
+                                              int32_t* status, void* stream);
+
+/* Quantise the K and V rows of `tokens` tokens into the cache: token t goes to
+ * slot slots[t] (int64; -1 skips the token). The bytes written are those of
+ * nvfp4_quantize on each head's rows with that head's amax (row blocks, E4M3
+ * scales, RNE, cache->four_over_six). k_dq, v_dq (bf16
+ * [tokens][kv_heads][head_dim], either may be NULL) receive the values that
+ * the codes stand for, of skipped tokens too. Two tokens of one call must not
+ * share a slot.
+ * Data errors: NVFP4_DEV_BAD_INDEX for a slot other than -1 outside the cache
+ * (the token is skipped), NVFP4_DEV_NONFINITE_INPUT, NVFP4_DEV_BAD_AMAX.
+ * Errors: NULL pointers, sizes out of range, strides as nvfp4_qk_norm_rope,
+ * misalignment (cache arrays 16 bytes). */
+NVFP4_API nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, nvfp4_rows k, nvfp4_rows v,
+                                       const int64_t* slots, int64_t tokens, void* k_dq,
+                                       void* v_dq, int32_t* status, void* stream);
+
+/* Attention of new queries over the cache. Request b owns query rows
+ * q_start[b] .. q_start[b+1]-1 (n of them) and the first seq_len[b] tokens of
+ * its block table row; row i of it stands at position p = seq_len[b] - n + i
+ * and sees the keys at positions <= p, with window > 0 only those > p -
+ * window. Query head h reads KV head h / (q_heads / kv_heads).
+ *   out = softmax(scale * q . K^T) V,  lse = log(sum(exp(scale * q . K^T)))
+ * A row that sees no key (an empty request, or n > seq_len) gets out = 0 and
+ * lse = -infinity. What the cache holds past seq_len or outside the window
+ * does not matter, NaN scale bytes included. Accumulation, softmax statistics
+ * and partial results are fp32; K and V enter the products exactly, the
+ * probabilities rounded to f16. */
+typedef struct {
+  const int32_t* block_table;  /* int32 [requests][table_cols]                   */
+  const int32_t* seq_len;      /* int32 [requests]                               */
+  const int32_t* q_start;      /* int32 [requests + 1]                           */
+  int64_t requests;
+  int64_t table_cols;
+  int64_t tokens;              /* query rows                                     */
+  int32_t q_heads;             /* a multiple of cache->kv_heads                  */
+  int32_t max_q;               /* no request has more query rows than this       */
+  int32_t window;              /* 0 = no window                                  */
+  float scale;
+} nvfp4_attention_config;
+
+/* q: bf16 rows; out: bf16 [tokens][q_heads][head_dim]; lse: fp32
+ * [tokens][q_heads], may be NULL. Rows that no request owns are not written.
+ * workspace: device memory, >= nvfp4_kv_attention_ws_bytes() bytes, 16-byte
+ * aligned, ALL ZERO before its first use; every call leaves its counters zero
+ * again. It serves one call at a time.
+ * Results are the same bits for the same inputs on the same device.
+ * Data errors: NVFP4_DEV_BAD_INDEX for a page outside the cache (page 0 stands
+ * in for it), a seq_len past the table or q_start out of order or past
+ * `tokens`, or more than max_q rows in a request (such a request is skipped);
+ * NVFP4_DEV_NONFINITE_INPUT for NaN or Inf in q; NVFP4_DEV_BAD_AMAX.
+ * Errors: NULL pointers, sizes out of range, head counts, head_dim, misaligned
+ * pointers, a scale that is not finite (NVFP4_ERR_ENUM), and those of the
+ * workspace (as nvfp4_amax_ws). */
+NVFP4_API size_t nvfp4_kv_attention_ws_bytes(void);
+NVFP4_API nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache,
+                                          const nvfp4_attention_config* cfg, nvfp4_rows q,
+                                          void* out, float* lse, void* workspace, size_t ws_bytes,
+                                          int32_t* status, void* stream);
 
 /* ---- diagnostics: the device codecs element by element -------------------
  * For exhaustive checks of the conversions the kernels use. op:

@@ -29,7 +29,9 @@ __all__ = [
     "alloc_encoding", "alloc_requant", "PeriodicAmax", "BLOCKS_ROW", "BLOCKS_COL", "BLOCKS_BOTH",
     "BLOCKS_TILE16",
     "SCALE_E4M3", "SCALE_UE5M3", "ROUND_RNE", "ROUND_SR", "FOS_MSE", "FOS_MAE", "FOS_MAX",
-    "DEV_NONFINITE_INPUT", "DEV_BAD_SCALE", "DEV_BAD_AMAX",
+    "DEV_NONFINITE_INPUT", "DEV_BAD_SCALE", "DEV_BAD_AMAX", "DEV_BAD_INDEX", "DEV_NO_PAGES",
+    "alloc_kv_cache", "kv_attention_workspace", "nvfp4_kv_append", "nvfp4_kv_attention",
+    "nvfp4_kv_plan", "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_bwd", "qk_norm_rope_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +42,7 @@ FOS_MSE, FOS_MAE, FOS_MAX = 0, 1, 2
 SCALE_E4M3, SCALE_UE5M3 = 0, 1
 ROUND_RNE, ROUND_SR = 0, 1
 DEV_NONFINITE_INPUT, DEV_BAD_SCALE, DEV_BAD_AMAX = 1, 2, 4
+DEV_BAD_INDEX, DEV_NO_PAGES = 8, 16
 TARGET_MXFP8, TARGET_NVFP4 = 0, 1
 
 _STATUS = {0: "ok", 1: "null pointer", 2: "shape", 3: "alignment", 4: "enum", 6: "cuda"}
@@ -135,6 +138,7 @@ def lib() -> C.CDLL:
                          "nvfp4_scale_init_mse", "nvfp4_export_scales", "nvfp4_mx_quantize",
                          "nvfp4_scale_grad_bwd", "nvfp4_codec_probe", "nvfp4_sr_bits"):
                 getattr(L, name).restype = C.c_int
+            kv.declare(L)
             _lib = L
     return _lib
 
@@ -636,3 +640,9 @@ class PeriodicAmax:
             self._fn(x, self.amax)
             self.refreshes += 1
         return self.amax
+
+
+from . import kv  # noqa: E402  (the cache operators use the marshalling above)
+from .kv import (alloc_kv_cache, kv_attention_workspace, nvfp4_kv_append,  # noqa: E402
+                 nvfp4_kv_attention, nvfp4_kv_plan, nvfp4_qk_norm_rope, nvfp4_qk_norm_rope_bwd,
+                 qk_norm_rope_workspace)

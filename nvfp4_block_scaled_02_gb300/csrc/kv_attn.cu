@@ -1,0 +1,587 @@
+// kv_attn.cu -- attention over a paged KV cache held in NVFP4, for few query
+// rows per KV head (single tokens and a few drafted ones, grouped heads).
+//
+//   out = softmax(scale q K^T) V over the keys a row sees,
+//   K = code_k * scale_k * g_k, V = code_v * scale_v * g_v.
+//
+// Numerics. code * block scale has at most 2 + 4 significant bits and lies in
+// [2^-10, 2688], so it is exact in f16; g_k goes into the softmax scale and
+// g_v into the final division. A query row is multiplied by a power of two
+// that puts its largest element in [2^13, 2^14): its bf16 elements are then
+// exact in f16 down to 2^-27 of that one, and off by at most 2^-39 of it below.
+// Scores, maxima, sums and outputs are fp32. The probabilities are rounded to
+// f16 for the second product (2^-11 relative; the sum that divides them is
+// taken before rounding), times 2^kBias so that they stay normal down to
+// 2^-20 of the largest.
+//
+// One pass over K and V with a running maximum per row. The maximum is only
+// raised (and the accumulators rescaled) when a score exceeds it by more than
+// kSlack powers of two: the result is the same, the rescaling is rare, and
+// 2^(kBias + kSlack) is far from f16's largest value.
+//
+// Work split. A query row block (the rows of one request that share a KV head)
+// and its tiles of 16 tokens form an item; all items' tiles, one after the
+// other, are cut into equal runs, one per CTA, whatever the requests' lengths.
+// An item cut between CTAs leaves a record (out, maximum, sum) per CTA in the
+// workspace, and the CTA that takes the item's last ticket joins the records
+// in order. Inside a CTA the warps take tiles in turn and join at the item's
+// end.
+//
+// Tile layout (m16n8k16, K or V as the 16-row operand, query rows as the 8
+// columns). Lane (g, t) = (lane / 4, lane % 4). Which token a K row index
+// stands for and which dimension a k index stands for are free as long as both
+// products agree, so they are chosen for wide loads: lane t holds dimensions
+// [t D/4, (t+1) D/4) of K rows g and g + 8 (one 128-bit load each), and lane g
+// holds dimensions [g D/8, (g+1) D/8) of V for the tokens 4 i + t, i < 4. The
+// probabilities of K rows (g, g + 8) become the second product's operand by an
+// 8x8 transpose between lanes. Two V bytes of neighbouring tokens are merged
+// to (even nibbles) and (odd nibbles) before conversion, so that a converted
+// pair holds one dimension of two tokens, as the operand wants.
+#include "kv.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kBias = 6;
+constexpr float kSlack = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two E4M3 scale bytes (low 16 bits) -> f16x2, exact.
+__device__ __forceinline__ uint32_t scales2(uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(r) : "r"(b));
+  return r;
+}
+// 8 codes of a word -> 4 f16x2 (byte i: low nibble in the low half).
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A request's rows and keys. rows = query tokens; keys [lo, hi) are seen by
+// some row, lo rounded down to a tile.
+struct Request {
+  int q0, n, len, lo16, tiles;
+};
+__device__ __forceinline__ Request request(const KvAttnParams& p, int b, bool& bad) {
+  Request r;
+  r.q0 = p.q_start[b];
+  const int q1 = p.q_start[b + 1];
+  r.len = p.seq_len[b];
+  r.n = q1 - r.q0;
+  bad = r.q0 < 0 || q1 < r.q0 || q1 > p.T || r.n > p.max_q || r.len < 0 ||
+        r.len > INT32_MAX - 16 || (int64_t)r.len > (int64_t)p.cols * p.P;
+  if (bad) r.q0 = r.n = r.len = 0;
+  int lo = 0;
+  if (p.window > 0) lo = max(0, r.len - r.n + 1 - min(p.window, r.len));
+  r.lo16 = lo & ~15;
+  r.tiles = r.n > 0 ? (r.len - r.lo16 + 15) >> 4 : 0;
+  return r;
+}
+
+template <int D>
+struct Stage {
+  uint8_t k[16 * D / 2], v[16 * D / 2], ks[16 * D / 16], vs[16 * D / 16];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+    kv_attn_kernel(const KvAttnParams p, const int ctas) {
+  pdl_begin();
+  constexpr int kStages = 5;
+  constexpr int kRows = 8 * NT;  // query rows of an item at most
+  constexpr int KS = D / 16;     // k steps of q K^T, and 16-row tiles of V^T
+  constexpr int DQ = D / 4;      // dimensions of K per lane
+  extern __shared__ __align__(16) uint8_t smem[];
+  Stage<D>* stages = reinterpret_cast<Stage<D>*>(smem) + (threadIdx.x >> 5) * kStages;
+  float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][kRows][D], after the tiles are done
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ int s_b0;
+  __shared__ int64_t s_off;
+  __shared__ uint32_t s_ticket;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+
+  // ---- this CTA's run of tiles: a scan over the requests -------------------
+  const int share = (p.B + kThreads - 1) / kThreads;
+  const int rb0 = min(tid * share, p.B), rb1 = min(rb0 + share, p.B);
+  int64_t mine = 0;
+  for (int b = rb0; b < rb1; ++b) {
+    bool bad;
+    const Request r = request(p, b, bad);
+    if (bad && blockIdx.x == 0) flag(p.status, kDevBadIndex);
+    const int blocks = (r.n * p.G + kRows - 1) / kRows;
+    mine += (int64_t)r.tiles * blocks * p.hk;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(kAll, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) incl += s_scan[w];
+    total += s_scan[w];
+  }
+  // equal runs, 8 tiles (two per warp) at least
+  const int64_t run = max((total + ctas - 1) / ctas, (int64_t)(2 * kWarps));
+  const int64_t first = (int64_t)blockIdx.x * run, last = min(first + run, total);
+  if (first < last && incl - mine <= first && first < incl) {
+    int64_t at = incl - mine;
+    for (int b = rb0; b < rb1; ++b) {
+      bool bad;
+      const Request r = request(p, b, bad);
+      const int blocks = (r.n * p.G + kRows - 1) / kRows;
+      const int64_t c = (int64_t)r.tiles * blocks * p.hk;
+      if (first < at + c) {
+        s_b0 = b;
+        s_off = first - at;
+        break;
+      }
+      at += c;
+    }
+  }
+
+  // ---- rows that see no key ------------------------------------------------
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    bool bad;
+    const Request r = request(p, b, bad);
+    if (r.n == 0 || r.tiles > 0) continue;
+    const int64_t rows = (int64_t)r.n * p.hq;
+    for (int64_t i = tid; i < rows * (D / 8); i += kThreads)
+      reinterpret_cast<uint4*>(p.out)[(int64_t)r.q0 * p.hq * (D / 8) + i] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int64_t i = tid; i < rows; i += kThreads)
+        p.lse[(int64_t)r.q0 * p.hq + i] = __int_as_float(0xFF800000);
+  }
+  __syncthreads();
+  if (first >= last) return;
+
+  int b = s_b0;
+  int64_t off = s_off;  // tiles of request b before this CTA's next one
+  int64_t pos = first;
+  while (pos < last) {
+    bool bad;
+    Request r = request(p, b, bad);
+    const int blocks = (r.n * p.G + kRows - 1) / kRows;
+    if (off >= (int64_t)r.tiles * blocks * p.hk) {
+      off -= (int64_t)r.tiles * blocks * p.hk;
+      ++b;
+      continue;
+    }
+    // the item: KV head h, row block rb of request b; tiles [t0, t1) of it
+    const int item = (int)(off / r.tiles), t0 = (int)(off - (int64_t)item * r.tiles);
+    const int t1 = (int)min((int64_t)r.tiles, t0 + (last - pos));
+    const int h = item / blocks, row0 = (item - h * blocks) * kRows;
+    const int nrows = min(kRows, r.n * p.G - row0);
+    const int32_t* table = p.table + (int64_t)b * p.cols;
+
+    // ---- loads: tile j of the item is this warp's when j = t0 + warp mod 4 --
+    auto issue = [&](int j, int slot) {
+      if (j < t1) {
+        const int tok = r.lo16 + j * 16;
+        int pg, of;
+        if (p.page_shift >= 0) {
+          pg = tok >> p.page_shift;
+          of = tok & (p.P - 1);
+        } else {
+          pg = (int)fastdiv((uint32_t)tok, p.by_page);
+          of = tok - pg * p.P;
+        }
+        int64_t page = table[pg];
+        if (page < 0 || page >= p.pages) {
+          page = 0;
+          if (lane == 0) flag(p.status, kDevBadIndex);
+        }
+        const int64_t row = (page * p.hk + h) * p.P + of;
+        Stage<D>& s = stages[slot];
+        constexpr int CPR = D / 32;  // 16-byte chunks of a code row
+#pragma unroll
+        for (int c = lane; c < 16 * CPR; c += 32) {
+          const int tk = c / CPR, part = c % CPR;
+          // K row index of the token (the inverse of token = 4 (r & 1) + r / 2 + 8 (r / 8))
+          const int kr = 2 * (tk & 3) + ((tk >> 2) & 1) + 8 * (tk >> 3);
+          cp_async16(s.k + kr * (D / 2) + part * 16, p.kc + row * (D / 2) + c * 16);
+          // V chunks swapped so that lanes (g, t) read 4 tokens without bank conflicts
+          const int vp = D == 128 ? part ^ (((tk >> 1) & 1) << 1) : part;
+          cp_async16(s.v + tk * (D / 2) + vp * 16, p.vc + row * (D / 2) + c * 16);
+        }
+        if (lane < D / 16) {
+          cp_async16(s.ks + lane * 16, p.ks + row * (D / 16) + lane * 16);
+        } else if (lane < D / 8) {
+          const int c = lane - D / 16;
+          cp_async16(s.vs + c * 16, p.vs + row * (D / 16) + c * 16);
+        }
+      }
+      cp_async_commit();
+    };
+    int slot = 0;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(t0 + warp + i * kWarps, i);
+
+    // ---- query rows ---------------------------------------------------------
+    // column n of row tile nt is row row0 + 8 nt + n = (token, head of the group)
+    uint32_t qb[NT][KS][2];
+    float fac[NT][2];     // scores to powers of two, for columns 2t and 2t + 1
+    int lim[NT][2];       // keys below this are seen
+    const SliceScale kss = slice_scale(p.k_amax[h], p.M);
+    const SliceScale vss = slice_scale(p.v_amax[h], p.M);
+    if ((kss.bad || vss.bad) && tid == 0) flag(p.status, NVFP4_DEV_BAD_AMAX_BIT);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = nt * 8 + g;
+      uint4 raw[DQ / 8];
+      if (row < nrows) {
+        const int tk = (row0 + row) / p.G, hh = (row0 + row) - tk * p.G;
+        const uint16_t* src = p.q + (r.q0 + tk) * p.q_st + (int64_t)(h * p.G + hh) * D + t * DQ;
+#pragma unroll
+        for (int i = 0; i < DQ / 8; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < DQ / 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < DQ / 8; ++i) m = max(m, absmax_bits4(raw[i]));
+      m = max(m, __shfl_xor_sync(kAll, m, 1));
+      m = max(m, __shfl_xor_sync(kAll, m, 2));
+      if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
+      // 2^(13 - e) for a row whose largest element lies in [2^e, 2^(e+1))
+      const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      const float f = p.scale * kLog2e * kss.g * __uint_as_float((uint32_t)(127 - e) << 23);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          qb[nt][j][i] = pack_f16x2(bf16_lo(w[2 * j + i]) * up, bf16_hi(w[2 * j + i]) * up);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fac[nt][i] = __shfl_sync(kAll, f, (2 * t + i) * 4);
+        const int rr = nt * 8 + 2 * t + i;
+        lim[nt][i] = rr < nrows ? r.len - r.n + (row0 + rr) / p.G + 1 : 0;
+      }
+    }
+    const int lim_min = r.len - r.n + row0 / p.G + 1;       // keys below are seen by every row
+    const int low_max = p.window > 0                        // and from here on
+                            ? r.len - r.n + (row0 + nrows - 1) / p.G + 1 - min(p.window, r.len)
+                            : 0;
+    float o[NT][KS][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[nt][i] = __int_as_float(0xFF800000), l[nt][i] = 0.0f;
+    }
+
+    // ---- tiles --------------------------------------------------------------
+    for (int j = t0 + warp; j < t1; j += kWarps) {
+      issue(j + (kStages - 1) * kWarps, (slot + kStages - 1) % kStages);
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      const Stage<D>& s = stages[slot];
+      const int tok = r.lo16 + j * 16;
+      const bool edge = tok + 16 > lim_min || tok < low_max;
+
+      // scores: S^T[token][row]
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[nt][c] = 0.0f;
+      const int tg = (g >> 1) + 4 * (g & 1);  // token of K row g; row g + 8: token tg + 8
+      {
+        uint32_t ka[DQ / 8], kb[DQ / 8];
+        const uint8_t* k0 = s.k + g * (D / 2) + t * (DQ / 2);
+#pragma unroll
+        for (int i = 0; i < DQ / 8; ++i) {
+          ka[i] = reinterpret_cast<const uint32_t*>(k0)[i];
+          kb[i] = reinterpret_cast<const uint32_t*>(k0 + 8 * (D / 2))[i];
+        }
+        uint32_t sa, sb;  // block scales of the two rows as f16x2 (D = 128: two blocks)
+        if constexpr (D == 128) {
+          sa = scales2(reinterpret_cast<const uint16_t*>(s.ks)[tg * 4 + t]);
+          sb = scales2(reinterpret_cast<const uint16_t*>(s.ks)[(tg + 8) * 4 + t]);
+        } else {
+          sa = scales2(s.ks[tg * 4 + t]);
+          sb = scales2(s.ks[(tg + 8) * 4 + t]);
+        }
+#pragma unroll
+        for (int i = 0; i < DQ / 8; ++i) {
+          const uint32_t fa = __byte_perm(sa, 0, (D == 128 && i >= 2) ? 0x3232 : 0x1010);
+          const uint32_t fb = __byte_perm(sb, 0, (D == 128 && i >= 2) ? 0x3232 : 0x1010);
+          uint32_t ha[4], hb[4];
+          codes8(ka[i], ha);
+          codes8(kb[i], hb);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ha[c] = h2mul(ha[c], fa), hb[c] = h2mul(hb[c], fb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(sc[nt], ha[0], hb[0], ha[1], hb[1], qb[nt][2 * i][0], qb[nt][2 * i][1]);
+            mma(sc[nt], ha[2], hb[2], ha[3], hb[3], qb[nt][2 * i + 1][0], qb[nt][2 * i + 1][1]);
+          }
+        }
+      }
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x = sc[nt][c] * fac[nt][c & 1];
+          if (edge) {
+            const int key = tok + tg + 8 * (c >> 1), hi = lim[nt][c & 1];
+            const bool seen = key < hi && (p.window == 0 || key >= hi - min(p.window, r.len));
+            x = seen ? x : __int_as_float(0xFF800000);
+          }
+          sc[nt][c] = x;
+          raise |= x > m[nt][c & 1] + kSlack;
+        }
+      if (__any_sync(kAll, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = fmaxf(sc[nt][i], sc[nt][i + 2]);
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+            const float mn = fmaxf(m[nt][i], x);
+            // 0 for a row that has seen nothing yet (its sums are 0)
+            const float a = m[nt][i] == __int_as_float(0xFF800000) ? 0.0f : ex2(m[nt][i] - mn);
+            m[nt][i] = mn;
+            l[nt][i] *= a;
+#pragma unroll
+            for (int d = 0; d < KS; ++d) o[nt][d][i] *= a, o[nt][d][i + 2] *= a;
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float mm = m[nt][c & 1];
+          e[c] = ex2(sc[nt][c] - (mm == __int_as_float(0xFF800000) ? 0.0f : mm - kBias));
+          l[nt][c & 1] += e[c];
+        }
+        pb[nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+        pb[nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
+      }
+      // K row 2t is token t, row 2t + 1 token 4 + t, rows + 8 tokens + 8
+      {
+        constexpr int VW = D / 64;  // words of a lane's V chunk
+        uint32_t vw[4][VW], vb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tk = 4 * i + t;
+          if constexpr (D == 128) {
+            const int chunk = (g >> 1) ^ (((tk >> 1) & 1) << 1);
+            const uint2 w = *reinterpret_cast<const uint2*>(s.v + tk * 64 + chunk * 16 + (g & 1) * 8);
+            vw[i][0] = w.x, vw[i][VW - 1] = w.y;
+            vb[i] = s.vs[tk * 8 + g];
+          } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(s.v + tk * 32 + g * 4);
+            vb[i] = s.vs[tk * 4 + (g >> 1)];
+          }
+          // bytes past the request may hold anything, a NaN scale included
+          if (edge && tok + tk >= r.len) vb[i] = 0;
+        }
+        const uint32_t f01 = scales2(vb[0] | (vb[1] << 8)), f23 = scales2(vb[2] | (vb[3] << 8));
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t e01 = (vw[0][w] & 0x0F0F0F0Fu) | ((vw[1][w] << 4) & 0xF0F0F0F0u);
+          const uint32_t o01 = ((vw[0][w] >> 4) & 0x0F0F0F0Fu) | (vw[1][w] & 0xF0F0F0F0u);
+          const uint32_t e23 = (vw[2][w] & 0x0F0F0F0Fu) | ((vw[3][w] << 4) & 0xF0F0F0F0u);
+          const uint32_t o23 = ((vw[2][w] >> 4) & 0x0F0F0F0Fu) | (vw[3][w] & 0xF0F0F0F0u);
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          codes8(e01, a0);
+          codes8(o01, a1);
+          codes8(e23, a2);
+          codes8(o23, a3);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            a0[c] = h2mul(a0[c], f01), a1[c] = h2mul(a1[c], f01);
+            a2[c] = h2mul(a2[c], f23), a3[c] = h2mul(a3[c], f23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma(o[nt][4 * w + c], a0[c], a1[c], a2[c], a3[c], pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the slot before it is filled again
+      slot = (slot + 1) % kStages;
+    }
+    cp_async_wait<0>();
+
+    // ---- join the warps ------------------------------------------------------
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v = l[nt][i];
+        v += __shfl_xor_sync(kAll, v, 4);
+        v += __shfl_xor_sync(kAll, v, 8);
+        v += __shfl_xor_sync(kAll, v, 16);
+        if (g == 0) {
+          s_m[warp][nt * 8 + 2 * t + i] = m[nt][i];
+          s_l[warp][nt * 8 + 2 * t + i] = v;
+        }
+      }
+    __syncthreads();  // the sums are there, and every warp is done with its stages
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = nt * 8 + 2 * t + i;
+        float mx = s_m[0][rr];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][rr]);
+        const float a = m[nt][i] == __int_as_float(0xFF800000) ? 0.0f : ex2(m[nt][i] - mx);
+        float* dst = s_o + (warp * kRows + rr) * D;
+#pragma unroll
+        for (int c = 0; c < KS; ++c)
+          *reinterpret_cast<float2*>(dst + g * (D / 8) + 2 * c) =
+              make_float2(o[nt][c][i] * a, o[nt][c][i + 2] * a);
+      }
+    __syncthreads();
+    const int64_t item_first = pos - t0, item_last = item_first + r.tiles - 1;
+    const int64_t c0 = item_first / run, c1 = item_last / run;  // CTAs of the item
+    const bool whole = c0 == c1;
+    float* rec = p.part + ((int64_t)blockIdx.x * 2 + (blockIdx.x == c0 ? 1 : 0)) * kAttnRecord;
+    auto finish = [&](int rr, int d, float4 v, float mx, float sum) {
+      // the row's final result
+      const int tk = (row0 + rr) / p.G, hh = (row0 + rr) - tk * p.G;
+      const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + h * p.G + hh;
+      const float f = sum == 0.0f ? 0.0f : vss.g / sum;
+      reinterpret_cast<uint2*>(p.out)[orow * (D / 4) + d / 4] =
+          make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+      if (p.lse && d == 0)
+        p.lse[orow] = sum == 0.0f ? __int_as_float(0xFF800000) : (mx - kBias + log2f(sum)) * kLn2;
+    };
+    for (int i = tid; i < nrows * (D / 4); i += kThreads) {
+      const int rr = i / (D / 4), d = (i % (D / 4)) * 4;
+      float mx = s_m[0][rr];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][rr]);
+      float sum = 0.0f;
+      float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = s_m[w][rr];
+        sum += mw == __int_as_float(0xFF800000) ? 0.0f : s_l[w][rr] * ex2(mw - mx);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + rr) * D + d);
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      if (whole) {
+        finish(rr, d, v, mx, sum);
+      } else {
+        *reinterpret_cast<float4*>(rec + rr * D + d) = v;
+        if (d == 0) {
+          rec[kAttnRows * 128 + rr] = mx;
+          rec[kAttnRows * 129 + rr] = sum;
+        }
+      }
+    }
+
+    // ---- join the CTAs of a cut item ------------------------------------------
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_ticket = atomicAdd(p.tickets + c0, 1u);
+      __syncthreads();
+      if (s_ticket == (uint32_t)(c1 - c0)) {
+        __threadfence();
+        for (int i = tid; i < nrows * (D / 4); i += kThreads) {
+          const int rr = i / (D / 4), d = (i % (D / 4)) * 4;
+          float mx = __int_as_float(0xFF800000), sum = 0.0f;
+          float4 v = make_float4(0, 0, 0, 0);
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float* q = p.part + (c * 2 + (c == c0 ? 1 : 0)) * kAttnRecord;
+            const float mc = __ldcg(q + kAttnRows * 128 + rr), lc = __ldcg(q + kAttnRows * 129 + rr);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + rr * D + d));
+            if (mc == __int_as_float(0xFF800000)) continue;
+            const float mn = fmaxf(mx, mc);
+            const float a = ex2(mx - mn), e = ex2(mc - mn);
+            sum = sum * a + lc * e;
+            v.x = v.x * a + x.x * e, v.y = v.y * a + x.y * e;
+            v.z = v.z * a + x.z * e, v.w = v.w * a + x.w * e;
+            mx = mn;
+          }
+          finish(rr, d, v, mx, sum);
+        }
+        if (tid == 0) p.tickets[c0] = 0;
+      }
+    }
+    __syncthreads();  // the stages are free again
+    pos += t1 - t0;
+    off += t1 - t0;
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_t(const KvAttnParams& p, cudaStream_t st) {
+  constexpr size_t stages = sizeof(Stage<D>) * 5 * kWarps, join = (size_t)kWarps * 8 * NT * D * 4;
+  constexpr size_t smem = stages > join ? stages : join;
+  static_assert(smem + 1024 <= 48 * 1024, "fits the default shared memory limit");
+  static const int per_sm = resident_ctas(kv_attn_kernel<D, NT>, kThreads, smem);
+  const int ctas = std::min(sm_count() * per_sm, kAttnMaxCtas);
+  return launch_pdl_smem(kv_attn_kernel<D, NT>, dim3(ctas), dim3(kThreads), smem, st, p, ctas);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t st) {
+  const bool one = (int64_t)p.max_q * p.G <= 8;
+  if (D == 128) return one ? launch_t<128, 1>(p, st) : launch_t<128, 2>(p, st);
+  return one ? launch_t<64, 1>(p, st) : launch_t<64, 2>(p, st);
+}
+
+}  // namespace nvfp4
