@@ -15,13 +15,14 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import math
+import struct
 
 import torch
 
-from . import _check, _dev, _i32, _i64, _need, _stream, _vp, lib
+from . import _check, _i32, _i64, _vp, lib
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
-_BYTES = (torch.uint8, torch.int8)
+_I32 = (torch.int32, torch.uint32)
 
 
 class _Cache(C.Structure):
@@ -47,16 +48,33 @@ class _AttentionConfig(C.Structure):
                 ("window", _i32), ("scale", C.c_float)]
 
 
+# the same structs, packed into bytes: several times cheaper than filling a
+# ctypes structure field by field
+_CACHE, _QK, _ATTENTION = struct.Struct("@6Pq4i"), struct.Struct("@q5if4Pq"), struct.Struct(
+    "@3P3q3if")
+assert (_CACHE.size, _QK.size, _ATTENTION.size) == tuple(
+    map(C.sizeof, (_Cache, _QkConfig, _AttentionConfig)))
+
+_loaded = None
+
+
+def _lib() -> C.CDLL:
+    global _loaded
+    if _loaded is None:
+        _loaded = lib()
+    return _loaded
+
+
 def declare(L: C.CDLL) -> None:
     """Argument types of the library's entry points of this module."""
     size = C.c_size_t
     L.nvfp4_kv_plan.argtypes = [_vp, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _vp, _vp, _vp,
                                 _vp, _vp, _vp, _vp]
-    L.nvfp4_qk_norm_rope.argtypes = [C.POINTER(_QkConfig), _Rows, _Rows, _Rows, _Rows, _vp, _vp]
-    L.nvfp4_qk_norm_rope_bwd.argtypes = [C.POINTER(_QkConfig)] + [_Rows] * 6 + [
+    L.nvfp4_qk_norm_rope.argtypes = [_vp, _Rows, _Rows, _Rows, _Rows, _vp, _vp]
+    L.nvfp4_qk_norm_rope_bwd.argtypes = [_vp] + [_Rows] * 6 + [
         _vp, _vp, _vp, size, _vp, _vp]
-    L.nvfp4_kv_append.argtypes = [C.POINTER(_Cache), _Rows, _Rows, _vp, _i64, _vp, _vp, _vp, _vp]
-    L.nvfp4_kv_attention.argtypes = [C.POINTER(_Cache), C.POINTER(_AttentionConfig), _Rows, _vp,
+    L.nvfp4_kv_append.argtypes = [_vp, _Rows, _Rows, _vp, _i64, _vp, _vp, _vp, _vp]
+    L.nvfp4_kv_attention.argtypes = [_vp, _vp, _Rows, _vp,
                                      _vp, _vp, size, _vp, _vp]
     for name in ("nvfp4_kv_plan", "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_bwd",
                  "nvfp4_kv_append", "nvfp4_kv_attention"):
@@ -72,40 +90,76 @@ def _on_device(fn):
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         x = args[0] if not isinstance(args[0], dict) else args[0]["k_codes"]
-        if not x.is_cuda or x.device.index == torch.cuda.current_device():
+        dev = x.get_device()
+        if dev == _current_device() or dev < 0:
             return fn(*args, **kwargs)
-        with torch.cuda.device(x.device):
+        with torch.cuda.device(dev):
             return fn(*args, **kwargs)
     return wrapper
 
 
-def _rows(t: torch.Tensor, name: str, tokens: int, heads: int, dim: int) -> _Rows:
+def _current_device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+# A call here lasts a few microseconds on the GPU, so a tensor is checked by one
+# short expression and what is wrong with it is looked up only if that fails.
+
+def _refuse(t, name: str, shape, dtypes, dev: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        kind = "bf16" if dtypes is _BF16 else dtypes[0]
+        raise TypeError(f"{name} must hold {kind} data, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device} but the call runs on cuda:{dev}: every buffer "
+                         "of a call must be on one device")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _typed(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _refuse(t, name, shape, (dtype,), dev)
+
+
+def _optional(t: torch.Tensor | None, name: str, n: int, dtypes, dev: int) -> int:
+    """A buffer of at least n elements, or None."""
+    if t is None:
+        return 0
+    if t.dtype not in dtypes or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _refuse(t, name, None, dtypes, dev)
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements; the call needs {n}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, tokens: int, heads: int, dim: int,
+          dev: int | None = None) -> _Rows:
     """A [tokens, heads, dim] bf16 tensor whose heads are contiguous and whose
     tokens may be apart (a view of a packed projection)."""
-    if t.dtype not in _BF16:
-        raise TypeError(f"{name} must hold bf16 data, got {t.dtype}")
-    if t.shape != (tokens, heads, dim):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {list(t.shape)}")
+    dev = t.get_device() if dev is None else dev
+    if t.dtype not in _BF16 or t.shape != (tokens, heads, dim) or t.get_device() != dev or dev < 0:
+        st = t.stride()
+        if len(st) == 3 and t.shape == (tokens, heads, dim) and t.dtype in _BF16 and (
+                (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim)):
+            raise ValueError(f"{name}: the values of a token's heads must be contiguous")
+        _refuse(t, name, (tokens, heads, dim), _BF16, dev)
     if t.is_contiguous():
-        return _Rows(_dev(t, name), heads * dim)
+        return _Rows(t.data_ptr(), heads * dim)
     st = t.stride()
     if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
         raise ValueError(f"{name}: the values of a token's heads must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device} but the call runs on "
-                         f"cuda:{torch.cuda.current_device()}: every buffer of a call must "
-                         "be on one device")
     return _Rows(t.data_ptr(), st[0] if tokens > 1 else max(st[0], heads * dim))
-
-
-def _typed(t: torch.Tensor, name: str, shape, dtype) -> int:
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _dev(t, name)
 
 
 # ------------------------------------------------------------------- cache --
@@ -124,19 +178,21 @@ def alloc_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int,
     return c
 
 
-def _cache(c: dict) -> _Cache:
-    kc = c["k_codes"]
+def _cache(c: dict, dev: int) -> tuple[bytes, int, int]:
+    """The C struct of a cache, its KV heads and head_dim."""
+    kc, u8 = c["k_codes"], torch.uint8
     if kc.dim() != 4:
         raise ValueError("k_codes must be [pages, kv_heads, page_size, head_dim/2]")
     pages, heads, page, half = shape = kc.shape
     scales = (pages, heads, page, half // 8)
-    return _Cache(_typed(kc, "k_codes", shape, torch.uint8),
-                  _typed(c["k_scales"], "k_scales", scales, torch.uint8),
-                  _typed(c["v_codes"], "v_codes", shape, torch.uint8),
-                  _typed(c["v_scales"], "v_scales", scales, torch.uint8),
-                  _typed(c["k_amax"], "k_amax", (heads,), torch.float32),
-                  _typed(c["v_amax"], "v_amax", (heads,), torch.float32),
-                  pages, heads, page, 2 * half, int(c.get("four_over_six", 0)))
+    return _CACHE.pack(_typed(kc, "k_codes", shape, u8, dev),
+                       _typed(c["k_scales"], "k_scales", scales, u8, dev),
+                       _typed(c["v_codes"], "v_codes", shape, u8, dev),
+                       _typed(c["v_scales"], "v_scales", scales, u8, dev),
+                       _typed(c["k_amax"], "k_amax", (heads,), torch.float32, dev),
+                       _typed(c["v_amax"], "v_amax", (heads,), torch.float32, dev),
+                       pages, heads, page, 2 * half, int(c.get("four_over_six", 0))
+                       ), heads, 2 * half
 
 
 # ----------------------------------------------------------------- entries --
@@ -153,30 +209,32 @@ def nvfp4_kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor,
     B = cached.shape[0]
     if table.dim() != 2:
         raise ValueError("table must be [requests, columns]")
-    dev, i32 = cached.device, torch.int32
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    device, dev, i32 = cached.device, cached.get_device(), torch.int32
+    ins = (_typed(cached, "cached", (B,), i32, dev), _typed(new, "new", (B,), i32, dev), B,
+           _typed(table, "table", (B, table.shape[1]), i32, dev), table.shape[1], page_size,
+           _typed(free_pages, "free_pages", (free_pages.numel(),), i32, dev), free_pages.numel(),
+           tokens)
     if out is None:
-        if tokens < 0:
-            raise ValueError("tokens must not be negative")
-        out = {"seq_lens": torch.empty(B, dtype=i32, device=dev),
-               "q_start": torch.empty(B + 1, dtype=i32, device=dev),
-               "slots": torch.empty(tokens, dtype=torch.int64, device=dev),
-               "positions": torch.empty(tokens, dtype=i32, device=dev),
-               "pages_used": torch.empty(1, dtype=i32, device=dev)}
-    _need(status, "status", 1, "i32")
-    _check("nvfp4_kv_plan", lib().nvfp4_kv_plan(
-        _typed(cached, "cached", (B,), i32), _typed(new, "new", (B,), i32), B,
-        _typed(table, "table", (B, table.shape[1]), i32), table.shape[1], page_size,
-        _typed(free_pages, "free_pages", (free_pages.numel(),), i32), free_pages.numel(), tokens,
-        _typed(out["seq_lens"], "seq_lens", (B,), i32),
-        _typed(out["q_start"], "q_start", (B + 1,), i32),
-        _typed(out["slots"], "slots", (tokens,), torch.int64),
-        _typed(out["positions"], "positions", (tokens,), i32),
-        _typed(out["pages_used"], "pages_used", (1,), i32), _dev(status, "status"), _stream(dev)))
-    out["table"] = table
+        out = {"seq_lens": torch.empty(B, dtype=i32, device=device),
+               "q_start": torch.empty(B + 1, dtype=i32, device=device),
+               "slots": torch.empty(tokens, dtype=torch.int64, device=device),
+               "positions": torch.empty(tokens, dtype=i32, device=device),
+               "pages_used": torch.empty(1, dtype=i32, device=device), "table": table}
+    else:
+        out = dict(out, table=table)
+    _check("nvfp4_kv_plan", _lib().nvfp4_kv_plan(
+        *ins, _typed(out["seq_lens"], "seq_lens", (B,), i32, dev),
+        _typed(out["q_start"], "q_start", (B + 1,), i32, dev),
+        _typed(out["slots"], "slots", (tokens,), torch.int64, dev),
+        _typed(out["positions"], "positions", (tokens,), i32, dev),
+        _typed(out["pages_used"], "pages_used", (1,), i32, dev),
+        _optional(status, "status", 1, _I32, dev), _stream(dev)))
     return out
 
 
-def _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved) -> _QkConfig:
+def _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev) -> bytes:
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [tokens, heads, head_dim]")
     T, hq, D = q.shape
@@ -184,14 +242,15 @@ def _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved) -> _QkCo
         raise ValueError("cos_sin must be [positions, rotary_dim]")
     if cos_sin.dtype is not torch.float32:
         raise TypeError(f"cos_sin must be torch.float32, got {cos_sin.dtype}")
+    length, rotary = cos_sin.shape
     for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None and (w.dtype not in _BF16 or w.shape != (D,)):
             raise ValueError(f"{n} must be bf16 [{D}]")
-    return _QkConfig(T, hq, k.shape[1], D, cos_sin.shape[1], int(interleaved), eps,
-                     _dev(q_weight, "q_weight"), _dev(k_weight, "k_weight"),
-                     _typed(positions, "positions", (T,), torch.int32),
-                     _typed(cos_sin, "cos_sin", tuple(cos_sin.shape), torch.float32),
-                     cos_sin.shape[0])
+    return _QK.pack(T, hq, k.shape[1], D, rotary, int(interleaved), eps,
+                    _optional(q_weight, "q_weight", D, _BF16, dev),
+                    _optional(k_weight, "k_weight", D, _BF16, dev),
+                    _typed(positions, "positions", (T,), torch.int32, dev),
+                    _typed(cos_sin, "cos_sin", (length, rotary), torch.float32, dev), length)
 
 
 @_on_device
@@ -205,18 +264,17 @@ def nvfp4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor
     [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim] (bf16; tokens
     may be apart) in one launch. cos_sin: fp32 [positions, rotary_dim], cosines
     then sines. Returns {"q", "k"}; q_out, k_out may be q and k themselves."""
-    cfg = _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved)
-    T, hq, D = q.shape
-    hk = k.shape[1]
+    dev = q.get_device()
+    cfg = _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev)
+    (T, hq, D), hk = q.shape, k.shape[1]
+    rq, rk = _rows(q, "q", T, hq, D, dev), _rows(k, "k", T, hk, D, dev)
     if q_out is None:
         q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
     if k_out is None:
         k_out = torch.empty((T, hk, D), dtype=k.dtype, device=q.device)
-    _need(status, "status", 1, "i32")
-    _check("nvfp4_qk_norm_rope", lib().nvfp4_qk_norm_rope(
-        C.byref(cfg), _rows(q, "q", T, hq, D), _rows(k, "k", T, hk, D),
-        _rows(q_out, "q_out", T, hq, D), _rows(k_out, "k_out", T, hk, D),
-        _dev(status, "status"), _stream(q.device)))
+    _check("nvfp4_qk_norm_rope", _lib().nvfp4_qk_norm_rope(
+        cfg, rq, rk, _rows(q_out, "q_out", T, hq, D, dev), _rows(k_out, "k_out", T, hk, D, dev),
+        _optional(status, "status", 1, _I32, dev), _stream(dev)))
     return {"q": q_out, "k": k_out}
 
 
@@ -227,7 +285,7 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
 def qk_norm_rope_workspace(device) -> torch.Tensor:
     """A zeroed workspace for nvfp4_qk_norm_rope_bwd, for calls of any size: it
     serves one call at a time and is allocated and cleared once."""
-    return _workspace(lib().nvfp4_qk_norm_rope_ws_bytes(), device)
+    return _workspace(_lib().nvfp4_qk_norm_rope_ws_bytes(), device)
 
 
 @_on_device
@@ -242,25 +300,26 @@ def nvfp4_qk_norm_rope_bwd(gq_out: torch.Tensor, gk_out: torch.Tensor, q: torch.
     inputs: {"gq", "gk", "gq_weight", "gk_weight"} (weight gradients fp32, None
     without the weight). workspace: from qk_norm_rope_workspace; a fresh one is
     cleared for the call when none is given."""
-    cfg = _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved)
-    T, hq, D = q.shape
-    hk, dev = k.shape[1], q.device
+    dev, device = q.get_device(), q.device
+    cfg = _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev)
+    (T, hq, D), hk = q.shape, k.shape[1]
+    ins = (_rows(gq_out, "gq_out", T, hq, D, dev), _rows(gk_out, "gk_out", T, hk, D, dev),
+           _rows(q, "q", T, hq, D, dev), _rows(k, "k", T, hk, D, dev))
     if gq is None:
-        gq = torch.empty((T, hq, D), dtype=q.dtype, device=dev)
+        gq = torch.empty((T, hq, D), dtype=q.dtype, device=device)
     if gk is None:
-        gk = torch.empty((T, hk, D), dtype=k.dtype, device=dev)
-    gqw = None if q_weight is None else torch.empty(D, dtype=torch.float32, device=dev)
-    gkw = None if k_weight is None else torch.empty(D, dtype=torch.float32, device=dev)
+        gk = torch.empty((T, hk, D), dtype=k.dtype, device=device)
+    f32 = torch.float32
+    gqw = None if q_weight is None else torch.empty(D, dtype=f32, device=device)
+    gkw = None if k_weight is None else torch.empty(D, dtype=f32, device=device)
     if workspace is None and (gqw is not None or gkw is not None):
-        workspace = qk_norm_rope_workspace(dev)
-    _need(workspace, "workspace", 1, "i32")
-    _need(status, "status", 1, "i32")
-    _check("nvfp4_qk_norm_rope_bwd", lib().nvfp4_qk_norm_rope_bwd(
-        C.byref(cfg), _rows(gq_out, "gq_out", T, hq, D), _rows(gk_out, "gk_out", T, hk, D),
-        _rows(q, "q", T, hq, D), _rows(k, "k", T, hk, D), _rows(gq, "gq", T, hq, D),
-        _rows(gk, "gk", T, hk, D), _dev(gqw, "gq_weight"), _dev(gkw, "gk_weight"),
-        _dev(workspace, "workspace"), 0 if workspace is None else workspace.numel() * 4,
-        _dev(status, "status"), _stream(dev)))
+        workspace = qk_norm_rope_workspace(device)
+    _check("nvfp4_qk_norm_rope_bwd", _lib().nvfp4_qk_norm_rope_bwd(
+        cfg, *ins, _rows(gq, "gq", T, hq, D, dev), _rows(gk, "gk", T, hk, D, dev),
+        0 if gqw is None else gqw.data_ptr(), 0 if gkw is None else gkw.data_ptr(),
+        _optional(workspace, "workspace", 1, _I32, dev),
+        0 if workspace is None else 4 * workspace.numel(),
+        _optional(status, "status", 1, _I32, dev), _stream(dev)))
     return {"gq": gq, "gk": gk, "gq_weight": gqw, "gk_weight": gkw}
 
 
@@ -270,24 +329,25 @@ def nvfp4_kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, slots: torch.
     """Quantise K and V rows (bf16 [tokens, kv_heads, head_dim]; tokens may be
     apart) into the cache's slots (int64 [tokens], -1 = skip). Returns {"k",
     "v"}: with dequant the values the codes stand for (bf16), else None."""
-    c = _cache(cache)
-    T, hk, D = k.shape[0], c.kv_heads, c.head_dim
+    dev = cache["k_codes"].get_device()
+    c, hk, D = _cache(cache, dev)
+    T = k.shape[0]
+    rk, rv = _rows(k, "k", T, hk, D, dev), _rows(v, "v", T, hk, D, dev)
+    at = _typed(slots, "slots", (T,), torch.int64, dev)
     kd = vd = None
     if dequant:
         kd = torch.empty((T, hk, D), dtype=torch.bfloat16, device=k.device)
         vd = torch.empty((T, hk, D), dtype=torch.bfloat16, device=k.device)
-    _need(status, "status", 1, "i32")
-    _check("nvfp4_kv_append", lib().nvfp4_kv_append(
-        C.byref(c), _rows(k, "k", T, hk, D), _rows(v, "v", T, hk, D),
-        _typed(slots, "slots", (T,), torch.int64), T, _dev(kd, "k dequant"),
-        _dev(vd, "v dequant"), _dev(status, "status"), _stream(k.device)))
+    _check("nvfp4_kv_append", _lib().nvfp4_kv_append(
+        c, rk, rv, at, T, kd.data_ptr() if dequant else 0, vd.data_ptr() if dequant else 0,
+        _optional(status, "status", 1, _I32, dev), _stream(dev)))
     return {"k": kd, "v": vd}
 
 
 def kv_attention_workspace(device) -> torch.Tensor:
     """A zeroed workspace for nvfp4_kv_attention, for calls of any size: it
     serves one call at a time and is allocated and cleared once."""
-    return _workspace(lib().nvfp4_kv_attention_ws_bytes(), device)
+    return _workspace(_lib().nvfp4_kv_attention_ws_bytes(), device)
 
 
 @_on_device
@@ -302,33 +362,32 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: dict, table: torch.Tensor, seq_le
     bound of the requests' query rows. scale defaults to head_dim ** -0.5.
     workspace: from kv_attention_workspace; a fresh one is cleared for the call
     when none is given. Returns {"out", "lse"}."""
-    c = _cache(cache)
+    dev, device, i32 = q.get_device(), q.device, torch.int32
     if q.dim() != 3 or table.dim() != 2:
         raise ValueError("q must be [tokens, q_heads, head_dim], table [requests, columns]")
+    c, _, dim = _cache(cache, dev)
     T, hq, D = q.shape
-    B, dev, i32 = seq_lens.shape[0], q.device, torch.int32
-    if D != c.head_dim:
-        raise ValueError(f"q has head_dim {D}, the cache {c.head_dim}")
-    if out is None:
-        out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=dev)
-    else:
-        _need(out, "out", T * hq * D, "bf16")
-    if lse is None:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", T * hq, "f32")
-    if workspace is None:
-        workspace = kv_attention_workspace(dev)
-    _need(workspace, "workspace", 1, "i32")
-    _need(status, "status", 1, "i32")
-    cfg = _AttentionConfig(_typed(table, "table", (B, table.shape[1]), i32),
-                           _typed(seq_lens, "seq_lens", (B,), i32),
-                           _typed(q_start, "q_start", (B + 1,), i32), B, table.shape[1], T, hq,
-                           max_q, window, D ** -0.5 if scale is None else scale)
-    if not math.isfinite(cfg.scale):
+    if D != dim:
+        raise ValueError(f"q has head_dim {D}, the cache {dim}")
+    if scale is None:
+        scale = D ** -0.5
+    elif not math.isfinite(scale):
         raise ValueError("scale must be finite")
-    _check("nvfp4_kv_attention", lib().nvfp4_kv_attention(
-        C.byref(c), C.byref(cfg), _rows(q, "q", T, hq, D), _dev(out, "out"), _dev(lse, "lse"),
-        _dev(workspace, "workspace"), workspace.numel() * 4, _dev(status, "status"),
-        _stream(dev)))
+    B, cols = seq_lens.shape[0], table.shape[1]
+    cfg = _ATTENTION.pack(_typed(table, "table", (B, cols), i32, dev),
+                          _typed(seq_lens, "seq_lens", (B,), i32, dev),
+                          _typed(q_start, "q_start", (B + 1,), i32, dev), B, cols, T, hq, max_q,
+                          window, scale)
+    rq = _rows(q, "q", T, hq, D, dev)
+    if out is None:
+        out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((T, hq), dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = kv_attention_workspace(device)
+    _check("nvfp4_kv_attention", _lib().nvfp4_kv_attention(
+        c, cfg, rq, _optional(out, "out", T * hq * D, _BF16, dev),
+        _optional(lse, "lse", T * hq, (torch.float32,), dev),
+        _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel(),
+        _optional(status, "status", 1, _I32, dev), _stream(dev)))
     return {"out": out, "lse": lse}
