@@ -67,6 +67,8 @@ typedef enum {
                                     /* out of range (nothing is read or        */
                                     /* written there)                          */
 #define NVFP4_DEV_NO_PAGES 16       /* fewer free pages than the requests need */
+#define NVFP4_DEV_TIMEOUT 32        /* a wait inside a kernel ran out (a fault */
+                                    /* of the library or the device)           */
 
 /* nvfp4_config.blocks */
 #define NVFP4_BLOCKS_ROW 1  /* 1x16 blocks along the last dimension            */

@@ -30,6 +30,7 @@ __all__ = [
     "BLOCKS_TILE16",
     "SCALE_E4M3", "SCALE_UE5M3", "ROUND_RNE", "ROUND_SR", "FOS_MSE", "FOS_MAE", "FOS_MAX",
     "DEV_NONFINITE_INPUT", "DEV_BAD_SCALE", "DEV_BAD_AMAX", "DEV_BAD_INDEX", "DEV_NO_PAGES",
+    "DEV_TIMEOUT",
     "alloc_kv_cache", "kv_attention_workspace", "nvfp4_kv_append", "nvfp4_kv_attention",
     "nvfp4_kv_plan", "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_bwd", "qk_norm_rope_workspace",
 ]
@@ -42,7 +43,7 @@ FOS_MSE, FOS_MAE, FOS_MAX = 0, 1, 2
 SCALE_E4M3, SCALE_UE5M3 = 0, 1
 ROUND_RNE, ROUND_SR = 0, 1
 DEV_NONFINITE_INPUT, DEV_BAD_SCALE, DEV_BAD_AMAX = 1, 2, 4
-DEV_BAD_INDEX, DEV_NO_PAGES = 8, 16
+DEV_BAD_INDEX, DEV_NO_PAGES, DEV_TIMEOUT = 8, 16, 32
 TARGET_MXFP8, TARGET_NVFP4 = 0, 1
 
 _STATUS = {0: "ok", 1: "null pointer", 2: "shape", 3: "alignment", 4: "enum", 6: "cuda"}

@@ -284,10 +284,17 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_attenti
   p.lse = lse;
   p.tickets = static_cast<uint32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                    (size_t)nvfp4::kAttnMaxCtas * 4);
+                                    (size_t)nvfp4::kAttnTickets * 4);
   p.status = status;
-  return cuda_status(
-      nvfp4::launch_kv_attention(p, cache->head_dim, static_cast<cudaStream_t>(stream)));
+  // The requests share the call, their row counts are on the device: each kernel
+  // takes the requests that are its own, and the one for many rows is launched
+  // only if max_q allows such a request.
+  p.few_rows = nvfp4::kAttnRows;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t ce = nvfp4::launch_kv_few(p, cache->head_dim, st);
+  if (ce == cudaSuccess && cfg->max_q * group > p.few_rows)
+    ce = nvfp4::launch_kv_prefill(p, cache->head_dim, st);
+  return cuda_status(ce);
 }
 
 }  // extern "C"

@@ -8,6 +8,7 @@ namespace nvfp4 {
 
 constexpr int kDevBadIndex = NVFP4_DEV_BAD_INDEX;
 constexpr int kDevNoPages = NVFP4_DEV_NO_PAGES;
+constexpr int kDevTimeout = NVFP4_DEV_TIMEOUT;
 
 // launch_pdl with dynamic shared memory.
 template <class... KArgs, class... Args>
@@ -103,15 +104,22 @@ struct KvAttnParams {
   int64_t q_st;
   uint16_t* out;
   float* lse;
-  uint32_t* tickets;       // [kAttnMaxCtas], zero between calls
+  int32_t few_rows;        // requests with at most so many rows per KV head go to kv_attn.cu
+  uint32_t* tickets;       // [kAttnTickets], zero between calls
   float* part;             // partial results, two records per CTA
   int32_t* status;
 };
 constexpr int kAttnMaxCtas = 1024;
-constexpr int kAttnRows = 16;                           // query rows of a record at most
+constexpr int kAttnRows = 16;                           // query rows of an item at most
 constexpr int kAttnRecord = kAttnRows * (128 + 2);      // floats: rows x (out, max, sum)
-constexpr size_t kAttnWsBytes =
-    (size_t)kAttnMaxCtas * 4 + (size_t)kAttnMaxCtas * 2 * kAttnRecord * 4;
-cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t st);
+constexpr int kPrefillMaxCtas = 192;
+constexpr int kPrefillRecord = 256 * (128 + 2);
+constexpr int kAttnTickets = kAttnMaxCtas + 8 * kPrefillMaxCtas;
+// the two kernels of a call run one after the other: they share the records
+constexpr size_t kAttnPartBytes =
+    (size_t)4 * std::max(2 * kAttnMaxCtas * kAttnRecord, 2 * kPrefillMaxCtas * kPrefillRecord);
+constexpr size_t kAttnWsBytes = (size_t)4 * kAttnTickets + kAttnPartBytes;
+cudaError_t launch_kv_few(const KvAttnParams& p, int D, cudaStream_t st);
+cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, cudaStream_t st);
 
 }  // namespace nvfp4

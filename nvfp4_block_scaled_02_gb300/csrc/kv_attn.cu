@@ -37,7 +37,7 @@
 // 8x8 transpose between lanes. Two V bytes of neighbouring tokens are merged
 // to (even nibbles) and (odd nibbles) before conversion, so that a converted
 // pair holds one dimension of two tokens, as the operand wants.
-#include "kv.h"
+#include "kv_attn.cuh"
 
 namespace nvfp4 {
 
@@ -45,75 +45,10 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kBias = 6;
-constexpr float kSlack = 8.0f;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Two E4M3 scale bytes (low 16 bits) -> f16x2, exact.
-__device__ __forceinline__ uint32_t scales2(uint32_t b) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
-      : "=r"(r) : "r"(b));
-  return r;
-}
-// 8 codes of a word -> 4 f16x2 (byte i: low nibble in the low half).
-__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// A request's rows and keys. rows = query tokens; keys [lo, hi) are seen by
-// some row, lo rounded down to a tile.
-struct Request {
-  int q0, n, len, lo16, tiles;
-};
-__device__ __forceinline__ Request request(const KvAttnParams& p, int b, bool& bad) {
-  Request r;
-  r.q0 = p.q_start[b];
-  const int q1 = p.q_start[b + 1];
-  r.len = p.seq_len[b];
-  r.n = q1 - r.q0;
-  bad = r.q0 < 0 || q1 < r.q0 || q1 > p.T || r.n > p.max_q || r.len < 0 ||
-        r.len > INT32_MAX - 16 || (int64_t)r.len > (int64_t)p.cols * p.P;
-  if (bad) r.q0 = r.n = r.len = 0;
-  int lo = 0;
-  if (p.window > 0) lo = max(0, r.len - r.n + 1 - min(p.window, r.len));
-  r.lo16 = lo & ~15;
-  r.tiles = r.n > 0 ? (r.len - r.lo16 + 15) >> 4 : 0;
+// A request this kernel takes.
+__device__ __forceinline__ Request few_rows(const KvAttnParams& p, int b, bool& bad) {
+  Request r = request(p, b, bad);
+  if ((int64_t)r.n * p.G > p.few_rows) r.n = r.tiles = 0;
   return r;
 }
 
@@ -147,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   int64_t mine = 0;
   for (int b = rb0; b < rb1; ++b) {
     bool bad;
-    const Request r = request(p, b, bad);
+    const Request r = few_rows(p, b, bad);
     if (bad && blockIdx.x == 0) flag(p.status, kDevBadIndex);
     const int blocks = (r.n * p.G + kRows - 1) / kRows;
     mine += (int64_t)r.tiles * blocks * p.hk;
@@ -173,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     int64_t at = incl - mine;
     for (int b = rb0; b < rb1; ++b) {
       bool bad;
-      const Request r = request(p, b, bad);
+      const Request r = few_rows(p, b, bad);
       const int blocks = (r.n * p.G + kRows - 1) / kRows;
       const int64_t c = (int64_t)r.tiles * blocks * p.hk;
       if (first < at + c) {
@@ -188,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   // ---- rows that see no key ------------------------------------------------
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     bool bad;
-    const Request r = request(p, b, bad);
+    const Request r = few_rows(p, b, bad);
     if (r.n == 0 || r.tiles > 0) continue;
     const int64_t rows = (int64_t)r.n * p.hq;
     for (int64_t i = tid; i < rows * (D / 8); i += kThreads)
@@ -205,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   int64_t pos = first;
   while (pos < last) {
     bool bad;
-    Request r = request(p, b, bad);
+    Request r = few_rows(p, b, bad);
     const int blocks = (r.n * p.G + kRows - 1) / kRows;
     if (off >= (int64_t)r.tiles * blocks * p.hk) {
       off -= (int64_t)r.tiles * blocks * p.hk;
@@ -578,7 +513,7 @@ cudaError_t launch_t(const KvAttnParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_kv_attention(const KvAttnParams& p, int D, cudaStream_t st) {
+cudaError_t launch_kv_few(const KvAttnParams& p, int D, cudaStream_t st) {
   const bool one = (int64_t)p.max_q * p.G <= 8;
   if (D == 128) return one ? launch_t<128, 1>(p, st) : launch_t<128, 2>(p, st);
   return one ? launch_t<64, 1>(p, st) : launch_t<64, 2>(p, st);
