@@ -10,7 +10,9 @@
 // Tensor memory: S0 S1 (128 columns each), O0 O1 (D each): 512 columns at D = 128.
 //
 // Warps: 0-3 softmax of tile 0 (thread = row), 4-7 of tile 1, 8-11 dequantise K
-// and V tiles into shared memory, 12 issues the MMAs. While one tile's softmax
+// and V tiles into shared memory, 12 issues the MMAs, 13 hands out
+// the items (14 and 15 only fill up their warpgroup, whose registers go to the
+// softmax). While one tile's softmax
 // runs, the other tile's products do. K and V tiles are double-buffered. All
 // hand-overs are mbarriers; QK of the next tile is issued right behind PV of the
 // previous one, so the barrier that says "S is ready" also says that the output
@@ -33,15 +35,21 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kThreads = 416;  // 13 warps
+constexpr int kThreads = 512;  // 4 warpgroups
+// Registers per thread: the softmax keeps a whole row of scores. Two softmax
+// warpgroups, one that dequantises, one that issues: 2 x 184 + 80 + 64 = 4 x 128.
+constexpr int kRegsSoftmax = 184, kRegsDequant = 80, kRegsMma = 64;
+static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsMma <= 4 * 128, "the block's registers");
 constexpr int kTileN = 128;    // keys per tile
 constexpr int kRowsTile = 128, kRowsItem = 256;
+constexpr int kItems = 4;      // items handed out ahead
 constexpr long long kWaitCycles = 2000000000;  // about a second
 constexpr uint32_t kNegInf = 0xFF800000u;
 
 struct Bars {
   uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+  uint64_t item_full[kItems], item_free[kItems];
   uint64_t end;
 };
 
@@ -155,9 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   __shared__ Bars bar;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_dead;
-  __shared__ int64_t s_scan[13];
+  __shared__ int64_t s_scan[kThreads / 32];
   __shared__ int s_b0;
   __shared__ int64_t s_off;
+  __shared__ Item s_item[kItems];
   constexpr int kTile = Smem<D>::kTile;
   uint8_t* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   uint8_t* sq = base;               // [2] Q tiles
@@ -195,12 +204,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       mbar_init(&bar.k_free[i], 1);
       mbar_init(&bar.v_free[i], 1);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_free[i], 13);  // the softmax, dequantising and issuing warps
+    }
     mbar_init(&bar.end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   int64_t total = 0;
-  for (int w = 0; w < 13; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) incl += s_scan[w];
     total += s_scan[w];
   }
@@ -260,32 +273,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     return __all_sync(kAll, wait(b, parity));
   };
 
-  Walk walk;
-  walk.start(p, first, last, s_b0, s_off);
-  Item it;
+  // The item a warp is at: handed out by warp 13, one after the other, by way of
+  // a ring; t1 = 0 ends the run.
+  uint32_t items = 0;
+  auto next = [&](const Item*& it) -> bool {
+    if (items > 0) {
+      __syncwarp();  // every lane is done with the last item
+      if (lane == 0) mbar_arrive(&bar.item_free[(items - 1) % kItems]);
+    }
+    if (!wait_warp(&bar.item_full[items % kItems], (items / kItems) & 1)) return false;
+    it = &s_item[items % kItems];
+    ++items;
+    return it->t1 > 0;
+  };
+  const Item* it;
 
   if (warp < 8) {
     // ==== softmax: thread = row of its tile ====================================
+    more_registers<kRegsSoftmax>();
     const int tile = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane offset in a TMEM address
     const uint32_t ts = t_s(tile) + lanes, to = t_o(tile) + lanes;
     uint32_t sphase = 0, ophase = 0;
     bool ok = true;
-    while (ok && walk.next(p, it)) {
-      if (tile * kRowsTile >= it.rows) continue;
-      const Request& r = it.r;
-      const int rr = it.row0 + tile * kRowsTile + row;  // row of the request
+    while (ok && next(it)) {
+      if (tile * kRowsTile >= it->rows) continue;
+      const Request r = it->r;
+      const int rr = it->row0 + tile * kRowsTile + row;  // row of the request
       const bool live = rr < r.n * p.G;
       const int tk = live ? rr / p.G : 0, hh = rr - tk * p.G;
-      const SliceScale kss = slice_scale(p.k_amax[it.h], p.M);
-      const SliceScale vss = slice_scale(p.v_amax[it.h], p.M);
+      const SliceScale kss = slice_scale(p.k_amax[it->h], p.M);
+      const SliceScale vss = slice_scale(p.v_amax[it->h], p.M);
       if ((kss.bad || vss.bad) && row == 0) flag(p.status, NVFP4_DEV_BAD_AMAX_BIT);
 
       // -- query row: scaled to f16, into the swizzled tile
       float f;
       {
         const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (int64_t)(r.q0 + tk) * p.q_st + (int64_t)(it.h * p.G + hh) * D);
+            p.q + (int64_t)(r.q0 + tk) * p.q_st + (int64_t)(it->h * p.G + hh) * D);
         uint4 raw[D / 8];
         uint32_t m = 0;
 #pragma unroll
@@ -296,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
         float up = __uint_as_float((uint32_t)(127 + e) << 23);
         f = p.scale * kLog2e * kss.g * __uint_as_float((uint32_t)(127 - e) << 23);
-        if (f < 0.0f) f = -f, up = -up;  // the running maximum needs f >= 0
+        if (f < 0.0f) f = -f, up = -up;  // the running maximum needs f > 0, and a masked
+        f = fmaxf(f, 1.17549435e-38f);   // score (-inf) must stay -inf times f
         uint8_t* dst = sq + tile * kTile + row * 128;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -311,77 +337,70 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       fence_smem_async();
       mbar_arrive(&bar.q_full[tile]);
 
+      // the row sees keys [low, low + span)
       const int lim = live ? r.len - r.n + tk + 1 : 0;
       const int low = p.window > 0 ? lim - min(p.window, r.len) : 0;
+      const uint32_t span = (uint32_t)max(lim - low, 0);
       // keys in [safe_lo, safe_hi) are seen by every live row of the tile
-      const int trow0 = it.row0 + tile * kRowsTile;
+      const int trow0 = it->row0 + tile * kRowsTile;
       const int trow1 = min(trow0 + kRowsTile, r.n * p.G) - 1;
       const int safe_hi = r.len - r.n + trow0 / p.G + 1;
       const int safe_lo = p.window > 0 ? r.len - r.n + trow1 / p.G + 1 - min(p.window, r.len) : 0;
       float m = __uint_as_float(kNegInf), l = 0.0f;
 
-      for (int j = it.t0; j < it.t1; ++j) {
+      const int t0 = it->t0, t1 = it->t1;
+      for (int j = t0; j < t1; ++j) {
         if (!(ok = wait_warp(&bar.s_full[tile], sphase))) break;
         sphase ^= 1;
         fence_after();
         const int key0 = r.lo16 + j * kTileN;
-        const bool edge = key0 + kTileN > safe_hi || key0 < safe_lo;
-        uint32_t s[32];
-        float mx = __uint_as_float(kNegInf);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(ts + 32 * c, s);
-          tmem_wait_ld();
-          if (edge) {
+        uint32_t s[4][32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int key = key0 + 32 * c + i;
-              if (key < lim && key >= low) mx = fmaxf(mx, __uint_as_float(s[i]));
-            }
-          } else {
-            float a = mx, b = mx;
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+        tmem_wait_ld();
+        if (key0 + kTileN > safe_hi || key0 < safe_lo) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              a = fmax3(a, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-              b = fmax3(b, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-            }
-            mx = fmaxf(a, b);
-          }
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((uint32_t)(key0 - low + 32 * c + i) >= span) s[c][i] = kNegInf;
         }
-        if (mx != __uint_as_float(kNegInf)) mx *= f;
+        float mx = __uint_as_float(kNegInf), mb = mx;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            mx = fmax3(mx, __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+            mb = fmax3(mb, __uint_as_float(s[c][i + 2]), __uint_as_float(s[c][i + 3]));
+          }
+        mx = fmaxf(mx, mb) * f;
         if (__any_sync(kAll, mx > m + kSlack)) {
           const float mn = fmaxf(m, mx);
           const float a = m == __uint_as_float(kNegInf) ? 0.0f : ex2(m - mn);
           m = mn;
           l *= a;
-          if (j > it.t0) {  // S is ready, so PV of the previous tile is done
+          if (j > t0) {  // S is ready, so PV of the previous tile is done
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              tmem_ld32(to + 32 * c, s);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * a);
-              tmem_st32(to + 32 * c, s);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st16(to + 16 * c, o);
             }
           }
         }
         const float sub = m == __uint_as_float(kNegInf) ? 0.0f : kBias - m;
         const f2 ff = make_float2(f, f), cc = make_float2(sub, sub);
         f2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          tmem_ld32(ts + 32 * c, s);
-          tmem_wait_ld();
           uint32_t h[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            f2 x = f2_fma(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff,
-                          cc);
-            if (edge) {
-              const int key = key0 + 32 * c + 2 * i;
-              if (!(key < lim && key >= low)) x.x = __uint_as_float(kNegInf);
-              if (!(key + 1 < lim && key + 1 >= low)) x.y = __uint_as_float(kNegInf);
-            }
+            f2 x = f2_fma(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])),
+                          ff, cc);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
             sum = __fadd2_rn(sum, x);
@@ -400,11 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       if (!(ok = wait_warp(&bar.o_done[tile], ophase))) break;
       ophase ^= 1;
       fence_after();
-      const int64_t c0 = it.first / run, c1 = (it.first + it.nt - 1) / run;
+      const int64_t c0 = it->first / run, c1 = (it->first + it->nt - 1) / run;
       uint32_t s[32];
       if (c0 == c1) {
         const float fo = l == 0.0f ? 0.0f : vss.g / l;
-        const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it.h * p.G + hh;
+        const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it->h * p.G + hh;
         uint4* dst = reinterpret_cast<uint4*>(p.out) + orow * (D / 8);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -457,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               sum += __ldcg(q + kRowsItem * 129 + ri) * ex2(mc - mx);
           }
           const float fo = sum == 0.0f ? 0.0f : vss.g / sum;
-          const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it.h * p.G + hh;
+          const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it->h * p.G + hh;
           uint2* dst = reinterpret_cast<uint2*>(p.out) + orow * (D / 4);
 #pragma unroll 4
           for (int d = 0; d < D / 4; ++d) {
@@ -482,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     }
   } else if (warp < 12) {
     // ==== dequantise ============================================================
+    fewer_registers<kRegsDequant>();
     // thread: rows 8 w + (lane & 7) + 32 i of a tile, 16-byte chunk lane / 8 of the
     // codes (D = 64: two row halves instead of four chunks)
     constexpr int kRowsPer = D == 128 ? 4 : 2;
@@ -491,16 +511,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     constexpr int kRowStep = D == 128 ? 32 : 64;
     uint32_t n = 0;  // tiles done
     bool ok = true;
-    while (ok && walk.next(p, it)) {
-      const int32_t* table = p.table + (int64_t)it.b * p.cols;
-      const int len = it.r.len;
+    while (ok && next(it)) {
+      const int32_t* table = p.table + (int64_t)it->b * p.cols;
+      const int len = it->r.len;
       uint4 ck[kRowsPer], cv[kRowsPer];
       uint32_t bk[kRowsPer], bv[kRowsPer];
       int64_t at[kRowsPer];  // cache row of this thread's rows, or -1
       auto locate = [&](int j) {
 #pragma unroll
         for (int i = 0; i < kRowsPer; ++i) {
-          const int tok = it.r.lo16 + j * kTileN + rbase + kRowStep * i;
+          const int tok = it->r.lo16 + j * kTileN + rbase + kRowStep * i;
           at[i] = -1;
           if (tok < len) {
             const int pg = p.page_shift >= 0 ? tok >> p.page_shift
@@ -510,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               page = 0;
               flag(p.status, kDevBadIndex);
             }
-            at[i] = (page * p.hk + it.h) * p.P + (tok - pg * p.P);
+            at[i] = (page * p.hk + it->h) * p.P + (tok - pg * p.P);
           }
         }
       };
@@ -544,102 +564,126 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           }
         }
       };
-      locate(it.t0);
+      locate(it->t0);
       load(p.kc, p.ks, ck, bk);
       load(p.vc, p.vs, cv, bv);
-      for (int j = it.t0; j < it.t1; ++j, ++n) {
+      for (int j = it->t0; j < it->t1; ++j, ++n) {
         const int st = n & 1;
         const uint32_t par = ((n >> 1) & 1) ^ 1;
-        if (j + 1 < it.t1) locate(j + 1);
+        if (j + 1 < it->t1) locate(j + 1);
         if (!(ok = wait_warp(&bar.k_free[st], par))) break;
         store(sk + st * kTile, ck, bk);
         fence_smem_async();
         mbar_arrive(&bar.k_full[st]);
-        if (j + 1 < it.t1) load(p.kc, p.ks, ck, bk);
+        if (j + 1 < it->t1) load(p.kc, p.ks, ck, bk);
         if (!(ok = wait_warp(&bar.v_free[st], par))) break;
         store(sv + st * kTile, cv, bv);
         fence_smem_async();
         mbar_arrive(&bar.v_full[st]);
-        if (j + 1 < it.t1) load(p.vc, p.vs, cv, bv);
+        if (j + 1 < it->t1) load(p.vc, p.vs, cv, bv);
       }
     }
   } else {
     // ==== MMAs: one thread =======================================================
-    if (lane == 0) {
+    fewer_registers<kRegsMma>();
+    if (warp == 12) {
       constexpr uint32_t kQK = mma_desc(128, false), kPV = mma_desc(D, true);
-      const uint64_t dq = smem_desc(smem_addr(sq), 0), dk = smem_desc(smem_addr(sk), 0);
-      const uint64_t dv = smem_desc(smem_addr(sv), 128 * 128);
+      const uint32_t dq = smem_addr(sq) >> 4, dk = smem_addr(sk) >> 4, dv = smem_addr(sv) >> 4;
       auto qk = [&](int tile, int st) {
+        uint32_t a = dq + (kTile >> 4) * tile, b = dk + (kTile >> 4) * st;
+        asm volatile("" : "+r"(a), "+r"(b));  // the steps' addresses are added here, not kept
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           // 16 values = 32 bytes along a row; 64 values per panel
-          const uint64_t o = (uint64_t)((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-          mma_ss(t_s(tile), dq + (kTile >> 4) * tile + o, dk + (kTile >> 4) * st + o, kQK, k > 0);
+          const uint32_t o = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+          mma_ss(t_s(tile), smem_desc(a + o, 0), smem_desc(b + o, 0), kQK, k > 0);
         }
         mma_commit(&bar.s_full[tile]);
       };
       auto pv = [&](int tile, int st, bool add) {
+        uint32_t b = dv + (kTile >> 4) * st, a = t_s(tile);
+        asm volatile("" : "+r"(a), "+r"(b));
 #pragma unroll
         for (int k = 0; k < kTileN / 16; ++k)  // 16 keys = two atoms of 8 rows
-          mma_ts(t_o(tile), t_s(tile) + 8 * k, dv + (kTile >> 4) * st + (2048 >> 4) * k, kPV,
+          mma_ts(t_o(tile), a + 8 * k, smem_desc(b + (2048 >> 4) * k, 128 * 128), kPV,
                  add || k > 0);
       };
       uint32_t n = 0;  // tiles done
       uint32_t qphase = 0, q1phase = 0, pphase = 0, p1phase = 0;
       bool ok = true;
-      while (ok && walk.next(p, it)) {
-        const bool two = it.rows > kRowsTile;
-        if (!(ok = wait(&bar.q_full[0], qphase))) break;
-        qphase ^= 1;
-        if (two) {
-          if (!(ok = wait(&bar.q_full[1], q1phase))) break;
-          q1phase ^= 1;
-        }
-        if (!(ok = wait(&bar.k_full[n & 1], (n >> 1) & 1))) break;
-        fence_after();
-        qk(0, n & 1);
-        if (two) qk(1, n & 1);
-        mma_commit(&bar.k_free[n & 1]);
-        for (int j = it.t0; j < it.t1; ++j, ++n) {
-          const int st = n & 1, sn = st ^ 1;
-          const bool more = j + 1 < it.t1;
-          if (!(ok = wait(&bar.v_full[st], (n >> 1) & 1))) break;
-          if (!(ok = wait(&bar.p_full[0], pphase))) break;
-          pphase ^= 1;
+      while (ok && next(it)) {
+        const int tiles = it->t1 - it->t0;
+        const bool two = it->rows > kRowsTile;
+        if (lane == 0) ok = [&]() -> bool {
+          if (!wait(&bar.q_full[0], qphase)) return false;
+          if (two && !wait(&bar.q_full[1], q1phase)) return false;
+          if (!wait(&bar.k_full[n & 1], (n >> 1) & 1)) return false;
           fence_after();
-          pv(0, st, j > it.t0);
-          if (!more) mma_commit(&bar.o_done[0]);
-          if (more) {
-            if (!(ok = wait(&bar.k_full[sn], ((n + 1) >> 1) & 1))) break;
+          qk(0, n & 1);
+          if (two) qk(1, n & 1);
+          mma_commit(&bar.k_free[n & 1]);
+          for (int j = 0; j < tiles; ++j) {
+            const uint32_t nj = n + j;
+            const int st = nj & 1, sn = st ^ 1;
+            const bool more = j + 1 < tiles;
+            if (!wait(&bar.v_full[st], (nj >> 1) & 1)) return false;
+            if (!wait(&bar.p_full[0], (pphase + j) & 1)) return false;
             fence_after();
-            qk(0, sn);
+            pv(0, st, j > 0);
+            if (more) {
+              if (!wait(&bar.k_full[sn], ((nj + 1) >> 1) & 1)) return false;
+              fence_after();
+              qk(0, sn);
+            } else {
+              mma_commit(&bar.o_done[0]);
+            }
+            if (two) {
+              if (!wait(&bar.p_full[1], (p1phase + j) & 1)) return false;
+              fence_after();
+              pv(1, st, j > 0);
+              if (!more) mma_commit(&bar.o_done[1]);
+            }
+            mma_commit(&bar.v_free[st]);
+            if (more) {
+              if (two) qk(1, sn);
+              mma_commit(&bar.k_free[sn]);
+            }
           }
-          if (two) {
-            if (!(ok = wait(&bar.p_full[1], p1phase))) break;
-            p1phase ^= 1;
-            fence_after();
-            pv(1, st, j > it.t0);
-            if (!more) mma_commit(&bar.o_done[1]);
-          }
-          mma_commit(&bar.v_free[st]);
-          if (more) {
-            if (two) qk(1, sn);
-            mma_commit(&bar.k_free[sn]);
-          }
+          return true;
+        }();
+        ok = __shfl_sync(kAll, ok, 0);
+        n += tiles;
+        qphase ^= 1;
+        pphase += tiles;
+        if (two) {
+          q1phase ^= 1;
+          p1phase += tiles;
         }
       }
-      // nothing of this CTA's is in flight when its tensor memory is freed: the
-      // last tiles' frees were committed after every MMA
-      if (ok && n > 0) {
-        wait(&bar.v_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
-      } else if (!ok) {
+      // nothing of this CTA's is in flight when its tensor memory is freed
+      if (lane == 0) {
         mma_commit(&bar.end);
         const long long t0 = clock64();
         while (!mbar_try(&bar.end, 0) && clock64() - t0 < kWaitCycles) {
         }
       }
+      __syncwarp();
+    } else if (warp == 13) {
+      if (lane == 0) {
+        Walk walk;
+        walk.start(p, first, last, s_b0, s_off);
+        bool more = true;
+        for (uint32_t i = 0; more; ++i) {
+          if (!wait(&bar.item_free[i % kItems], ((i / kItems) & 1) ^ 1)) break;
+          Item x;
+          more = walk.next(p, x);
+          if (!more) x.t1 = 0;
+          s_item[i % kItems] = x;
+          mbar_arrive(&bar.item_full[i % kItems]);
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
   fence_before();
   __syncthreads();
