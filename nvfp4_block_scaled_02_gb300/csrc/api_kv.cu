@@ -33,7 +33,9 @@ nvfp4_status check_cache(const nvfp4_kv_cache* c) {
   if (!c) return NVFP4_ERR_NULL;
   if (!dim_ok(c->head_dim) || c->kv_heads < 1 || c->kv_heads > kMaxHeads || c->page_size < 16 ||
       c->page_size % 16 != 0 || c->pages < 0 ||
-      !fits(c->pages, (int64_t)c->page_size * c->kv_heads, c->head_dim))
+      !fits(c->pages, (int64_t)c->page_size * c->kv_heads, c->head_dim) ||
+      // rows (a token of a head) are counted in 32 bits: 309 GB of cache at head_dim 64
+      c->pages * c->page_size * c->kv_heads > UINT32_MAX)
     return NVFP4_ERR_SHAPE;
   if (c->four_over_six != 0 && c->four_over_six != 1) return NVFP4_ERR_ENUM;
   return NVFP4_OK;
@@ -275,6 +277,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_attenti
   p.T = (int32_t)cfg->tokens;
   p.hq = cfg->q_heads;
   p.G = (int32_t)group;
+  p.by_group = nvfp4::make_fastdiv((uint32_t)group);
   p.max_q = cfg->max_q;
   p.window = cfg->window;
   p.scale = cfg->scale;

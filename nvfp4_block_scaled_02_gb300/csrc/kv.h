@@ -96,7 +96,7 @@ struct KvAttnParams {
   float M;
   int64_t pages;
   int32_t hk, P, page_shift;  // page_shift: log2(P) or -1
-  FastDiv by_page;
+  FastDiv by_page, by_group;
   const int32_t *table, *seq_len, *q_start;
   int32_t B, cols, T, hq, G, max_q, window;
   float scale;

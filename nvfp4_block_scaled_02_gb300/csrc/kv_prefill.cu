@@ -3,20 +3,20 @@
 //
 // The formula, the exactness of K and V in f16 and the numerics of the softmax
 // are those of kv_attn.cu. Here a CTA takes 256 query rows of one KV head as
-// two tiles of 128 (M), and walks over the keys in tiles of 128:
+// two tiles of 128 (M), and walks over the keys 64 at a time:
 //   S = Q K^T  (Q, K in shared memory; S fp32 in tensor memory)
 //   P = 2^(S f - m + bias), f16, written over S in tensor memory
 //   O += P V   (P from tensor memory, V in shared memory; O fp32 in tensor memory)
-// Tensor memory: S0 S1 (128 columns each), O0 O1 (D each): 512 columns at D = 128.
+// Tensor memory: two S of 64 columns per tile, O of D columns per tile: 512
+// columns at D = 128. With two S per tile the products of the next 64 keys run
+// while the softmax works on these, and the softmax never waits for them.
 //
-// Warps: 0-3 softmax of tile 0 (thread = row), 4-7 of tile 1, 8-11 dequantise K
-// and V tiles into shared memory, 12 issues the MMAs, 13 hands out
-// the items (14 and 15 only fill up their warpgroup, whose registers go to the
-// softmax). While one tile's softmax
-// runs, the other tile's products do. K and V tiles are double-buffered. All
-// hand-overs are mbarriers; QK of the next tile is issued right behind PV of the
-// previous one, so the barrier that says "S is ready" also says that the output
-// accumulator may be rescaled.
+// Warps: 0-3 softmax of tile 0 (thread = row), 4-7 of tile 1, which also load
+// the next item's query rows while the last products run; 8-11 dequantise K and V
+// into shared memory (128 keys at a time, two buffers each); 12 issues the MMAs;
+// 13 hands out the items; 14 finds the cache rows of the keys (block table); 15
+// only fills up the warpgroup, whose registers go to the softmax. All hand-overs
+// are mbarriers.
 //
 // K and V are dequantised once per 256 query rows: 128 threads turn 16 bytes of
 // codes into 32 f16 values each, in the 128-byte-swizzled layout the tensor
@@ -40,16 +40,20 @@ constexpr int kThreads = 512;  // 4 warpgroups
 // warpgroups, one that dequantises, one that issues: 2 x 184 + 80 + 64 = 4 x 128.
 constexpr int kRegsSoftmax = 184, kRegsDequant = 80, kRegsMma = 64;
 static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsMma <= 4 * 128, "the block's registers");
-constexpr int kTileN = 128;    // keys per tile
+constexpr int kTileN = 128;    // keys per tile (dequantised together)
+constexpr int kStepN = 64;     // keys per product
 constexpr int kRowsTile = 128, kRowsItem = 256;
 constexpr int kItems = 4;      // items handed out ahead
 constexpr long long kWaitCycles = 2000000000;  // about a second
 constexpr uint32_t kNegInf = 0xFF800000u;
 
 struct Bars {
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+  uint64_t q_full[2];
+  uint64_t s_full[2][2], p_full[2][2];  // [tile][S buffer]
+  uint64_t o_done[2];                   // one phase per P V
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
   uint64_t item_full[kItems], item_free[kItems];
+  uint64_t rows_full[kItems], rows_free[kItems];  // cache rows of a tile's keys
   uint64_t end;
 };
 
@@ -94,20 +98,22 @@ __device__ __forceinline__ int64_t request_tiles(const KvAttnParams& p, const Re
 struct Item {
   Request r;
   int b, h, row0, rows;
+  float kg, vg;   // outer scales of K and V
   int t0, t1;     // this CTA's tiles, counted from key lo16
-  int64_t first;  // the item's first tile in the run of all tiles
-  int nt;         // all its tiles
+  int c0, c1;     // the CTAs that share it
 };
 
 // The items of this CTA's run [pos, last) of tiles, in the same order in every
 // warp: row blocks inside heads inside requests.
 struct Walk {
-  int64_t pos, last;
+  int64_t pos, last, run;
   int64_t skip;  // tiles before pos, counted from (b, h, pt)
   int b, h, pt, blocks;
   Request r;
-  __device__ void start(const KvAttnParams& p, int64_t first, int64_t end, int b0, int64_t off) {
+  __device__ void start(const KvAttnParams& p, int64_t first, int64_t end, int64_t per_cta, int b0,
+                        int64_t off) {
     pos = first;
+    run = per_cta;
     last = end;
     b = b0;
     bool bad;
@@ -145,8 +151,12 @@ struct Walk {
       it.rows = min(kRowsItem, r.n * p.G - it.row0);
       it.t0 = t.begin + (int)skip;
       it.t1 = it.t0 + count;
-      it.first = pos - skip;
-      it.nt = t.count;
+      it.c0 = (int)((pos - skip) / run);
+      it.c1 = (int)((pos - skip + t.count - 1) / run);
+      const SliceScale ks = slice_scale(p.k_amax[h], p.M), vs = slice_scale(p.v_amax[h], p.M);
+      if (ks.bad || vs.bad) flag(p.status, NVFP4_DEV_BAD_AMAX_BIT);
+      it.kg = ks.g;
+      it.vg = vs.g;
       pos += count;
       skip += count;
       return true;
@@ -166,14 +176,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   __shared__ int64_t s_scan[kThreads / 32];
   __shared__ int s_b0;
   __shared__ int64_t s_off;
+  __shared__ Walk s_walk;
   __shared__ Item s_item[kItems];
+  // first cache row of every 16 keys of a tile: 16 neighbours never leave a page
+  __shared__ uint32_t s_rows[kItems][kTileN / 16];
   constexpr int kTile = Smem<D>::kTile;
   uint8_t* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   uint8_t* sq = base;               // [2] Q tiles
   uint8_t* sk = base + 2 * kTile;   // [2] K tiles
   uint8_t* sv = base + 4 * kTile;   // [2] V tiles
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
 
   // ---- this CTA's run -------------------------------------------------------
   const int share = (p.B + kThreads - 1) / kThreads;
@@ -195,18 +208,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   if (tid == 0) {
     s_dead = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.q_full[i], 128);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.q_full[i], 4);
       mbar_init(&bar.o_done[i], 1);
-      mbar_init(&bar.k_full[i], 128);
-      mbar_init(&bar.v_full[i], 128);
+      mbar_init(&bar.k_full[i], 4);
+      mbar_init(&bar.v_full[i], 4);
       mbar_init(&bar.k_free[i], 1);
       mbar_init(&bar.v_free[i], 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&bar.s_full[i][j], 1);
+        mbar_init(&bar.p_full[i][j], 4);
+      }
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bar.item_full[i], 1);
-      mbar_init(&bar.item_free[i], 13);  // the softmax, dequantising and issuing warps
+      mbar_init(&bar.item_free[i], 14);  // softmax, dequantising, issuing, row-finding warps
+      mbar_init(&bar.rows_full[i], 1);
+      mbar_init(&bar.rows_free[i], 4);
     }
     mbar_init(&bar.end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   };
 
   // The item a warp is at: handed out by warp 13, one after the other, by way of
-  // a ring; t1 = 0 ends the run.
+  // a ring; t1 = 0 ends the run. Asking for the next one gives the last one back.
   uint32_t items = 0;
   auto next = [&](const Item*& it) -> bool {
     if (items > 0) {
@@ -294,92 +311,125 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     const int tile = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane offset in a TMEM address
     const uint32_t ts = t_s(tile) + lanes, to = t_o(tile) + lanes;
-    uint32_t sphase = 0, ophase = 0;
-    bool ok = true;
-    while (ok && next(it)) {
-      if (tile * kRowsTile >= it->rows) continue;
-      const Request r = it->r;
-      const int rr = it->row0 + tile * kRowsTile + row;  // row of the request
-      const bool live = rr < r.n * p.G;
-      const int tk = live ? rr / p.G : 0, hh = rr - tk * p.G;
-      const SliceScale kss = slice_scale(p.k_amax[it->h], p.M);
-      const SliceScale vss = slice_scale(p.v_amax[it->h], p.M);
-      if ((kss.bad || vss.bad) && row == 0) flag(p.status, NVFP4_DEV_BAD_AMAX_BIT);
-
-      // -- query row: scaled to f16, into the swizzled tile
-      float f;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (int64_t)(r.q0 + tk) * p.q_st + (int64_t)(it->h * p.G + hh) * D);
-        uint4 raw[D / 8];
-        uint32_t m = 0;
+    // Loads the item's query rows of this warp into the tile, LPR lanes to a row,
+    // scaled to f16; returns the score factor of this thread's row. The products
+    // with the rows that were there are done: their last scores have been seen.
+    constexpr int LPR = D / 8, kPer = 32 / LPR;
+    const int sub = lane / LPR, ql = lane % LPR;
+    auto load_q = [&](const Item& x) -> float {
+      const int rows = x.r.n * p.G, first_row = x.row0 + tile * kRowsTile + (warp & 3) * 32;
+      const float fk = p.scale * kLog2e * x.kg;
+      float f = 0.0f;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        constexpr int U = 16 / kPer;
+        uint4 raw[U];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) raw[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < U; ++u) {
+          const int rr = first_row + half * 16 + u * kPer + sub;
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if (rr < rows) {
+            const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
+            raw[u] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(x.r.q0 + tk) * p.q_st +
+                                                     (int64_t)(x.h * p.G + hh) * D + ql * 8);
+          }
+        }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) m = max(m, absmax_bits4(raw[i]));
-        if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
-        const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
-        float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        f = p.scale * kLog2e * kss.g * __uint_as_float((uint32_t)(127 - e) << 23);
-        if (f < 0.0f) f = -f, up = -up;  // the running maximum needs f > 0, and a masked
-        f = fmaxf(f, 1.17549435e-38f);   // score (-inf) must stay -inf times f
-        uint8_t* dst = sq + tile * kTile + row * 128;
+        for (int u = 0; u < U; ++u) {
+          const int row32 = half * 16 + u * kPer;  // + sub: the row inside the warp's 32
+          const int row = (warp & 3) * 32 + row32 + sub;
+          const uint4 v = raw[u];
+          uint32_t m = absmax_bits4(v);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = raw[i];
-          const uint4 h = make_uint4(pack_f16x2(bf16_lo(w.x) * up, bf16_hi(w.x) * up),
-                                     pack_f16x2(bf16_lo(w.y) * up, bf16_hi(w.y) * up),
-                                     pack_f16x2(bf16_lo(w.z) * up, bf16_hi(w.z) * up),
-                                     pack_f16x2(bf16_lo(w.w) * up, bf16_hi(w.w) * up));
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (row & 7)) << 4)) = h;
+          for (int d = LPR / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+          if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
+          // 2^e brings the row's largest element to [2^13, 2^14)
+          const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
+          float up = __uint_as_float((uint32_t)(127 + e) << 23);
+          float fr = fk * __uint_as_float((uint32_t)(127 - e) << 23);
+          if (fr < 0.0f) fr = -fr, up = -up;  // the running maximum needs f > 0, and a masked
+          fr = fmaxf(fr, 1.17549435e-38f);    // score (-inf) must stay -inf times f
+          *reinterpret_cast<uint4*>(sq + tile * kTile + (ql >> 3) * (128 * 128) + row * 128 +
+                                    (((ql & 7) ^ (row & 7)) << 4)) =
+              make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                         pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                         pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                         pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+          const float mine_f = __shfl_sync(kAll, fr, (lane % kPer) * LPR);
+          if (lane / kPer == row32 / kPer) f = mine_f;
         }
       }
       fence_smem_async();
-      mbar_arrive(&bar.q_full[tile]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_full[tile]);
+      return f;
+    };
 
+    uint32_t n = 0;  // steps of 64 keys done by this tile
+    bool ok = true, have = next(it);
+    float f = 0.0f;
+    auto mine_of = [&](const Item& x) { return tile * kRowsTile < x.rows; };
+    if (have && mine_of(*it)) f = load_q(*it);
+    while (ok && have) {
+      if (!mine_of(*it)) {
+        have = next(it);
+        if (have && mine_of(*it)) f = load_q(*it);
+        continue;
+      }
+      const Request r = it->r;
+      const int row0 = it->row0 + tile * kRowsTile, rows = r.n * p.G;
+      const int tk = (int)fastdiv((uint32_t)(row0 + row), p.by_group);
+      const bool live = row0 + row < rows;
       // the row sees keys [low, low + span)
       const int lim = live ? r.len - r.n + tk + 1 : 0;
       const int low = p.window > 0 ? lim - min(p.window, r.len) : 0;
       const uint32_t span = (uint32_t)max(lim - low, 0);
       // keys in [safe_lo, safe_hi) are seen by every live row of the tile
-      const int trow0 = it->row0 + tile * kRowsTile;
-      const int trow1 = min(trow0 + kRowsTile, r.n * p.G) - 1;
-      const int safe_hi = r.len - r.n + trow0 / p.G + 1;
-      const int safe_lo = p.window > 0 ? r.len - r.n + trow1 / p.G + 1 - min(p.window, r.len) : 0;
+      const int last_row = min(row0 + kRowsTile, rows) - 1;
+      const int safe_hi = r.len - r.n + (int)fastdiv((uint32_t)row0, p.by_group) + 1;
+      const int safe_lo = p.window > 0 ? r.len - r.n + (int)fastdiv((uint32_t)last_row, p.by_group) +
+                                             1 - min(p.window, r.len)
+                                       : 0;
       float m = __uint_as_float(kNegInf), l = 0.0f;
+      const int steps = 2 * (it->t1 - it->t0);
+      int key0 = r.lo16 + it->t0 * kTileN;
 
-      const int t0 = it->t0, t1 = it->t1;
-      for (int j = t0; j < t1; ++j) {
-        if (!(ok = wait_warp(&bar.s_full[tile], sphase))) break;
-        sphase ^= 1;
+      for (int j = 0; j < steps; ++j, ++n, key0 += kStepN) {
+        const uint32_t sb = n & 1;
+        if (!(ok = wait_warp(&bar.s_full[tile][sb], (n >> 1) & 1))) break;
         fence_after();
-        const int key0 = r.lo16 + j * kTileN;
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+        uint32_t s[2][32];
+        tmem_ld32(ts + kStepN * sb, s[0]);
+        tmem_ld32(ts + kStepN * sb + 32, s[1]);
         tmem_wait_ld();
-        if (key0 + kTileN > safe_hi || key0 < safe_lo) {
+        if (key0 + kStepN > safe_hi || key0 < safe_lo) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((uint32_t)(key0 - low + 32 * c + i) >= span) s[c][i] = kNegInf;
         }
-        float mx = __uint_as_float(kNegInf), mb = mx;
+        float mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[0][i]);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            mx = fmax3(mx, __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-            mb = fmax3(mb, __uint_as_float(s[c][i + 2]), __uint_as_float(s[c][i + 3]));
-          }
-        mx = fmaxf(mx, mb) * f;
-        if (__any_sync(kAll, mx > m + kSlack)) {
-          const float mn = fmaxf(m, mx);
+        for (int i = 4; i < 64; i += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (i + 2 * q + 1 < 64)
+              mx[q] = fmax3(mx[q], __uint_as_float(s[(i + 2 * q) >> 5][(i + 2 * q) & 31]),
+                            __uint_as_float(s[(i + 2 * q + 1) >> 5][(i + 2 * q + 1) & 31]));
+        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
+        if (__any_sync(kAll, top > m + kSlack)) {
+          const float mn = fmaxf(m, top);
           const float a = m == __uint_as_float(kNegInf) ? 0.0f : ex2(m - mn);
           m = mn;
           l *= a;
-          if (j > t0) {  // S is ready, so PV of the previous tile is done
+          if (j > 0) {
+            // the previous P V has to be done (the one before it is: the scores here
+            // were asked for behind it)
+            if (!(ok = wait_warp(&bar.o_done[tile], (n - 1) & 1))) break;
+            fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
@@ -393,9 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }
         const float sub = m == __uint_as_float(kNegInf) ? 0.0f : kBias - m;
         const f2 ff = make_float2(f, f), cc = make_float2(sub, sub);
-        f2 sum = make_float2(0.0f, 0.0f);
+        f2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t h[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -403,27 +453,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
                           ff, cc);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
-            sum = __fadd2_rn(sum, x);
+            sum[i & 1] = __fadd2_rn(sum[i & 1], x);
             h[i] = pack_f16x2(x.x, x.y);
           }
-          tmem_st16(ts + 16 * c, h);
+          tmem_st16(ts + kStepN * sb + 16 * c, h);
         }
-        l += sum.x + sum.y;
         tmem_wait_st();
+        // A phase's parity does not tell it from the one two before. Scores n say
+        // that P V n - 2 is done, and P V n cannot start before this arrival: so the
+        // last step of an item sees P V n - 1 done here, and n behind the loop.
+        if (j == steps - 1 && !(ok = wait_warp(&bar.o_done[tile], (n - 1) & 1))) break;
         fence_before();
-        mbar_arrive(&bar.p_full[tile]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[tile][sb]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
 
+      // -- the next item's query rows, while the last P V runs
+      const int hh = row0 + row - tk * p.G;
+      const float vg = it->vg;
+      const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it->h * p.G + hh;
+      const int c0 = it->c0, c1 = it->c1;
+      have = next(it);
+      if (have && mine_of(*it)) f = load_q(*it);
+
       // -- result: the whole row, or a record of this CTA's part of it
-      if (!(ok = wait_warp(&bar.o_done[tile], ophase))) break;
-      ophase ^= 1;
+      if (!(ok = wait_warp(&bar.o_done[tile], (n - 1) & 1))) break;
       fence_after();
-      const int64_t c0 = it->first / run, c1 = (it->first + it->nt - 1) / run;
       uint32_t s[32];
       if (c0 == c1) {
-        const float fo = l == 0.0f ? 0.0f : vss.g / l;
-        const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it->h * p.G + hh;
+        const float fo = l == 0.0f ? 0.0f : vg / l;
         uint4* dst = reinterpret_cast<uint4*>(p.out) + orow * (D / 8);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -465,24 +525,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (__shfl_sync(kAll, mine_ticket, 0) == (uint32_t)(c1 - c0)) {
           __threadfence();
           float mx = __uint_as_float(kNegInf);
-          for (int64_t c = c0; c <= c1; ++c)
-            mx = fmaxf(mx, __ldcg(p.part + (c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord +
+          for (int c = c0; c <= c1; ++c)
+            mx = fmaxf(mx, __ldcg(p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord +
                                   kRowsItem * 128 + ri));
           float sum = 0.0f;
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* q = p.part + (c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
+          for (int c = c0; c <= c1; ++c) {
+            const float* q = p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
             const float mc = __ldcg(q + kRowsItem * 128 + ri);
             if (mc != __uint_as_float(kNegInf))
               sum += __ldcg(q + kRowsItem * 129 + ri) * ex2(mc - mx);
           }
-          const float fo = sum == 0.0f ? 0.0f : vss.g / sum;
-          const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it->h * p.G + hh;
+          const float fo = sum == 0.0f ? 0.0f : vg / sum;
           uint2* dst = reinterpret_cast<uint2*>(p.out) + orow * (D / 4);
 #pragma unroll 4
           for (int d = 0; d < D / 4; ++d) {
             float4 v = make_float4(0, 0, 0, 0);
-            for (int64_t c = c0; c <= c1; ++c) {
-              const float* q = p.part + (c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
+            for (int c = c0; c <= c1; ++c) {
+              const float* q = p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
               const float mc = __ldcg(q + kRowsItem * 128 + ri);
               const float4 x = __ldcg(reinterpret_cast<const float4*>(q) + d * kRowsItem + ri);
               if (mc == __uint_as_float(kNegInf)) continue;
@@ -503,36 +562,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     // ==== dequantise ============================================================
     fewer_registers<kRegsDequant>();
     // thread: rows 8 w + (lane & 7) + 32 i of a tile, 16-byte chunk lane / 8 of the
-    // codes (D = 64: two row halves instead of four chunks)
-    constexpr int kRowsPer = D == 128 ? 4 : 2;
+    // codes (D = 64: rows 16 w + (lane & 15) + 64 i, chunk lane / 16): a quarter
+    // warp's stores hit all banks once
+    constexpr int kRowsPer = D == 128 ? 4 : 2, kRowStep = D == 128 ? 32 : 64;
     const int w = warp - 8;
     const int rbase = D == 128 ? w * 8 + (lane & 7) : w * 16 + (lane & 15);
     const int chunk = D == 128 ? lane >> 3 : lane >> 4;
-    constexpr int kRowStep = D == 128 ? 32 : 64;
     uint32_t n = 0;  // tiles done
     bool ok = true;
     while (ok && next(it)) {
-      const int32_t* table = p.table + (int64_t)it->b * p.cols;
-      const int len = it->r.len;
+      const int len = it->r.len, t1 = it->t1;
+      int tok = it->r.lo16 + it->t0 * kTileN + rbase;  // this thread's first key of a tile
       uint4 ck[kRowsPer], cv[kRowsPer];
       uint32_t bk[kRowsPer], bv[kRowsPer];
-      int64_t at[kRowsPer];  // cache row of this thread's rows, or -1
-      auto locate = [&](int j) {
+      uint32_t at[kRowsPer];   // cache rows of this thread's keys
+      bool in[kRowsPer];       // ... that the request has
+      auto locate = [&](uint32_t tile_n, int first) -> bool {
+        const uint32_t slot = tile_n % kItems;
+        if (!wait_warp(&bar.rows_full[slot], (tile_n / kItems) & 1)) return false;
 #pragma unroll
         for (int i = 0; i < kRowsPer; ++i) {
-          const int tok = it->r.lo16 + j * kTileN + rbase + kRowStep * i;
-          at[i] = -1;
-          if (tok < len) {
-            const int pg = p.page_shift >= 0 ? tok >> p.page_shift
-                                             : (int)fastdiv((uint32_t)tok, p.by_page);
-            int64_t page = table[pg];
-            if (page < 0 || page >= p.pages) {
-              page = 0;
-              flag(p.status, kDevBadIndex);
-            }
-            at[i] = (page * p.hk + it->h) * p.P + (tok - pg * p.P);
-          }
+          const int row = rbase + kRowStep * i;
+          at[i] = s_rows[slot][row >> 4] + (row & 15);
+          in[i] = first + kRowStep * i < len;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.rows_free[slot]);
+        return true;
       };
       auto load = [&](const uint8_t* codes, const uint8_t* scales, uint4 (&c)[kRowsPer],
                       uint32_t (&b)[kRowsPer]) {
@@ -540,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         for (int i = 0; i < kRowsPer; ++i) {
           c[i] = make_uint4(0, 0, 0, 0);
           b[i] = 0;  // keys past the request: zeros, whatever the cache holds there
-          if (at[i] >= 0) {
-            c[i] = *reinterpret_cast<const uint4*>(codes + at[i] * (D / 2) + chunk * 16);
-            b[i] = *reinterpret_cast<const uint16_t*>(scales + at[i] * (D / 16) + chunk * 2);
+          if (in[i]) {
+            c[i] = *reinterpret_cast<const uint4*>(codes + (uint64_t)at[i] * (D / 2) + chunk * 16);
+            b[i] = *reinterpret_cast<const uint16_t*>(scales + (uint64_t)at[i] * (D / 16) + chunk * 2);
           }
         }
       };
@@ -555,113 +611,120 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t fs = __byte_perm(sc, 0, k < 2 ? 0x1010 : 0x3232);
-            uint32_t h[4];
-            codes8(words[k], h);
+            uint32_t v[4];
+            codes8(words[k], v);
             const int c16 = chunk * 4 + k;
             *reinterpret_cast<uint4*>(dst + (c16 >> 3) * (128 * 128) + row * 128 +
                                       (((c16 & 7) ^ (row & 7)) << 4)) =
-                make_uint4(h2mul(h[0], fs), h2mul(h[1], fs), h2mul(h[2], fs), h2mul(h[3], fs));
+                make_uint4(h2mul(v[0], fs), h2mul(v[1], fs), h2mul(v[2], fs), h2mul(v[3], fs));
           }
         }
+        fence_smem_async();
+        __syncwarp();
       };
-      locate(it->t0);
+      if (!(ok = locate(n, tok))) break;
       load(p.kc, p.ks, ck, bk);
       load(p.vc, p.vs, cv, bv);
-      for (int j = it->t0; j < it->t1; ++j, ++n) {
+      for (int j = it->t0; j < t1; ++j, ++n, tok += kTileN) {
         const int st = n & 1;
         const uint32_t par = ((n >> 1) & 1) ^ 1;
-        if (j + 1 < it->t1) locate(j + 1);
+        const bool more = j + 1 < t1;
+        if (more && !(ok = locate(n + 1, tok + kTileN))) break;
         if (!(ok = wait_warp(&bar.k_free[st], par))) break;
         store(sk + st * kTile, ck, bk);
-        fence_smem_async();
-        mbar_arrive(&bar.k_full[st]);
-        if (j + 1 < it->t1) load(p.kc, p.ks, ck, bk);
+        if (lane == 0) mbar_arrive(&bar.k_full[st]);
+        if (more) load(p.kc, p.ks, ck, bk);
         if (!(ok = wait_warp(&bar.v_free[st], par))) break;
         store(sv + st * kTile, cv, bv);
-        fence_smem_async();
-        mbar_arrive(&bar.v_full[st]);
-        if (j + 1 < it->t1) load(p.vc, p.vs, cv, bv);
+        if (lane == 0) mbar_arrive(&bar.v_full[st]);
+        if (more) load(p.vc, p.vs, cv, bv);
       }
     }
   } else {
-    // ==== MMAs: one thread =======================================================
     fewer_registers<kRegsMma>();
     if (warp == 12) {
-      constexpr uint32_t kQK = mma_desc(128, false), kPV = mma_desc(D, true);
+      // ==== MMAs: one thread =====================================================
+      constexpr uint32_t kQK = mma_desc(kStepN, false), kPV = mma_desc(D, true);
       const uint32_t dq = smem_addr(sq) >> 4, dk = smem_addr(sk) >> 4, dv = smem_addr(sv) >> 4;
-      auto qk = [&](int tile, int st) {
-        uint32_t a = dq + (kTile >> 4) * tile, b = dk + (kTile >> 4) * st;
+      // S of one tile for 64 keys: half `half` of the K tile in stage st
+      auto qk = [&](int tile, int st, int half) {
+        uint32_t a = dq + (kTile >> 4) * tile;
+        uint32_t b = dk + (kTile >> 4) * st + (kStepN * 128 >> 4) * half;
         asm volatile("" : "+r"(a), "+r"(b));  // the steps' addresses are added here, not kept
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           // 16 values = 32 bytes along a row; 64 values per panel
           const uint32_t o = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-          mma_ss(t_s(tile), smem_desc(a + o, 0), smem_desc(b + o, 0), kQK, k > 0);
+          mma_ss(t_s(tile) + kStepN * half, smem_desc(a + o, 0), smem_desc(b + o, 0), kQK, k > 0);
         }
-        mma_commit(&bar.s_full[tile]);
+        mma_commit(&bar.s_full[tile][half]);
       };
-      auto pv = [&](int tile, int st, bool add) {
-        uint32_t b = dv + (kTile >> 4) * st, a = t_s(tile);
+      auto pv = [&](int tile, int st, int half, bool add) {
+        uint32_t a = t_s(tile) + kStepN * half;
+        uint32_t b = dv + (kTile >> 4) * st + (kStepN * 128 >> 4) * half;
         asm volatile("" : "+r"(a), "+r"(b));
 #pragma unroll
-        for (int k = 0; k < kTileN / 16; ++k)  // 16 keys = two atoms of 8 rows
+        for (int k = 0; k < kStepN / 16; ++k)  // 16 keys = two atoms of 8 rows
           mma_ts(t_o(tile), a + 8 * k, smem_desc(b + (2048 >> 4) * k, 128 * 128), kPV,
                  add || k > 0);
+        mma_commit(&bar.o_done[tile]);
       };
-      uint32_t n = 0;  // tiles done
-      uint32_t qphase = 0, q1phase = 0, pphase = 0, p1phase = 0;
+      uint32_t n = 0, n1 = 0;  // tiles done, and those with both query tiles
+      uint32_t qphase = 0, q1phase = 0;
       bool ok = true;
       while (ok && next(it)) {
         const int tiles = it->t1 - it->t0;
         const bool two = it->rows > kRowsTile;
-        if (lane == 0) ok = [&]() -> bool {
-          if (!wait(&bar.q_full[0], qphase)) return false;
-          if (two && !wait(&bar.q_full[1], q1phase)) return false;
+        if (elect_one()) ok = [&]() -> bool {
           if (!wait(&bar.k_full[n & 1], (n >> 1) & 1)) return false;
+          if (!wait(&bar.q_full[0], qphase)) return false;
           fence_after();
-          qk(0, n & 1);
-          if (two) qk(1, n & 1);
+          qk(0, n & 1, 0);
+          if (two) {
+            if (!wait(&bar.q_full[1], q1phase)) return false;
+            fence_after();
+            qk(1, n & 1, 0);
+          }
+          qk(0, n & 1, 1);
+          if (two) qk(1, n & 1, 1);
           mma_commit(&bar.k_free[n & 1]);
           for (int j = 0; j < tiles; ++j) {
             const uint32_t nj = n + j;
             const int st = nj & 1, sn = st ^ 1;
             const bool more = j + 1 < tiles;
             if (!wait(&bar.v_full[st], (nj >> 1) & 1)) return false;
-            if (!wait(&bar.p_full[0], (pphase + j) & 1)) return false;
-            fence_after();
-            pv(0, st, j > 0);
-            if (more) {
-              if (!wait(&bar.k_full[sn], ((nj + 1) >> 1) & 1)) return false;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (!wait(&bar.p_full[0][half], nj & 1)) return false;
               fence_after();
-              qk(0, sn);
-            } else {
-              mma_commit(&bar.o_done[0]);
-            }
-            if (two) {
-              if (!wait(&bar.p_full[1], (p1phase + j) & 1)) return false;
-              fence_after();
-              pv(1, st, j > 0);
-              if (!more) mma_commit(&bar.o_done[1]);
+              pv(0, st, half, j > 0 || half > 0);
+              if (more) {
+                if (half == 0 && !wait(&bar.k_full[sn], ((nj + 1) >> 1) & 1)) return false;
+                fence_after();
+                qk(0, sn, half);
+              }
+              if (two) {
+                if (!wait(&bar.p_full[1][half], (n1 + j) & 1)) return false;
+                fence_after();
+                pv(1, st, half, j > 0 || half > 0);
+                if (more) qk(1, sn, half);
+              }
             }
             mma_commit(&bar.v_free[st]);
-            if (more) {
-              if (two) qk(1, sn);
-              mma_commit(&bar.k_free[sn]);
-            }
+            if (more) mma_commit(&bar.k_free[sn]);
           }
           return true;
         }();
-        ok = __shfl_sync(kAll, ok, 0);
+        ok = __all_sync(kAll, ok);
         n += tiles;
         qphase ^= 1;
-        pphase += tiles;
         if (two) {
           q1phase ^= 1;
-          p1phase += tiles;
+          n1 += tiles;
         }
       }
       // nothing of this CTA's is in flight when its tensor memory is freed
-      if (lane == 0) {
+      if (elect_one()) {
         mma_commit(&bar.end);
         const long long t0 = clock64();
         while (!mbar_try(&bar.end, 0) && clock64() - t0 < kWaitCycles) {
@@ -669,20 +732,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       }
       __syncwarp();
     } else if (warp == 13) {
+      // ==== items ================================================================
       if (lane == 0) {
-        Walk walk;
-        walk.start(p, first, last, s_b0, s_off);
+        s_walk.start(p, first, last, run, s_b0, s_off);
         bool more = true;
         for (uint32_t i = 0; more; ++i) {
           if (!wait(&bar.item_free[i % kItems], ((i / kItems) & 1) ^ 1)) break;
-          Item x;
-          more = walk.next(p, x);
+          Item& x = s_item[i % kItems];
+          more = s_walk.next(p, x);
           if (!more) x.t1 = 0;
-          s_item[i % kItems] = x;
           mbar_arrive(&bar.item_full[i % kItems]);
         }
       }
       __syncwarp();
+    } else if (warp == 14) {
+      // ==== cache rows: lane g looks up keys 16 g .. 16 g + 15 of a tile ==========
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && next(it)) {
+        const int32_t* table = p.table + (int64_t)it->b * p.cols;
+        const int len = it->r.len, h = it->h, t1 = it->t1;
+        int key = it->r.lo16 + it->t0 * kTileN + 16 * lane;
+        for (int j = it->t0; j < t1; ++j, ++n, key += kTileN) {
+          uint32_t row = 0;
+          if (lane < kTileN / 16 && key < len) {
+            const int pg = p.page_shift >= 0 ? key >> p.page_shift
+                                             : (int)fastdiv((uint32_t)key, p.by_page);
+            int64_t page = table[pg];
+            if (page < 0 || page >= p.pages) {
+              page = 0;
+              flag(p.status, kDevBadIndex);
+            }
+            row = (uint32_t)((page * p.hk + h) * p.P + (key - pg * p.P));
+          }
+          if (!(ok = wait_warp(&bar.rows_free[n % kItems], ((n / kItems) & 1) ^ 1))) break;
+          if (lane < kTileN / 16) s_rows[n % kItems][lane] = row;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.rows_full[n % kItems]);
+        }
+      }
     }
   }
   fence_before();
