@@ -13,10 +13,9 @@
 //
 // Warps: 0-3 softmax of tile 0 (thread = row), 4-7 of tile 1, which also load
 // the next item's query rows while the last products run; 8-11 dequantise K and V
-// into shared memory (128 keys at a time, two buffers each); 12 issues the MMAs;
-// 13 hands out the items; 14 finds the cache rows of the keys (block table); 15
-// only fills up the warpgroup, whose registers go to the softmax. All hand-overs
-// are mbarriers.
+// into shared memory (128 keys at a time, two buffers each); 12 and 15 issue the
+// MMAs of tiles 0 and 1; 13 hands out the items; 14 finds the cache rows of the
+// keys (block table). All hand-overs are mbarriers.
 //
 // K and V are dequantised once per 256 query rows: 128 threads turn 16 bytes of
 // codes into 32 f16 values each, in the 128-byte-swizzled layout the tensor
@@ -212,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       mbar_init(&bar.o_done[i], 1);
       mbar_init(&bar.k_full[i], 4);
       mbar_init(&bar.v_full[i], 4);
-      mbar_init(&bar.k_free[i], 1);
-      mbar_init(&bar.v_free[i], 1);
+      mbar_init(&bar.k_free[i], 2);  // both issuing warps
+      mbar_init(&bar.v_free[i], 2);
       for (int j = 0; j < 2; ++j) {
         mbar_init(&bar.s_full[i][j], 1);
         mbar_init(&bar.p_full[i][j], 4);
@@ -221,11 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bar.item_full[i], 1);
-      mbar_init(&bar.item_free[i], 14);  // softmax, dequantising, issuing, row-finding warps
+      mbar_init(&bar.item_free[i], 15);  // softmax, dequantising, issuing, row-finding warps
       mbar_init(&bar.rows_full[i], 1);
       mbar_init(&bar.rows_free[i], 4);
     }
-    mbar_init(&bar.end, 1);
+    mbar_init(&bar.end, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -524,32 +523,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (lane == 0) mine_ticket = atomicAdd(ticket, 1u);
         if (__shfl_sync(kAll, mine_ticket, 0) == (uint32_t)(c1 - c0)) {
           __threadfence();
+          auto record = [&](int c) {
+            return p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
+          };
           float mx = __uint_as_float(kNegInf);
-          for (int c = c0; c <= c1; ++c)
-            mx = fmaxf(mx, __ldcg(p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord +
-                                  kRowsItem * 128 + ri));
+          for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(record(c) + kRowsItem * 128 + ri));
           float sum = 0.0f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* q = p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
-            const float mc = __ldcg(q + kRowsItem * 128 + ri);
-            if (mc != __uint_as_float(kNegInf))
-              sum += __ldcg(q + kRowsItem * 129 + ri) * ex2(mc - mx);
-          }
+          auto weight = [&](int c) {
+            const float mc = __ldcg(record(c) + kRowsItem * 128 + ri);
+            return mc == __uint_as_float(kNegInf) ? 0.0f : ex2(mc - mx);
+          };
+          for (int c = c0; c <= c1; ++c) sum += weight(c) * __ldcg(record(c) + kRowsItem * 129 + ri);
           const float fo = sum == 0.0f ? 0.0f : vg / sum;
           uint2* dst = reinterpret_cast<uint2*>(p.out) + orow * (D / 4);
-#pragma unroll 4
-          for (int d = 0; d < D / 4; ++d) {
-            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int d0 = 0; d0 < D / 4; d0 += 16) {  // 16 loads of 16 bytes in flight
+            float4 v[16];
+#pragma unroll
+            for (int d = 0; d < 16; ++d) v[d] = make_float4(0, 0, 0, 0);
             for (int c = c0; c <= c1; ++c) {
-              const float* q = p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
-              const float mc = __ldcg(q + kRowsItem * 128 + ri);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(q) + d * kRowsItem + ri);
-              if (mc == __uint_as_float(kNegInf)) continue;
-              const float w = ex2(mc - mx);
-              v.x += x.x * w, v.y += x.y * w, v.z += x.z * w, v.w += x.w * w;
+              const float w = weight(c);
+              const float4* q = reinterpret_cast<const float4*>(record(c)) + d0 * kRowsItem + ri;
+              float4 x[16];
+#pragma unroll
+              for (int d = 0; d < 16; ++d) x[d] = __ldcg(q + d * kRowsItem);
+              if (w != 0.0f)  // a part that saw nothing of this row holds no numbers
+#pragma unroll
+                for (int d = 0; d < 16; ++d) {
+                  v[d].x = __fmaf_rn(x[d].x, w, v[d].x), v[d].y = __fmaf_rn(x[d].y, w, v[d].y);
+                  v[d].z = __fmaf_rn(x[d].z, w, v[d].z), v[d].w = __fmaf_rn(x[d].w, w, v[d].w);
+                }
             }
             if (live)
-              dst[d] = make_uint2(pack_bf16x2(v.x * fo, v.y * fo), pack_bf16x2(v.z * fo, v.w * fo));
+#pragma unroll
+              for (int d = 0; d < 16; ++d)
+                dst[d0 + d] = make_uint2(pack_bf16x2(v[d].x * fo, v[d].y * fo),
+                                         pack_bf16x2(v[d].z * fo, v[d].w * fo));
           }
           if (live && p.lse)
             p.lse[orow] =
@@ -642,51 +651,62 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     }
   } else {
     fewer_registers<kRegsMma>();
-    if (warp == 12) {
-      // ==== MMAs: one thread =====================================================
+    if (warp == 12 || warp == 15) {
+      // ==== MMAs: one warp per query tile, one thread of it ========================
+      const int tile = warp == 12 ? 0 : 1;
       constexpr uint32_t kQK = mma_desc(kStepN, false), kPV = mma_desc(D, true);
-      const uint32_t dq = smem_addr(sq) >> 4, dk = smem_addr(sk) >> 4, dv = smem_addr(sv) >> 4;
-      // S of one tile for 64 keys: half `half` of the K tile in stage st
-      auto qk = [&](int tile, int st, int half) {
-        uint32_t a = dq + (kTile >> 4) * tile;
-        uint32_t b = dk + (kTile >> 4) * st + (kStepN * 128 >> 4) * half;
+      const uint32_t dq = smem_addr(sq + tile * kTile) >> 4;
+      const uint32_t dk = smem_addr(sk) >> 4, dv = smem_addr(sv) >> 4;
+      const uint32_t ts = t_s(tile), to = t_o(tile);
+      // S for 64 keys: half `half` of the K tile in stage st
+      auto qk = [&](int st, int half) {
+        uint32_t a = dq, b = dk + (kTile >> 4) * st + (kStepN * 128 >> 4) * half;
         asm volatile("" : "+r"(a), "+r"(b));  // the steps' addresses are added here, not kept
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           // 16 values = 32 bytes along a row; 64 values per panel
           const uint32_t o = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-          mma_ss(t_s(tile) + kStepN * half, smem_desc(a + o, 0), smem_desc(b + o, 0), kQK, k > 0);
+          mma_ss(ts + kStepN * half, smem_desc(a + o, 0), smem_desc(b + o, 0), kQK, k > 0);
         }
         mma_commit(&bar.s_full[tile][half]);
       };
-      auto pv = [&](int tile, int st, int half, bool add) {
-        uint32_t a = t_s(tile) + kStepN * half;
+      auto pv = [&](int st, int half, bool add) {
+        uint32_t a = ts + kStepN * half;
         uint32_t b = dv + (kTile >> 4) * st + (kStepN * 128 >> 4) * half;
         asm volatile("" : "+r"(a), "+r"(b));
 #pragma unroll
         for (int k = 0; k < kStepN / 16; ++k)  // 16 keys = two atoms of 8 rows
-          mma_ts(t_o(tile), a + 8 * k, smem_desc(b + (2048 >> 4) * k, 128 * 128), kPV,
-                 add || k > 0);
+          mma_ts(to, a + 8 * k, smem_desc(b + (2048 >> 4) * k, 128 * 128), kPV, add || k > 0);
         mma_commit(&bar.o_done[tile]);
       };
-      uint32_t n = 0, n1 = 0;  // tiles done, and those with both query tiles
-      uint32_t qphase = 0, q1phase = 0;
+      uint32_t n = 0, mine_n = 0;  // key tiles done, and those of them with this query tile
+      uint32_t qphase = 0;
       bool ok = true;
       while (ok && next(it)) {
         const int tiles = it->t1 - it->t0;
         const bool two = it->rows > kRowsTile;
+        if (tile == 1 && !two) {
+          // follows tile by tile all the same: a barrier's parity only tells
+          // neighbouring phases apart
+          if (elect_one()) ok = [&]() -> bool {
+            for (uint32_t j = n; j < n + tiles; ++j) {
+              if (!wait(&bar.k_full[j & 1], (j >> 1) & 1)) return false;
+              mbar_arrive(&bar.k_free[j & 1]);
+              if (!wait(&bar.v_full[j & 1], (j >> 1) & 1)) return false;
+              mbar_arrive(&bar.v_free[j & 1]);
+            }
+            return true;
+          }();
+          ok = __all_sync(kAll, ok);
+          n += tiles;
+          continue;
+        }
         if (elect_one()) ok = [&]() -> bool {
           if (!wait(&bar.k_full[n & 1], (n >> 1) & 1)) return false;
-          if (!wait(&bar.q_full[0], qphase)) return false;
+          if (!wait(&bar.q_full[tile], qphase)) return false;
           fence_after();
-          qk(0, n & 1, 0);
-          if (two) {
-            if (!wait(&bar.q_full[1], q1phase)) return false;
-            fence_after();
-            qk(1, n & 1, 0);
-          }
-          qk(0, n & 1, 1);
-          if (two) qk(1, n & 1, 1);
+          qk(n & 1, 0);
+          qk(n & 1, 1);
           mma_commit(&bar.k_free[n & 1]);
           for (int j = 0; j < tiles; ++j) {
             const uint32_t nj = n + j;
@@ -695,19 +715,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             if (!wait(&bar.v_full[st], (nj >> 1) & 1)) return false;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              if (!wait(&bar.p_full[0][half], nj & 1)) return false;
+              if (!wait(&bar.p_full[tile][half], (mine_n + j) & 1)) return false;
               fence_after();
-              pv(0, st, half, j > 0 || half > 0);
+              pv(st, half, j > 0 || half > 0);
               if (more) {
                 if (half == 0 && !wait(&bar.k_full[sn], ((nj + 1) >> 1) & 1)) return false;
                 fence_after();
-                qk(0, sn, half);
-              }
-              if (two) {
-                if (!wait(&bar.p_full[1][half], (n1 + j) & 1)) return false;
-                fence_after();
-                pv(1, st, half, j > 0 || half > 0);
-                if (more) qk(1, sn, half);
+                qk(sn, half);
               }
             }
             mma_commit(&bar.v_free[st]);
@@ -717,13 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }();
         ok = __all_sync(kAll, ok);
         n += tiles;
+        mine_n += tiles;
         qphase ^= 1;
-        if (two) {
-          q1phase ^= 1;
-          n1 += tiles;
-        }
       }
-      // nothing of this CTA's is in flight when its tensor memory is freed
+      // nothing of this warp's is in flight when the tensor memory is freed
       if (elect_one()) {
         mma_commit(&bar.end);
         const long long t0 = clock64();
