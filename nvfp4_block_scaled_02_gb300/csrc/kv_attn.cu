@@ -45,6 +45,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 4;  // tiles in flight per warp (cp.async groups)
 // A request this kernel takes.
 __device__ __forceinline__ Request few_rows(const KvAttnParams& p, int b, bool& bad) {
   Request r = request(p, b, bad);
@@ -57,24 +58,46 @@ struct Stage {
   uint8_t k[16 * D / 2], v[16 * D / 2], ks[16 * D / 16], vs[16 * D / 16];
 };
 
+// Padded row of the joined outputs (floats), and where the four values at
+// float4 index q of a row lie in it: the writing lanes (g, t) then hit all banks.
+template <int D>
+constexpr int kJoinRow = D + 4;
+template <int D>
+__device__ __forceinline__ int join_at(int q) {
+  return D == 128 ? (q ^ ((q >> 2) & 1)) * 4 : q * 4;
+}
+
+template <int D, int NT>
+struct Layout {
+  static constexpr size_t kStage = sizeof(Stage<D>) * kStages * kWarps;
+  static constexpr size_t kJoin = (size_t)kWarps * 8 * NT * kJoinRow<D> * 4;
+  static constexpr size_t kBytes = kStage + kJoin;
+};
+
+// Tiles [t0, t1) of KV head h of request b.
+struct Segment {
+  Request r;
+  int b, h, t0, t1;
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     kv_attn_kernel(const KvAttnParams p, const int ctas) {
   pdl_begin();
-  constexpr int kStages = 5;
   constexpr int kRows = 8 * NT;  // query rows of an item at most
   constexpr int KS = D / 16;     // k steps of q K^T, and 16-row tiles of V^T
   constexpr int DQ = D / 4;      // dimensions of K per lane
   extern __shared__ __align__(16) uint8_t smem[];
   Stage<D>* stages = reinterpret_cast<Stage<D>*>(smem) + (threadIdx.x >> 5) * kStages;
-  float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][kRows][D], after the tiles are done
+  float* s_o = reinterpret_cast<float*>(smem + Layout<D, NT>::kStage);  // [kWarps][kRows][row]
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int64_t s_scan[kWarps];
   __shared__ int s_b0;
   __shared__ int64_t s_off;
   __shared__ uint32_t s_ticket;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(kAll, tid >> 5, 0);
 
   // ---- this CTA's run of tiles: a scan over the requests -------------------
   const int share = (p.B + kThreads - 1) / kThreads;
@@ -84,8 +107,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     bool bad;
     const Request r = few_rows(p, b, bad);
     if (bad && blockIdx.x == 0) flag(p.status, kDevBadIndex);
-    const int blocks = (r.n * p.G + kRows - 1) / kRows;
-    mine += (int64_t)r.tiles * blocks * p.hk;
+    mine += (int64_t)r.tiles * p.hk;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -109,8 +131,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     for (int b = rb0; b < rb1; ++b) {
       bool bad;
       const Request r = few_rows(p, b, bad);
-      const int blocks = (r.n * p.G + kRows - 1) / kRows;
-      const int64_t c = (int64_t)r.tiles * blocks * p.hk;
+      const int64_t c = (int64_t)r.tiles * p.hk;
       if (first < at + c) {
         s_b0 = b;
         s_off = first - at;
@@ -135,70 +156,105 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   __syncthreads();
   if (first >= last) return;
 
-  int b = s_b0;
-  int64_t off = s_off;  // tiles of request b before this CTA's next one
-  int64_t pos = first;
-  while (pos < last) {
-    bool bad;
-    Request r = few_rows(p, b, bad);
-    const int blocks = (r.n * p.G + kRows - 1) / kRows;
-    if (off >= (int64_t)r.tiles * blocks * p.hk) {
-      off -= (int64_t)r.tiles * blocks * p.hk;
-      ++b;
-      continue;
-    }
-    // the item: KV head h, row block rb of request b; tiles [t0, t1) of it
-    const int item = (int)(off / r.tiles), t0 = (int)(off - (int64_t)item * r.tiles);
-    const int t1 = (int)min((int64_t)r.tiles, t0 + (last - pos));
-    const int h = item / blocks, row0 = (item - h * blocks) * kRows;
-    const int nrows = min(kRows, r.n * p.G - row0);
-    const int32_t* table = p.table + (int64_t)b * p.cols;
-
-    // ---- loads: tile j of the item is this warp's when j = t0 + warp mod 4 --
-    auto issue = [&](int j, int slot) {
-      if (j < t1) {
-        const int tok = r.lo16 + j * 16;
-        int pg, of;
-        if (p.page_shift >= 0) {
-          pg = tok >> p.page_shift;
-          of = tok & (p.P - 1);
-        } else {
-          pg = (int)fastdiv((uint32_t)tok, p.by_page);
-          of = tok - pg * p.P;
-        }
-        int64_t page = table[pg];
-        if (page < 0 || page >= p.pages) {
-          page = 0;
-          if (lane == 0) flag(p.status, kDevBadIndex);
-        }
-        const int64_t row = (page * p.hk + h) * p.P + of;
-        Stage<D>& s = stages[slot];
-        constexpr int CPR = D / 32;  // 16-byte chunks of a code row
-#pragma unroll
-        for (int c = lane; c < 16 * CPR; c += 32) {
-          const int tk = c / CPR, part = c % CPR;
-          // K row index of the token (the inverse of token = 4 (r & 1) + r / 2 + 8 (r / 8))
-          const int kr = 2 * (tk & 3) + ((tk >> 2) & 1) + 8 * (tk >> 3);
-          cp_async16(s.k + kr * (D / 2) + part * 16, p.kc + row * (D / 2) + c * 16);
-          // V chunks swapped so that lanes (g, t) read 4 tokens without bank conflicts
-          const int vp = D == 128 ? part ^ (((tk >> 1) & 1) << 1) : part;
-          cp_async16(s.v + tk * (D / 2) + vp * 16, p.vc + row * (D / 2) + c * 16);
-        }
-        if (lane < D / 16) {
-          cp_async16(s.ks + lane * 16, p.ks + row * (D / 16) + lane * 16);
-        } else if (lane < D / 8) {
-          const int c = lane - D / 16;
-          cp_async16(s.vs + c * 16, p.vs + row * (D / 16) + c * 16);
-        }
+  // ---- segments: what this CTA does of each item it meets ------------------
+  int64_t pos = first;  // tiles of the run not yet in a segment start here
+  Segment seg;
+  seg.b = s_b0;
+  bool bad0;
+  seg.r = few_rows(p, seg.b, bad0);
+  seg.h = (int)(s_off / seg.r.tiles);
+  seg.t0 = (int)(s_off - (int64_t)seg.h * seg.r.tiles);
+  seg.t1 = (int)min((int64_t)seg.r.tiles, seg.t0 + (last - pos));
+  pos += seg.t1 - seg.t0;
+  auto next = [&](Segment& s) -> bool {  // the one after s, which it replaces
+    if (pos >= last) return false;
+    if (s.t1 == s.r.tiles) {
+      s.t1 = 0;
+      if (++s.h == p.hk) {
+        s.h = 0;
+        do {
+          if (++s.b >= p.B) return false;
+          bool bad;
+          s.r = few_rows(p, s.b, bad);
+        } while (s.r.tiles == 0);
       }
-      cp_async_commit();
-    };
-    int slot = 0;
+    }
+    s.t0 = s.t1;
+    s.t1 = (int)min((int64_t)s.r.tiles, s.t0 + (last - pos));
+    pos += s.t1 - s.t0;
+    return true;
+  };
+
+  // A segment's tile j is this warp's when j = t0 + warp mod 4. Lane l holds the
+  // cache row of the first key of its l-th tile from `from` on: one table look-up
+  // for 32 tiles, well before the copies that need it.
+  auto look_up = [&](const Segment& s, int from) -> uint32_t {
+    const int j = from + lane * kWarps;
+    if (j >= s.t1) return 0;
+    const int tok = s.r.lo16 + j * 16;
+    int pg, of;
+    if (p.page_shift >= 0) {
+      pg = tok >> p.page_shift;
+      of = tok & (p.P - 1);
+    } else {
+      pg = (int)fastdiv((uint32_t)tok, p.by_page);
+      of = tok - pg * p.P;
+    }
+    int64_t page = p.table[(int64_t)s.b * p.cols + pg];
+    if (page < 0 || page >= p.pages) {
+      page = 0;
+      flag(p.status, kDevBadIndex);
+    }
+    return (uint32_t)((page * p.hk + s.h) * p.P + of);
+  };
+  // Copies 16 keys from cache row `row` on into stage `slot`.
+  auto copy = [&](uint32_t row, int slot) {
+    Stage<D>& s = stages[slot];
+    constexpr int CPR = D / 32;  // 16-byte chunks of a code row
+    const uint64_t code_at = (uint64_t)row * (D / 2), scale_at = (uint64_t)row * (D / 16);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(t0 + warp + i * kWarps, i);
+    for (int c = lane; c < 16 * CPR; c += 32) {
+      const int tk = c / CPR, part = c % CPR;
+      // K row index of the token (the inverse of token = 4 (r & 1) + r / 2 + 8 (r / 8))
+      const int kr = 2 * (tk & 3) + ((tk >> 2) & 1) + 8 * (tk >> 3);
+      cp_async16(s.k + kr * (D / 2) + part * 16, p.kc + code_at + c * 16);
+      // V chunks swapped so that lanes (g, t) read 4 tokens without bank conflicts
+      const int vp = D == 128 ? part ^ (((tk >> 1) & 1) << 1) : part;
+      cp_async16(s.v + tk * (D / 2) + vp * 16, p.vc + code_at + c * 16);
+    }
+    if (lane < D / 16) {
+      cp_async16(s.ks + lane * 16, p.ks + scale_at + lane * 16);
+    } else if (lane < D / 8) {
+      const int c = lane - D / 16;
+      cp_async16(s.vs + c * 16, p.vs + scale_at + c * 16);
+    }
+  };
+  // The first copies of a segment.
+  auto begin = [&](const Segment& s, uint32_t rows) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      const uint32_t row = __shfl_sync(kAll, rows, i);
+      if (s.t0 + warp + i * kWarps < s.t1) copy(row, i);
+      cp_async_commit();
+    }
+  };
+
+  uint32_t rows = look_up(seg, seg.t0 + warp);
+  begin(seg, rows);
+  bool have = true;
+  while (have) {
+    // the segment after this one: its rows are looked up now, its first copies run
+    // while this one's results are joined
+    const Request r = seg.r;
+    const int h = seg.h, t0 = seg.t0, t1 = seg.t1;
+    const int64_t item_first = pos - (t1 - t0) - t0, item_last = item_first + r.tiles - 1;
+    const int nrows = r.n * p.G;
+    Segment cur = seg;
+    have = next(seg);
+    uint32_t next_rows = have ? look_up(seg, seg.t0 + warp) : 0;
 
     // ---- query rows ---------------------------------------------------------
-    // column n of row tile nt is row row0 + 8 nt + n = (token, head of the group)
+    // column n of row tile nt is row 8 nt + n = (token, head of the group)
     uint32_t qb[NT][KS][2];
     float fac[NT][2];     // scores to powers of two, for columns 2t and 2t + 1
     int lim[NT][2];       // keys below this are seen
@@ -210,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       const int row = nt * 8 + g;
       uint4 raw[DQ / 8];
       if (row < nrows) {
-        const int tk = (row0 + row) / p.G, hh = (row0 + row) - tk * p.G;
+        const int tk = (int)fastdiv((uint32_t)row, p.by_group), hh = row - tk * p.G;
         const uint16_t* src = p.q + (r.q0 + tk) * p.q_st + (int64_t)(h * p.G + hh) * D + t * DQ;
 #pragma unroll
         for (int i = 0; i < DQ / 8; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -238,13 +294,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       for (int i = 0; i < 2; ++i) {
         fac[nt][i] = __shfl_sync(kAll, f, (2 * t + i) * 4);
         const int rr = nt * 8 + 2 * t + i;
-        lim[nt][i] = rr < nrows ? r.len - r.n + (row0 + rr) / p.G + 1 : 0;
+        lim[nt][i] = rr < nrows ? r.len - r.n + (int)fastdiv((uint32_t)rr, p.by_group) + 1 : 0;
       }
     }
-    const int lim_min = r.len - r.n + row0 / p.G + 1;       // keys below are seen by every row
-    const int low_max = p.window > 0                        // and from here on
-                            ? r.len - r.n + (row0 + nrows - 1) / p.G + 1 - min(p.window, r.len)
-                            : 0;
+    const int lim_min = r.len - r.n + 1;  // keys below are seen by every row
+    const int low_max = p.window > 0 ? r.len - min(p.window, r.len) : 0;  // and from here on
     float o[NT][KS][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -258,8 +312,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     }
 
     // ---- tiles --------------------------------------------------------------
+    int slot = 0, ahead = kStages - 1;  // ahead: this warp's tiles copied so far
+    uint32_t more_rows = look_up(cur, t0 + warp + 32 * kWarps);  // its tiles 32 .. 63
     for (int j = t0 + warp; j < t1; j += kWarps) {
-      issue(j + (kStages - 1) * kWarps, (slot + kStages - 1) % kStages);
+      {
+        const uint32_t row = __shfl_sync(kAll, rows, ahead & 31);
+        if (j + (kStages - 1) * kWarps < t1) copy(row, (slot + kStages - 1) % kStages);
+        cp_async_commit();
+        if ((++ahead & 31) == 0) {
+          rows = more_rows;
+          more_rows = look_up(cur, t0 + warp + (ahead + 32) * kWarps);
+        }
+      }
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const Stage<D>& s = stages[slot];
@@ -395,6 +459,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       slot = (slot + 1) % kStages;
     }
     cp_async_wait<0>();
+    __syncwarp();
+    rows = next_rows;
+    if (have) begin(seg, rows);
 
     // ---- join the warps ------------------------------------------------------
 #pragma unroll
@@ -409,31 +476,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
           s_m[warp][nt * 8 + 2 * t + i] = m[nt][i];
           s_l[warp][nt * 8 + 2 * t + i] = v;
         }
-      }
-    __syncthreads();  // the sums are there, and every warp is done with its stages
+        float* dst = s_o + (warp * kRows + nt * 8 + 2 * t + i) * kJoinRow<D>;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = nt * 8 + 2 * t + i;
-        float mx = s_m[0][rr];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][rr]);
-        const float a = m[nt][i] == __int_as_float(0xFF800000) ? 0.0f : ex2(m[nt][i] - mx);
-        float* dst = s_o + (warp * kRows + rr) * D;
-#pragma unroll
-        for (int c = 0; c < KS; ++c)
-          *reinterpret_cast<float2*>(dst + g * (D / 8) + 2 * c) =
-              make_float2(o[nt][c][i] * a, o[nt][c][i + 2] * a);
+        for (int c = 0; c < KS; c += 2)
+          *reinterpret_cast<float4*>(dst + join_at<D>(g * (D / 32) + c / 2)) =
+              make_float4(o[nt][c][i], o[nt][c][i + 2], o[nt][c + 1][i], o[nt][c + 1][i + 2]);
       }
     __syncthreads();
-    const int64_t item_first = pos - t0, item_last = item_first + r.tiles - 1;
-    const int64_t c0 = item_first / run, c1 = item_last / run;  // CTAs of the item
+    const int c0 = (int)(item_first / run), c1 = (int)(item_last / run);  // CTAs of the item
     const bool whole = c0 == c1;
-    float* rec = p.part + ((int64_t)blockIdx.x * 2 + (blockIdx.x == c0 ? 1 : 0)) * kAttnRecord;
+    auto record = [&](int c) { return p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * kAttnRecord; };
     auto finish = [&](int rr, int d, float4 v, float mx, float sum) {
       // the row's final result
-      const int tk = (row0 + rr) / p.G, hh = (row0 + rr) - tk * p.G;
+      const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
       const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + h * p.G + hh;
       const float f = sum == 0.0f ? 0.0f : vss.g / sum;
       reinterpret_cast<uint2*>(p.out)[orow * (D / 4) + d / 4] =
@@ -442,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         p.lse[orow] = sum == 0.0f ? __int_as_float(0xFF800000) : (mx - kBias + log2f(sum)) * kLn2;
     };
     for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-      const int rr = i / (D / 4), d = (i % (D / 4)) * 4;
+      const int rr = i / (D / 4), q = i % (D / 4);
       float mx = s_m[0][rr];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][rr]);
@@ -451,15 +506,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = s_m[w][rr];
-        sum += mw == __int_as_float(0xFF800000) ? 0.0f : s_l[w][rr] * ex2(mw - mx);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kRows + rr) * D + d);
-        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        const float a = mw == __int_as_float(0xFF800000) ? 0.0f : ex2(mw - mx);
+        sum = __fmaf_rn(s_l[w][rr], a, sum);
+        const float4 x =
+            *reinterpret_cast<const float4*>(s_o + (w * kRows + rr) * kJoinRow<D> + join_at<D>(q));
+        v.x = __fmaf_rn(x.x, a, v.x), v.y = __fmaf_rn(x.y, a, v.y);
+        v.z = __fmaf_rn(x.z, a, v.z), v.w = __fmaf_rn(x.w, a, v.w);
       }
       if (whole) {
-        finish(rr, d, v, mx, sum);
+        finish(rr, 4 * q, v, mx, sum);
       } else {
-        *reinterpret_cast<float4*>(rec + rr * D + d) = v;
-        if (d == 0) {
+        float* rec = record(blockIdx.x);
+        *reinterpret_cast<float4*>(rec + rr * D + 4 * q) = v;
+        if (q == 0) {
           rec[kAttnRows * 128 + rr] = mx;
           rec[kAttnRows * 129 + rr] = sum;
         }
@@ -475,37 +534,52 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       if (s_ticket == (uint32_t)(c1 - c0)) {
         __threadfence();
         for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-          const int rr = i / (D / 4), d = (i % (D / 4)) * 4;
+          const int rr = i / (D / 4), q = i % (D / 4);
           float mx = __int_as_float(0xFF800000), sum = 0.0f;
           float4 v = make_float4(0, 0, 0, 0);
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* q = p.part + (c * 2 + (c == c0 ? 1 : 0)) * kAttnRecord;
-            const float mc = __ldcg(q + kAttnRows * 128 + rr), lc = __ldcg(q + kAttnRows * 129 + rr);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + rr * D + d));
-            if (mc == __int_as_float(0xFF800000)) continue;
-            const float mn = fmaxf(mx, mc);
-            const float a = ex2(mx - mn), e = ex2(mc - mn);
-            sum = sum * a + lc * e;
-            v.x = v.x * a + x.x * e, v.y = v.y * a + x.y * e;
-            v.z = v.z * a + x.z * e, v.w = v.w * a + x.w * e;
+          for (int c = c0; c <= c1; c += 8) {  // 8 records in flight, joined in order
+            float mc[8], lc[8];
+            float4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const float* rec = record(min(c + u, c1));
+              mc[u] = __ldcg(rec + kAttnRows * 128 + rr);
+              lc[u] = __ldcg(rec + kAttnRows * 129 + rr);
+              x[u] = __ldcg(reinterpret_cast<const float4*>(rec + rr * D + 4 * q));
+              if (c + u > c1) mc[u] = __int_as_float(0xFF800000);
+            }
+            float mn = mx;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) mn = fmaxf(mn, mc[u]);
+            if (mn == __int_as_float(0xFF800000)) continue;
+            const float a = ex2(mx - mn);
+            sum *= a;
+            v.x *= a, v.y *= a, v.z *= a, v.w *= a;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if (mc[u] == __int_as_float(0xFF800000)) continue;
+              const float e = ex2(mc[u] - mn);
+              sum = __fmaf_rn(lc[u], e, sum);
+              v.x = __fmaf_rn(x[u].x, e, v.x), v.y = __fmaf_rn(x[u].y, e, v.y);
+              v.z = __fmaf_rn(x[u].z, e, v.z), v.w = __fmaf_rn(x[u].w, e, v.w);
+            }
             mx = mn;
           }
-          finish(rr, d, v, mx, sum);
+          finish(rr, 4 * q, v, mx, sum);
         }
         if (tid == 0) p.tickets[c0] = 0;
       }
     }
-    __syncthreads();  // the stages are free again
-    pos += t1 - t0;
-    off += t1 - t0;
+    __syncthreads();  // the joined outputs have been read
   }
 }
 
 template <int D, int NT>
 cudaError_t launch_t(const KvAttnParams& p, cudaStream_t st) {
-  constexpr size_t stages = sizeof(Stage<D>) * 5 * kWarps, join = (size_t)kWarps * 8 * NT * D * 4;
-  constexpr size_t smem = stages > join ? stages : join;
-  static_assert(smem + 1024 <= 48 * 1024, "fits the default shared memory limit");
+  constexpr size_t smem = Layout<D, NT>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(
+      kv_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   static const int per_sm = resident_ctas(kv_attn_kernel<D, NT>, kThreads, smem);
   const int ctas = std::min(sm_count() * per_sm, kAttnMaxCtas);
   return launch_pdl_smem(kv_attn_kernel<D, NT>, dim3(ctas), dim3(kThreads), smem, st, p, ctas);
