@@ -37,6 +37,8 @@
 // 8x8 transpose between lanes. Two V bytes of neighbouring tokens are merged
 // to (even nibbles) and (odd nibbles) before conversion, so that a converted
 // pair holds one dimension of two tokens, as the operand wants.
+#include <cstddef>
+
 #include "kv_attn.cuh"
 
 namespace nvfp4 {
@@ -57,6 +59,11 @@ template <int D>
 struct Stage {
   uint8_t k[16 * D / 2], v[16 * D / 2], ks[16 * D / 16], vs[16 * D / 16];
 };
+
+// 16 bytes from global to shared memory, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 // Padded row of the joined outputs (floats), and where the four values at
 // float4 index q of a row lie in it: the writing lanes (g, t) then hit all banks.
@@ -207,27 +214,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     }
     return (uint32_t)((page * p.hk + s.h) * p.P + of);
   };
-  // Copies 16 keys from cache row `row` on into stage `slot`.
+  // Copies 16 keys from cache row `row` on into stage `slot`: 16-byte chunks lane
+  // and lane + 32 (D = 128) of the tile's K and V codes, one chunk of the scales.
+  // What depends on the lane alone is worked out here, once.
+  constexpr int CPR = D / 32;  // 16-byte chunks of a code row
+  const int ctk = lane / CPR, cpart = lane % CPR;
+  // K row index of the token (the inverse of token = 4 (r & 1) + r / 2 + 8 (r / 8))
+  const int ckr = 2 * (ctk & 3) + ((ctk >> 2) & 1) + 8 * (ctk >> 3);
+  // V chunks swapped so that lanes (g, t) read 4 tokens without bank conflicts
+  const int cvp = D == 128 ? cpart ^ (((ctk >> 1) & 1) << 1) : cpart;
+  const uint32_t stage0 = (uint32_t)__cvta_generic_to_shared(stages);
+  const uint32_t k_dst = stage0 + ckr * (D / 2) + cpart * 16;
+  const uint32_t v_dst = stage0 + offsetof(Stage<D>, v) + ctk * (D / 2) + cvp * 16;
+  const uint32_t sc_dst = stage0 + offsetof(Stage<D>, ks) + lane * 16;  // ks, vs are neighbours
+  const uint8_t* k_src = p.kc + lane * 16;
+  const uint8_t* v_src = p.vc + lane * 16;
+  const uint8_t* sc_src = lane < D / 16 ? p.ks + lane * 16 : p.vs + (lane - D / 16) * 16;
   auto copy = [&](uint32_t row, int slot) {
-    Stage<D>& s = stages[slot];
-    constexpr int CPR = D / 32;  // 16-byte chunks of a code row
-    const uint64_t code_at = (uint64_t)row * (D / 2), scale_at = (uint64_t)row * (D / 16);
-#pragma unroll
-    for (int c = lane; c < 16 * CPR; c += 32) {
-      const int tk = c / CPR, part = c % CPR;
-      // K row index of the token (the inverse of token = 4 (r & 1) + r / 2 + 8 (r / 8))
-      const int kr = 2 * (tk & 3) + ((tk >> 2) & 1) + 8 * (tk >> 3);
-      cp_async16(s.k + kr * (D / 2) + part * 16, p.kc + code_at + c * 16);
-      // V chunks swapped so that lanes (g, t) read 4 tokens without bank conflicts
-      const int vp = D == 128 ? part ^ (((tk >> 1) & 1) << 1) : part;
-      cp_async16(s.v + tk * (D / 2) + vp * 16, p.vc + code_at + c * 16);
+    const uint32_t at = slot * (uint32_t)sizeof(Stage<D>);
+    const uint8_t* ks = k_src + (uint64_t)row * (D / 2);
+    const uint8_t* vs = v_src + (uint64_t)row * (D / 2);
+    copy16(k_dst + at, ks);
+    copy16(v_dst + at, vs);
+    if constexpr (D == 128) {  // the tile's second 8 tokens: 8 rows on in both places
+      copy16(k_dst + at + 512, ks + 512);
+      copy16(v_dst + at + 512, vs + 512);
     }
-    if (lane < D / 16) {
-      cp_async16(s.ks + lane * 16, p.ks + scale_at + lane * 16);
-    } else if (lane < D / 8) {
-      const int c = lane - D / 16;
-      cp_async16(s.vs + c * 16, p.vs + scale_at + c * 16);
-    }
+    if (lane < D / 8) copy16(sc_dst + at, sc_src + (uint64_t)row * (D / 16));
   };
   // The first copies of a segment.
   auto begin = [&](const Segment& s, uint32_t rows) {
@@ -282,8 +295,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
       // 2^(13 - e) for a row whose largest element lies in [2^e, 2^(e+1))
       const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float f = p.scale * kLog2e * kss.g * __uint_as_float((uint32_t)(127 - e) << 23);
+      float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      float f = p.scale * kLog2e * kss.g * __uint_as_float((uint32_t)(127 - e) << 23);
+      if (f < 0.0f) f = -f, up = -up;  // maxima are taken before the factor: f > 0
+      f = fmaxf(f, 1.17549435e-38f);
       const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
 #pragma unroll
       for (int j = 0; j < KS; ++j)
@@ -301,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     const int low_max = p.window > 0 ? r.len - min(p.window, r.len) : 0;  // and from here on
     float o[NT][KS][4];
     float m[NT][2], l[NT][2];
+    float sub[NT][2], above[NT][2];  // bias - m; the score above which m is raised
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -308,7 +324,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[nt][i] = __int_as_float(0xFF800000), l[nt][i] = 0.0f;
+      for (int i = 0; i < 2; ++i) {
+        m[nt][i] = above[nt][i] = __int_as_float(0xFF800000);
+        l[nt][i] = sub[nt][i] = 0.0f;
+      }
     }
 
     // ---- tiles --------------------------------------------------------------
@@ -369,20 +388,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
           }
         }
       }
+      if (edge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int key = tok + tg + 8 * (c >> 1), hi = lim[nt][c & 1];
+            const bool seen = key < hi && (p.window == 0 || key >= hi - min(p.window, r.len));
+            sc[nt][c] = seen ? sc[nt][c] : __int_as_float(0xFF800000);
+          }
+      }
       bool raise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x = sc[nt][c] * fac[nt][c & 1];
-          if (edge) {
-            const int key = tok + tg + 8 * (c >> 1), hi = lim[nt][c & 1];
-            const bool seen = key < hi && (p.window == 0 || key >= hi - min(p.window, r.len));
-            x = seen ? x : __int_as_float(0xFF800000);
-          }
-          sc[nt][c] = x;
-          raise |= x > m[nt][c & 1] + kSlack;
-        }
+        for (int i = 0; i < 2; ++i) raise |= fmaxf(sc[nt][i], sc[nt][i + 2]) > above[nt][i];
       if (__any_sync(kAll, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -391,11 +411,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
             float x = fmaxf(sc[nt][i], sc[nt][i + 2]);
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 16)) * fac[nt][i];
             const float mn = fmaxf(m[nt][i], x);
             // 0 for a row that has seen nothing yet (its sums are 0)
             const float a = m[nt][i] == __int_as_float(0xFF800000) ? 0.0f : ex2(m[nt][i] - mn);
             m[nt][i] = mn;
+            if (mn != __int_as_float(0xFF800000)) {
+              sub[nt][i] = kBias - mn;
+              above[nt][i] = (mn + kSlack) / fac[nt][i];
+            }
             l[nt][i] *= a;
 #pragma unroll
             for (int d = 0; d < KS; ++d) o[nt][d][i] *= a, o[nt][d][i + 2] *= a;
@@ -406,11 +430,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       for (int nt = 0; nt < NT; ++nt) {
         float e[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float mm = m[nt][c & 1];
-          e[c] = ex2(sc[nt][c] - (mm == __int_as_float(0xFF800000) ? 0.0f : mm - kBias));
-          l[nt][c & 1] += e[c];
-        }
+        for (int c = 0; c < 4; ++c)
+          e[c] = ex2(__fmaf_rn(sc[nt][c], fac[nt][c & 1], sub[nt][c & 1]));
+        const f2 two = __fadd2_rn(make_float2(e[0], e[1]), make_float2(e[2], e[3]));
+        l[nt][0] += two.x;
+        l[nt][1] += two.y;
         pb[nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
         pb[nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
       }
