@@ -65,6 +65,33 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
 // Padded row of the joined outputs (floats), and where the four values at
 // float4 index q of a row lie in it: the writing lanes (g, t) then hit all banks.
 template <int D>
@@ -94,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   constexpr int kRows = 8 * NT;  // query rows of an item at most
   constexpr int KS = D / 16;     // k steps of q K^T, and 16-row tiles of V^T
   constexpr int DQ = D / 4;      // dimensions of K per lane
+  constexpr uint32_t kStageBytes = sizeof(Stage<D>);
   extern __shared__ __align__(16) uint8_t smem[];
   Stage<D>* stages = reinterpret_cast<Stage<D>*>(smem) + (threadIdx.x >> 5) * kStages;
   float* s_o = reinterpret_cast<float*>(smem + Layout<D, NT>::kStage);  // [kWarps][kRows][row]
@@ -214,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     }
     return (uint32_t)((page * p.hk + s.h) * p.P + of);
   };
-  // Copies 16 keys from cache row `row` on into stage `slot`: 16-byte chunks lane
+  // Copies 16 keys from cache row `row` on into a stage: 16-byte chunks lane
   // and lane + 32 (D = 128) of the tile's K and V codes, one chunk of the scales.
   // What depends on the lane alone is worked out here, once.
   constexpr int CPR = D / 32;  // 16-byte chunks of a code row
@@ -230,8 +258,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   const uint8_t* k_src = p.kc + lane * 16;
   const uint8_t* v_src = p.vc + lane * 16;
   const uint8_t* sc_src = lane < D / 16 ? p.ks + lane * 16 : p.vs + (lane - D / 16) * 16;
-  auto copy = [&](uint32_t row, int slot) {
-    const uint32_t at = slot * (uint32_t)sizeof(Stage<D>);
+  auto copy = [&](uint32_t row, uint32_t at) {  // at: the stage's offset
     const uint8_t* ks = k_src + (uint64_t)row * (D / 2);
     const uint8_t* vs = v_src + (uint64_t)row * (D / 2);
     copy16(k_dst + at, ks);
@@ -242,12 +269,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     }
     if (lane < D / 8) copy16(sc_dst + at, sc_src + (uint64_t)row * (D / 16));
   };
+  // Where this lane reads a stage: K rows g and g + 8 with their scales, the V
+  // bytes and scales of tokens t, 4 + t, 8 + t, 12 + t.
+  const int tg = (g >> 1) + 4 * (g & 1);  // token of K row g; row g + 8: token tg + 8
+  const uint32_t k_ld = stage0 + g * (D / 2) + t * (DQ / 2);
+  const uint32_t ks_ld = stage0 + offsetof(Stage<D>, ks) + tg * (D / 16) + t * (D / 64);
+  const uint32_t v_ld =
+      stage0 + offsetof(Stage<D>, v) + t * (D / 2) +
+      (D == 128 ? ((g >> 1) ^ (((t >> 1) & 1) << 1)) * 16 + (g & 1) * 8 : g * 4);
+  const uint32_t vs_ld =
+      stage0 + offsetof(Stage<D>, vs) + t * (D / 16) + (D == 128 ? g : g >> 1);
   // The first copies of a segment.
   auto begin = [&](const Segment& s, uint32_t rows) {
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
       const uint32_t row = __shfl_sync(kAll, rows, i);
-      if (s.t0 + warp + i * kWarps < s.t1) copy(row, i);
+      if (s.t0 + warp + i * kWarps < s.t1) copy(row, i * kStageBytes);
       cp_async_commit();
     }
   };
@@ -331,22 +368,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     }
 
     // ---- tiles --------------------------------------------------------------
-    int slot = 0, ahead = kStages - 1;  // ahead: this warp's tiles copied so far
+    uint32_t at = 0, fill = (kStages - 1) * kStageBytes;  // stages read and filled now
+    int ahead = kStages - 1;                              // this warp's tiles copied so far
     uint32_t more_rows = look_up(cur, t0 + warp + 32 * kWarps);  // its tiles 32 .. 63
-    for (int j = t0 + warp; j < t1; j += kWarps) {
-      {
-        const uint32_t row = __shfl_sync(kAll, rows, ahead & 31);
-        if (j + (kStages - 1) * kWarps < t1) copy(row, (slot + kStages - 1) % kStages);
-        cp_async_commit();
-        if ((++ahead & 31) == 0) {
-          rows = more_rows;
-          more_rows = look_up(cur, t0 + warp + (ahead + 32) * kWarps);
-        }
+    int tok = r.lo16 + (t0 + warp) * 16;
+    const int tok_end = r.lo16 + t1 * 16, tok_fill = tok_end - (kStages - 1) * kWarps * 16;
+    for (; tok < tok_end; tok += kWarps * 16) {
+      const uint32_t row = __shfl_sync(kAll, rows, ahead & 31);
+      if (tok < tok_fill) copy(row, fill);
+      cp_async_commit();
+      fill = at;  // the next one to fill is the one read now
+      if ((++ahead & 31) == 0) {
+        rows = more_rows;
+        more_rows = look_up(cur, t0 + warp + (ahead + 32) * kWarps);
       }
       cp_async_wait<kStages - 1>();
       __syncwarp();
-      const Stage<D>& s = stages[slot];
-      const int tok = r.lo16 + j * 16;
       const bool edge = tok + 16 > lim_min || tok < low_max;
 
       // scores: S^T[token][row]
@@ -355,22 +392,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) sc[nt][c] = 0.0f;
-      const int tg = (g >> 1) + 4 * (g & 1);  // token of K row g; row g + 8: token tg + 8
       {
-        uint32_t ka[DQ / 8], kb[DQ / 8];
-        const uint8_t* k0 = s.k + g * (D / 2) + t * (DQ / 2);
-#pragma unroll
-        for (int i = 0; i < DQ / 8; ++i) {
-          ka[i] = reinterpret_cast<const uint32_t*>(k0)[i];
-          kb[i] = reinterpret_cast<const uint32_t*>(k0 + 8 * (D / 2))[i];
-        }
-        uint32_t sa, sb;  // block scales of the two rows as f16x2 (D = 128: two blocks)
+        uint32_t ka[DQ / 8], kb[DQ / 8], sa, sb;
         if constexpr (D == 128) {
-          sa = scales2(reinterpret_cast<const uint16_t*>(s.ks)[tg * 4 + t]);
-          sb = scales2(reinterpret_cast<const uint16_t*>(s.ks)[(tg + 8) * 4 + t]);
+          const uint4 a = lds128(k_ld + at), b = lds128(k_ld + at + 8 * (D / 2));
+          ka[0] = a.x, ka[1] = a.y, ka[DQ / 8 - 2] = a.z, ka[DQ / 8 - 1] = a.w;
+          kb[0] = b.x, kb[1] = b.y, kb[DQ / 8 - 2] = b.z, kb[DQ / 8 - 1] = b.w;
+          // block scales of the two rows as f16x2: two blocks
+          sa = scales2(lds16(ks_ld + at));
+          sb = scales2(lds16(ks_ld + at + 8 * (D / 16)));
         } else {
-          sa = scales2(s.ks[tg * 4 + t]);
-          sb = scales2(s.ks[(tg + 8) * 4 + t]);
+          const uint2 a = lds64(k_ld + at), b = lds64(k_ld + at + 8 * (D / 2));
+          ka[0] = a.x, ka[1] = a.y, kb[0] = b.x, kb[1] = b.y;
+          sa = scales2(lds8(ks_ld + at));
+          sb = scales2(lds8(ks_ld + at + 8 * (D / 16)));
         }
 #pragma unroll
         for (int i = 0; i < DQ / 8; ++i) {
@@ -444,20 +479,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         uint32_t vw[4][VW], vb[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int tk = 4 * i + t;
           if constexpr (D == 128) {
-            const int chunk = (g >> 1) ^ (((tk >> 1) & 1) << 1);
-            const uint2 w = *reinterpret_cast<const uint2*>(s.v + tk * 64 + chunk * 16 + (g & 1) * 8);
+            const uint2 w = lds64(v_ld + at + 4 * i * (D / 2));
             vw[i][0] = w.x, vw[i][VW - 1] = w.y;
-            vb[i] = s.vs[tk * 8 + g];
           } else {
-            vw[i][0] = *reinterpret_cast<const uint32_t*>(s.v + tk * 32 + g * 4);
-            vb[i] = s.vs[tk * 4 + (g >> 1)];
+            vw[i][0] = lds32(v_ld + at + 4 * i * (D / 2));
           }
-          // bytes past the request may hold anything, a NaN scale included
-          if (edge && tok + tk >= r.len) vb[i] = 0;
+          vb[i] = lds8(vs_ld + at + 4 * i * (D / 16));
         }
-        const uint32_t f01 = scales2(vb[0] | (vb[1] << 8)), f23 = scales2(vb[2] | (vb[3] << 8));
+        if (edge) {  // bytes past the request may hold anything, a NaN scale included
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (tok + 4 * i + t >= r.len) vb[i] = 0;
+        }
+        const uint32_t f01 = scales2(__byte_perm(vb[0], vb[1], 0x0040));
+        const uint32_t f23 = scales2(__byte_perm(vb[2], vb[3], 0x0040));
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           const uint32_t e01 = (vw[0][w] & 0x0F0F0F0Fu) | ((vw[1][w] << 4) & 0xF0F0F0F0u);
@@ -480,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         }
       }
       __syncwarp();  // every lane has read the slot before it is filled again
-      slot = (slot + 1) % kStages;
+      at = at == (kStages - 1) * kStageBytes ? 0 : at + kStageBytes;
     }
     cp_async_wait<0>();
     __syncwarp();
