@@ -2,6 +2,8 @@
 // operators (api_kv.cu) and their kernels. Not installed; the public interface
 // is nvfp4.h.
 #pragma once
+#include <atomic>
+
 #include "launch.h"
 
 namespace nvfp4 {
@@ -25,6 +27,20 @@ cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
   lc.attrs = at;
   lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, kernel, static_cast<Args&&>(args)...);
+}
+
+// Lets `kernel` use `smem` bytes of dynamic shared memory on the current device;
+// `ready` keeps a bit per device, so that only a device's first call sets it.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t smem, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Block tables and slot maps.

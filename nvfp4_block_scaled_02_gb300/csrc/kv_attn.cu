@@ -114,8 +114,73 @@ struct Segment {
   int b, h, t0, t1;
 };
 
+// Record of CTA c's part of an item that begins in CTA c0.
+__device__ __forceinline__ float* record(const KvAttnParams& p, int c, int c0) {
+  return p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * kAttnRecord;
+}
+// A row's final result: values d .. d + 3 of row rr (token, head of the group).
+template <int D>
+__device__ __forceinline__ void finish(const KvAttnParams& p, int q0, int h, int rr, int d,
+                                       float4 v, float mx, float sum, float vg) {
+  const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
+  const int64_t orow = (int64_t)(q0 + tk) * p.hq + h * p.G + hh;
+  const float f = sum == 0.0f ? 0.0f : vg / sum;
+  reinterpret_cast<uint2*>(p.out)[orow * (D / 4) + d / 4] =
+      make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+  if (p.lse && d == 0)
+    p.lse[orow] = sum == 0.0f ? __int_as_float(0xFF800000) : (mx - kBias + log2f(sum)) * kLn2;
+}
+// Joins the records of CTAs c0 .. c1 in order, 8 in flight. (16 would take 5 us off
+// one request of 32768 tokens, but their registers cost the tile loop 4%, inlined
+// or not.)
+template <int D>
+__device__ __noinline__ void join_records(const KvAttnParams& p, int q0, int h, int nrows, int c0,
+                                          int c1, float vg) {
+  constexpr int U = 8;
+  for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
+    const int rr = i / (D / 4), q = i % (D / 4);
+    float mx = __int_as_float(0xFF800000), sum = 0.0f;
+    float4 v = make_float4(0, 0, 0, 0);
+    for (int c = c0; c <= c1; c += U) {
+      float mc[U], lc[U];
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* rec = record(p, min(c + u, c1), c0);
+        mc[u] = __ldcg(rec + kAttnRows * 128 + rr);
+        lc[u] = __ldcg(rec + kAttnRows * 129 + rr);
+        x[u] = __ldcg(reinterpret_cast<const float4*>(rec + rr * D + 4 * q));
+        if (c + u > c1) mc[u] = __int_as_float(0xFF800000);
+      }
+      float mn = mx;
+#pragma unroll
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, mc[u]);
+      if (mn == __int_as_float(0xFF800000)) continue;
+      const float a = ex2(mx - mn);
+      sum *= a;
+      v.x *= a, v.y *= a, v.z *= a, v.w *= a;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (mc[u] == __int_as_float(0xFF800000)) continue;
+        const float e = ex2(mc[u] - mn);
+        sum = __fmaf_rn(lc[u], e, sum);
+        v.x = __fmaf_rn(x[u].x, e, v.x), v.y = __fmaf_rn(x[u].y, e, v.y);
+        v.z = __fmaf_rn(x[u].z, e, v.z), v.w = __fmaf_rn(x[u].w, e, v.w);
+      }
+      mx = mn;
+    }
+    finish<D>(p, q0, h, rr, 4 * q, v, mx, sum, vg);
+  }
+}
+
+// CTAs resident per SM. Three leave 168 registers a thread and four 128: at D = 128
+// the loads and conversions of a tile overlap better with three (64 x 8192 tokens,
+// 8 KV heads: 112 us against 121), at D = 64 four are better (74 us against 78).
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+constexpr int kCtasPerSm = D == 64 && NT == 1 ? 4 : 3;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     kv_attn_kernel(const KvAttnParams p, const int ctas) {
   pdl_begin();
   constexpr int kRows = 8 * NT;  // query rows of an item at most
@@ -289,7 +354,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     }
   };
 
+  // The query rows of a segment's item as they are in memory (column n of row tile
+  // nt is row 8 nt + n = (token, head of the group)), and its heads' amax.
+  // Loaded an item ahead where the registers allow it: two row tiles would spill, and
+  // at D = 64 the fourth CTA is worth more (73 us against 77).
+  constexpr bool kAhead = NT == 1 && D == 128;
+  uint4 raw[NT][DQ / 8];
+  float k_amax = 0.0f, v_amax = 0.0f;
+  auto load_q = [&](const Segment& s) {
+    k_amax = p.k_amax[s.h];
+    v_amax = p.v_amax[s.h];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = nt * 8 + g;
+      const int tk = (int)fastdiv((uint32_t)row, p.by_group), hh = row - tk * p.G;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (s.r.q0 + tk) * p.q_st + (int64_t)(s.h * p.G + hh) * D + t * DQ);
+#pragma unroll
+      for (int i = 0; i < DQ / 8; ++i)
+        raw[nt][i] = row < s.r.n * p.G ? src[i] : make_uint4(0, 0, 0, 0);
+    }
+  };
+
   uint32_t rows = look_up(seg, seg.t0 + warp);
+  if (kAhead) load_q(seg);
   begin(seg, rows);
   bool have = true;
   while (have) {
@@ -297,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     // while this one's results are joined
     const Request r = seg.r;
     const int h = seg.h, t0 = seg.t0, t1 = seg.t1;
+    if (!kAhead) load_q(seg);
     const int64_t item_first = pos - (t1 - t0) - t0, item_last = item_first + r.tiles - 1;
     const int nrows = r.n * p.G;
     Segment cur = seg;
@@ -304,29 +393,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     uint32_t next_rows = have ? look_up(seg, seg.t0 + warp) : 0;
 
     // ---- query rows ---------------------------------------------------------
-    // column n of row tile nt is row 8 nt + n = (token, head of the group)
     uint32_t qb[NT][KS][2];
     float fac[NT][2];     // scores to powers of two, for columns 2t and 2t + 1
     int lim[NT][2];       // keys below this are seen
-    const SliceScale kss = slice_scale(p.k_amax[h], p.M);
-    const SliceScale vss = slice_scale(p.v_amax[h], p.M);
+    const SliceScale kss = slice_scale(k_amax, p.M), vss = slice_scale(v_amax, p.M);
     if ((kss.bad || vss.bad) && tid == 0) flag(p.status, NVFP4_DEV_BAD_AMAX_BIT);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = nt * 8 + g;
-      uint4 raw[DQ / 8];
-      if (row < nrows) {
-        const int tk = (int)fastdiv((uint32_t)row, p.by_group), hh = row - tk * p.G;
-        const uint16_t* src = p.q + (r.q0 + tk) * p.q_st + (int64_t)(h * p.G + hh) * D + t * DQ;
-#pragma unroll
-        for (int i = 0; i < DQ / 8; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < DQ / 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-      }
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < DQ / 8; ++i) m = max(m, absmax_bits4(raw[i]));
+      for (int i = 0; i < DQ / 8; ++i) m = max(m, absmax_bits4(raw[nt][i]));
       m = max(m, __shfl_xor_sync(kAll, m, 1));
       m = max(m, __shfl_xor_sync(kAll, m, 2));
       if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
@@ -336,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       float f = p.scale * kLog2e * kss.g * __uint_as_float((uint32_t)(127 - e) << 23);
       if (f < 0.0f) f = -f, up = -up;  // maxima are taken before the factor: f > 0
       f = fmaxf(f, 1.17549435e-38f);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw[nt]);
 #pragma unroll
       for (int j = 0; j < KS; ++j)
 #pragma unroll
@@ -349,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         lim[nt][i] = rr < nrows ? r.len - r.n + (int)fastdiv((uint32_t)rr, p.by_group) + 1 : 0;
       }
     }
+    if (kAhead && have) load_q(seg);  // the next item's
     const int lim_min = r.len - r.n + 1;  // keys below are seen by every row
     const int low_max = p.window > 0 ? r.len - min(p.window, r.len) : 0;  // and from here on
     float o[NT][KS][4];
@@ -545,17 +622,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     __syncthreads();
     const int c0 = (int)(item_first / run), c1 = (int)(item_last / run);  // CTAs of the item
     const bool whole = c0 == c1;
-    auto record = [&](int c) { return p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * kAttnRecord; };
-    auto finish = [&](int rr, int d, float4 v, float mx, float sum) {
-      // the row's final result
-      const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
-      const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + h * p.G + hh;
-      const float f = sum == 0.0f ? 0.0f : vss.g / sum;
-      reinterpret_cast<uint2*>(p.out)[orow * (D / 4) + d / 4] =
-          make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
-      if (p.lse && d == 0)
-        p.lse[orow] = sum == 0.0f ? __int_as_float(0xFF800000) : (mx - kBias + log2f(sum)) * kLn2;
-    };
     for (int i = tid; i < nrows * (D / 4); i += kThreads) {
       const int rr = i / (D / 4), q = i % (D / 4);
       float mx = s_m[0][rr];
@@ -574,9 +640,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         v.z = __fmaf_rn(x.z, a, v.z), v.w = __fmaf_rn(x.w, a, v.w);
       }
       if (whole) {
-        finish(rr, 4 * q, v, mx, sum);
+        finish<D>(p, r.q0, h, rr, 4 * q, v, mx, sum, vss.g);
       } else {
-        float* rec = record(blockIdx.x);
+        float* rec = record(p, blockIdx.x, c0);
         *reinterpret_cast<float4*>(rec + rr * D + 4 * q) = v;
         if (q == 0) {
           rec[kAttnRows * 128 + rr] = mx;
@@ -593,40 +659,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       __syncthreads();
       if (s_ticket == (uint32_t)(c1 - c0)) {
         __threadfence();
-        for (int i = tid; i < nrows * (D / 4); i += kThreads) {
-          const int rr = i / (D / 4), q = i % (D / 4);
-          float mx = __int_as_float(0xFF800000), sum = 0.0f;
-          float4 v = make_float4(0, 0, 0, 0);
-          for (int c = c0; c <= c1; c += 8) {  // 8 records in flight, joined in order
-            float mc[8], lc[8];
-            float4 x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const float* rec = record(min(c + u, c1));
-              mc[u] = __ldcg(rec + kAttnRows * 128 + rr);
-              lc[u] = __ldcg(rec + kAttnRows * 129 + rr);
-              x[u] = __ldcg(reinterpret_cast<const float4*>(rec + rr * D + 4 * q));
-              if (c + u > c1) mc[u] = __int_as_float(0xFF800000);
-            }
-            float mn = mx;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) mn = fmaxf(mn, mc[u]);
-            if (mn == __int_as_float(0xFF800000)) continue;
-            const float a = ex2(mx - mn);
-            sum *= a;
-            v.x *= a, v.y *= a, v.z *= a, v.w *= a;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              if (mc[u] == __int_as_float(0xFF800000)) continue;
-              const float e = ex2(mc[u] - mn);
-              sum = __fmaf_rn(lc[u], e, sum);
-              v.x = __fmaf_rn(x[u].x, e, v.x), v.y = __fmaf_rn(x[u].y, e, v.y);
-              v.z = __fmaf_rn(x[u].z, e, v.z), v.w = __fmaf_rn(x[u].w, e, v.w);
-            }
-            mx = mn;
-          }
-          finish(rr, 4 * q, v, mx, sum);
-        }
+        join_records<D>(p, r.q0, h, nrows, c0, c1, vss.g);
         if (tid == 0) p.tickets[c0] = 0;
       }
     }
@@ -637,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 template <int D, int NT>
 cudaError_t launch_t(const KvAttnParams& p, cudaStream_t st) {
   constexpr size_t smem = Layout<D, NT>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kv_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(kv_attn_kernel<D, NT>, smem, ready);
   if (e != cudaSuccess) return e;
   static const int per_sm = resident_ctas(kv_attn_kernel<D, NT>, kThreads, smem);
   const int ctas = std::min(sm_count() * per_sm, kAttnMaxCtas);

@@ -793,8 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 template <int D>
 cudaError_t launch_t(const KvAttnParams& p, cudaStream_t st) {
   constexpr size_t smem = Smem<D>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(kv_prefill_kernel<D>, smem, ready);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(sm_count(), kPrefillMaxCtas);
   return launch_pdl_smem(kv_prefill_kernel<D>, dim3(ctas), dim3(kThreads), smem, st, p, ctas);

@@ -217,20 +217,26 @@ def nvfp4_kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor,
            _typed(free_pages, "free_pages", (free_pages.numel(),), i32, dev), free_pages.numel(),
            tokens)
     if out is None:
-        out = {"seq_lens": torch.empty(B, dtype=i32, device=device),
-               "q_start": torch.empty(B + 1, dtype=i32, device=device),
-               "slots": torch.empty(tokens, dtype=torch.int64, device=device),
-               "positions": torch.empty(tokens, dtype=i32, device=device),
-               "pages_used": torch.empty(1, dtype=i32, device=device), "table": table}
+        empty = torch.empty
+        seq, start = empty(B, dtype=i32, device=device), empty(B + 1, dtype=i32, device=device)
+        slots = empty(tokens, dtype=torch.int64, device=device)
+        pos, used = empty(tokens, dtype=i32, device=device), empty(1, dtype=i32, device=device)
+        outs = (seq.data_ptr(), start.data_ptr(), slots.data_ptr(), pos.data_ptr(),
+                used.data_ptr())
+        out = {"table": table, "seq_lens": seq, "q_start": start, "slots": slots,
+               "positions": pos, "pages_used": used}
     else:
+        outs = (_typed(out["seq_lens"], "seq_lens", (B,), i32, dev),
+                _typed(out["q_start"], "q_start", (B + 1,), i32, dev),
+                _typed(out["slots"], "slots", (tokens,), torch.int64, dev),
+                _typed(out["positions"], "positions", (tokens,), i32, dev),
+                _typed(out["pages_used"], "pages_used", (1,), i32, dev))
         out = dict(out, table=table)
-    _check("nvfp4_kv_plan", _lib().nvfp4_kv_plan(
-        *ins, _typed(out["seq_lens"], "seq_lens", (B,), i32, dev),
-        _typed(out["q_start"], "q_start", (B + 1,), i32, dev),
-        _typed(out["slots"], "slots", (tokens,), torch.int64, dev),
-        _typed(out["positions"], "positions", (tokens,), i32, dev),
-        _typed(out["pages_used"], "pages_used", (1,), i32, dev),
-        _optional(status, "status", 1, _I32, dev), _stream(dev)))
+    status_code = _lib().nvfp4_kv_plan(
+        *ins, *outs, 0 if status is None else _optional(status, "status", 1, _I32, dev),
+        _stream(dev))
+    if status_code:
+        _check("nvfp4_kv_plan", status_code)
     return out
 
 
@@ -270,11 +276,19 @@ def nvfp4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor
     rq, rk = _rows(q, "q", T, hq, D, dev), _rows(k, "k", T, hk, D, dev)
     if q_out is None:
         q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+        ro = _Rows(q_out.data_ptr(), hq * D)
+    else:
+        ro = _rows(q_out, "q_out", T, hq, D, dev)
     if k_out is None:
         k_out = torch.empty((T, hk, D), dtype=k.dtype, device=q.device)
-    _check("nvfp4_qk_norm_rope", _lib().nvfp4_qk_norm_rope(
-        cfg, rq, rk, _rows(q_out, "q_out", T, hq, D, dev), _rows(k_out, "k_out", T, hk, D, dev),
-        _optional(status, "status", 1, _I32, dev), _stream(dev)))
+        ko = _Rows(k_out.data_ptr(), hk * D)
+    else:
+        ko = _rows(k_out, "k_out", T, hk, D, dev)
+    status_code = _lib().nvfp4_qk_norm_rope(
+        cfg, rq, rk, ro, ko, 0 if status is None else _optional(status, "status", 1, _I32, dev),
+        _stream(dev))
+    if status_code:
+        _check("nvfp4_qk_norm_rope", status_code)
     return {"q": q_out, "k": k_out}
 
 
@@ -381,13 +395,20 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: dict, table: torch.Tensor, seq_le
     rq = _rows(q, "q", T, hq, D, dev)
     if out is None:
         out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=device)
+        out_at = out.data_ptr()
+    else:
+        out_at = _optional(out, "out", T * hq * D, _BF16, dev)
     if lse is None:
         lse = torch.empty((T, hq), dtype=torch.float32, device=device)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _optional(lse, "lse", T * hq, (torch.float32,), dev)
     if workspace is None:
         workspace = kv_attention_workspace(device)
-    _check("nvfp4_kv_attention", _lib().nvfp4_kv_attention(
-        c, cfg, rq, _optional(out, "out", T * hq * D, _BF16, dev),
-        _optional(lse, "lse", T * hq, (torch.float32,), dev),
-        _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel(),
-        _optional(status, "status", 1, _I32, dev), _stream(dev)))
+    status_code = _lib().nvfp4_kv_attention(
+        c, cfg, rq, out_at, lse_at, _optional(workspace, "workspace", 1, _I32, dev),
+        4 * workspace.numel(), 0 if status is None else _optional(status, "status", 1, _I32, dev),
+        _stream(dev))
+    if status_code:
+        _check("nvfp4_kv_attention", status_code)
     return {"out": out, "lse": lse}
