@@ -6,12 +6,13 @@
 // Backward: u = the output's gradient rotated by the opposite angle; gw = sum
 // over rows of u x r; gx = r (w u - x r^2 mean(w u x)).
 //
-// A head lies in D/8 adjacent lanes (8 values, one 128-bit load each): the
-// mean is a butterfly over those lanes, and a pair (i, i + R/2) is exchanged
-// by one shuffle per value (R/16 lanes away). A warp takes several heads of
-// one token in a row, so that the token's cosines and sines stay in registers.
-// Both directions are bound by DRAM: 4 (forward) and 6 (backward) bytes per
-// value, with some 3 instructions per value between.
+// A head lies in D/8 adjacent lanes, 8 values each: the mean is a butterfly over
+// those lanes. With rotated halves a lane holds values 4l .. 4l + 3 and their
+// partners R/2 on (two 64-bit loads), with interleaved pairs 8 values in a row:
+// either way a pair never leaves its lane, four angles serve eight values, and the
+// rotation needs no shuffle. A warp takes several heads of one token in a row, so
+// that the token's angles stay in registers. Both directions are bound by DRAM: 4
+// (forward) and 6 (backward) bytes per value.
 #include "kv.h"
 
 namespace nvfp4 {
@@ -26,65 +27,60 @@ constexpr int kBatch = 4;  // steps whose loads are in flight together
 struct V8 {
   float v[8];
 };
-__device__ __forceinline__ V8 unpack(const uint4& w) {
-  return {{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), bf16_lo(w.z), bf16_hi(w.z),
-           bf16_lo(w.w), bf16_hi(w.w)}};
-}
-__device__ __forceinline__ uint4 pack(const V8& x) {
-  return make_uint4(pack_bf16x2(x.v[0], x.v[1]), pack_bf16x2(x.v[2], x.v[3]),
-                    pack_bf16x2(x.v[4], x.v[5]), pack_bf16x2(x.v[6], x.v[7]));
+__device__ __forceinline__ V8 unpack(const uint2& a, const uint2& b) {
+  return {{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(b.x), bf16_hi(b.x),
+           bf16_lo(b.y), bf16_hi(b.y)}};
 }
 
-// The cosines and sines of one lane's 8 values. Halves layout: value i and its
-// partner share angle i mod R/2; the sine is negated in the first half, so
-// that y = x c + partner s in both (and, with s negated, the inverse).
-// Interleaved: angle k of the pair (2k, 2k + 1) in c[k], s[k], k < 4.
-// A lane past the rotated part passes its values through (on = false).
+// Where a lane's two groups of four values lie in its head, and its angles.
+template <int LPH, bool IL>
+struct Lane {
+  static constexpr int kHeads = 32 / LPH;  // heads per warp step
+  int sub, d0, d1;
+  bool on;      // the lane's values are rotated
+  int angle;    // of its first pair
+  __device__ explicit Lane(int R) {
+    const int lane = threadIdx.x & 31, l = lane % LPH;
+    sub = lane / LPH;
+    on = 8 * l < R;
+    d0 = !IL && on ? 4 * l : 8 * l;
+    d1 = !IL && on ? 4 * l + R / 2 : 8 * l + 4;
+    angle = 4 * l;
+  }
+};
 template <bool IL>
 struct Angles {
-  float c[IL ? 4 : 8] = {}, s[IL ? 4 : 8] = {};
-  bool on;
-  __device__ __forceinline__ void load(const float* cs, int R, int d0) {
-    constexpr int N = IL ? 4 : 8;
-    on = d0 < R;
-    if (on) {
-      const bool first = d0 < R / 2;
-      const int i = IL ? d0 / 2 : (first ? d0 : d0 - R / 2);
-#pragma unroll
-      for (int j = 0; j < N; j += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(cs + i + j);
-        const float4 b = *reinterpret_cast<const float4*>(cs + R / 2 + i + j);
-        c[j] = a.x, c[j + 1] = a.y, c[j + 2] = a.z, c[j + 3] = a.w;
-        s[j] = b.x, s[j + 1] = b.y, s[j + 2] = b.z, s[j + 3] = b.w;
-      }
-      if (!IL && first)
-#pragma unroll
-        for (int j = 0; j < N; ++j) s[j] = -s[j];
+  float4 c, s;
+  template <int LPH>
+  __device__ __forceinline__ void load(const Lane<LPH, IL>& ln, const float* cs, int R) {
+    c = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (ln.on) {
+      c = *reinterpret_cast<const float4*>(cs + ln.angle);
+      s = *reinterpret_cast<const float4*>(cs + R / 2 + ln.angle);
     }
   }
-  __device__ __forceinline__ void negate() {
-#pragma unroll
-    for (int j = 0; j < (IL ? 4 : 8); ++j) s[j] = -s[j];
+  __device__ __forceinline__ void negate() { s = make_float4(-s.x, -s.y, -s.z, -s.w); }
+  static __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float x = a;
+    a = __fmaf_rn(-b, s, __fmul_rn(x, c));
+    b = __fmaf_rn(x, s, __fmul_rn(b, c));
   }
-  // Rotates the lane's values; `partner` is the lane holding the other members
-  // (halves layout). Every lane of the warp calls this.
-  __device__ __forceinline__ V8 rotate(const V8& x, int partner) const {
-    V8 y;
+  // Pairs (j, j + 4) of the lane, or (2j, 2j + 1). Values that are not rotated pass
+  // through: 1 x + 0 y is x unless y is infinite, so they are left alone.
+  __device__ __forceinline__ void rotate(V8& x, bool on) const {
+    if (!on) return;
     if constexpr (IL) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float a = x.v[2 * k], b = x.v[2 * k + 1];
-        y.v[2 * k] = __fmaf_rn(-b, s[k], __fmul_rn(a, c[k]));
-        y.v[2 * k + 1] = __fmaf_rn(a, s[k], __fmul_rn(b, c[k]));
-      }
+      turn(x.v[0], x.v[1], c.x, s.x);
+      turn(x.v[2], x.v[3], c.y, s.y);
+      turn(x.v[4], x.v[5], c.z, s.z);
+      turn(x.v[6], x.v[7], c.w, s.w);
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float o = __shfl_sync(kAll, x.v[j], partner);
-        y.v[j] = __fmaf_rn(o, s[j], __fmul_rn(x.v[j], c[j]));
-      }
+      turn(x.v[0], x.v[4], c.x, s.x);
+      turn(x.v[1], x.v[5], c.y, s.y);
+      turn(x.v[2], x.v[6], c.z, s.z);
+      turn(x.v[3], x.v[7], c.w, s.w);
     }
-    return on ? y : x;
   }
 };
 
@@ -95,29 +91,35 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float dot8(const V8& a, const V8& b) {
-  float e = 0.0f, o = 0.0f;
+  f2 e = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    e = __fmaf_rn(a.v[j], b.v[j], e);
-    o = __fmaf_rn(a.v[j + 1], b.v[j + 1], o);
-  }
-  return __fadd_rn(e, o);
+  for (int j = 0; j < 8; j += 2)
+    e = f2_fma(make_float2(a.v[j], a.v[j + 1]), make_float2(b.v[j], b.v[j + 1]), e);
+  return __fadd_rn(e.x, e.y);
 }
 
-// What a lane does for its head in every step of a warp.
-template <int LPH>
-struct Lane {
-  static constexpr int kHeads = 32 / LPH;  // heads per step
-  int sub, l, d0, partner;
-  __device__ explicit Lane(int R) {
-    const int lane = threadIdx.x & 31;
-    sub = lane / LPH;
-    l = lane % LPH;
-    d0 = 8 * l;
-    const int far = R / 16;
-    partner = d0 >= R ? lane : d0 < R / 2 ? lane + far : lane - far;
-  }
+// The values of one lane of a head as they are in memory.
+struct Raw {
+  uint2 a, b;
 };
+template <class L>
+__device__ __forceinline__ Raw load8(const uint16_t* head, const L& ln) {
+  return {*reinterpret_cast<const uint2*>(head + ln.d0),
+          *reinterpret_cast<const uint2*>(head + ln.d1)};
+}
+template <class L>
+__device__ __forceinline__ void store8(uint16_t* head, const L& ln, const V8& x) {
+  *reinterpret_cast<uint2*>(head + ln.d0) =
+      make_uint2(pack_bf16x2(x.v[0], x.v[1]), pack_bf16x2(x.v[2], x.v[3]));
+  *reinterpret_cast<uint2*>(head + ln.d1) =
+      make_uint2(pack_bf16x2(x.v[4], x.v[5]), pack_bf16x2(x.v[6], x.v[7]));
+}
+// A weight's values for this lane, or ones.
+template <class L>
+__device__ __forceinline__ Raw weight8(const uint4* w, const L& ln) {
+  if (!w) return {make_uint2(0x3F803F80u, 0x3F803F80u), make_uint2(0x3F803F80u, 0x3F803F80u)};
+  return load8(reinterpret_cast<const uint16_t*>(w), ln);
+}
 
 __device__ __forceinline__ int64_t position(const QkRopeParams& p, int64_t t) {
   const int64_t pos = p.pos[t];
@@ -126,51 +128,52 @@ __device__ __forceinline__ int64_t position(const QkRopeParams& p, int64_t t) {
   return 0;
 }
 
-// Warp task: `per` consecutive steps of one token.
+// Warp task: `per` consecutive steps of one token. The first loads go out before
+// the token's position (whose angles depend on it) is waited for.
 template <int LPH, bool IL>
 __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const QkRopeParams p, int steps,
                                                            int per, FastDiv by_tasks, int tasks) {
   pdl_begin();
-  using L = Lane<LPH>;
+  using L = Lane<LPH, IL>;
+  constexpr int D = 8 * LPH;
   const L ln(p.R);
   const int H = p.hq + p.hk;
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (w >= p.T * tasks) return;
   const int64_t t = w < 0xFFFFFFFFll ? (int64_t)fastdiv((uint32_t)w, by_tasks) : w / tasks;
   const int s0 = (int)(w - t * tasks) * per, s1 = min(s0 + per, steps);
+  const uint16_t *q = p.q + t * p.q_st, *k = p.k + t * p.k_st - (int64_t)p.hq * D;
+  uint16_t *qo = p.qo + t * p.qo_st, *ko = p.ko + t * p.ko_st - (int64_t)p.hq * D;
   Angles<IL> an;
-  an.load(p.cs + position(p, t) * p.R, p.R, ln.d0);
-  const V8 one = {{1, 1, 1, 1, 1, 1, 1, 1}};
-  const V8 wq = p.qw ? unpack(p.qw[ln.l]) : one, wk = p.kw ? unpack(p.kw[ln.l]) : one;
-  const int64_t q_in = t * p.q_st + ln.d0, k_in = t * p.k_st + ln.d0;
-  const int64_t q_out = t * p.qo_st + ln.d0, k_out = t * p.ko_st + ln.d0;
+  Raw wq, wk;
   for (int s = s0; s < s1; s += kBatch) {
-    uint4 raw[kBatch];
+    Raw raw[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int h = (s + b) * L::kHeads + ln.sub;
-      raw[b] = make_uint4(0, 0, 0, 0);
-      if (s + b < s1 && h < H)
-        raw[b] = *reinterpret_cast<const uint4*>(
-            h < p.hq ? p.q + q_in + h * (8 * LPH) : p.k + k_in + (h - p.hq) * (8 * LPH));
+      raw[b] = {make_uint2(0, 0), make_uint2(0, 0)};
+      if (s + b < s1 && h < H) raw[b] = load8((h < p.hq ? q : k) + h * D, ln);
+    }
+    if (s == s0) {
+      wq = weight8(p.qw, ln);
+      wk = weight8(p.kw, ln);
+      an.load(ln, p.cs + position(p, t) * p.R, p.R);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       if (s + b >= s1) break;
       const int h = (s + b) * L::kHeads + ln.sub;
       const bool is_q = h < p.hq;
-      V8 x = unpack(raw[b]);
+      V8 x = unpack(raw[b].a, raw[b].b);
       const float ss = head_sum<LPH>(dot8(x, x));
       if (is_q ? p.qw != nullptr : p.kw != nullptr) {
-        const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / (8 * LPH)), p.eps));
+        const float r = rsqrtf(__fmaf_rn(ss, 1.0f / D, p.eps));
+        const V8 wt = unpack(is_q ? wq.a : wk.a, is_q ? wq.b : wk.b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x.v[j] = __fmul_rn(__fmul_rn(x.v[j], r), is_q ? wq.v[j] : wk.v[j]);
+        for (int j = 0; j < 8; ++j) x.v[j] = __fmul_rn(__fmul_rn(x.v[j], r), wt.v[j]);
       }
-      const V8 y = an.rotate(x, ln.partner);
-      if (h < H)
-        *reinterpret_cast<uint4*>(is_q ? p.qo + q_out + h * (8 * LPH)
-                                       : p.ko + k_out + (h - p.hq) * (8 * LPH)) = pack(y);
+      an.rotate(x, ln.on);
+      if (h < H) store8((is_q ? qo : ko) + h * D, ln, x);
     }
   }
 }
@@ -180,67 +183,68 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const QkRopeParams p,
 // workspace, and the CTA that takes the last ticket adds the rows in order:
 // the sums do not depend on which CTA finishes when.
 template <int LPH, bool IL>
-__global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const QkRopeParams p, int steps,
-                                                               int per, FastDiv by_tasks,
-                                                               int tasks) {
+__global__ void __launch_bounds__(kThreads, 2) qk_rope_bwd_kernel(const QkRopeParams p, int steps,
+                                                                  int per, FastDiv by_tasks,
+                                                                  int tasks) {
   pdl_begin();
-  using L = Lane<LPH>;
+  using L = Lane<LPH, IL>;
   constexpr int D = 8 * LPH;
   const L ln(p.R);
   const int H = p.hq + p.hk;
   const int warp = threadIdx.x >> 5;
-  const V8 one = {{1, 1, 1, 1, 1, 1, 1, 1}};
-  const V8 wq = p.qw ? unpack(p.qw[ln.l]) : one, wk = p.kw ? unpack(p.kw[ln.l]) : one;
+  const Raw wq = weight8(p.qw, ln), wk = weight8(p.kw, ln);
   V8 aq = {}, ak = {};
   const int64_t total = p.T * tasks;
   for (int64_t w = (int64_t)blockIdx.x * kWarps + warp; w < total;
        w += (int64_t)gridDim.x * kWarps) {
     const int64_t t = total < 0xFFFFFFFFll ? (int64_t)fastdiv((uint32_t)w, by_tasks) : w / tasks;
     const int s0 = (int)(w - t * tasks) * per, s1 = min(s0 + per, steps);
+    const int64_t k0 = -(int64_t)p.hq * D;
+    const uint16_t *gq = p.gq + t * p.gq_st, *gk = p.gk + t * p.gk_st + k0;
+    const uint16_t *q = p.q + t * p.q_st, *k = p.k + t * p.k_st + k0;
+    uint16_t *qo = p.qo + t * p.qo_st, *ko = p.ko + t * p.ko_st + k0;
     Angles<IL> an;
-    an.load(p.cs + position(p, t) * p.R, p.R, ln.d0);
-    an.negate();
     for (int s = s0; s < s1; s += kBatch) {
-      uint4 rg[kBatch], rx[kBatch];
+      Raw rg[kBatch], rx[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const int h = (s + b) * L::kHeads + ln.sub;
-        const bool ok = s + b < s1 && h < H, is_q = h < p.hq;
-        const int64_t at = (is_q ? h : h - p.hq) * D + ln.d0;
-        rg[b] = rx[b] = make_uint4(0, 0, 0, 0);
-        if (ok) {
-          rg[b] = *reinterpret_cast<const uint4*>((is_q ? p.gq + t * p.gq_st : p.gk + t * p.gk_st) + at);
-          if (is_q ? p.qw != nullptr : p.kw != nullptr)
-            rx[b] = *reinterpret_cast<const uint4*>((is_q ? p.q + t * p.q_st : p.k + t * p.k_st) + at);
+        const bool is_q = h < p.hq;
+        rg[b] = rx[b] = {make_uint2(0, 0), make_uint2(0, 0)};
+        if (s + b < s1 && h < H) {
+          rg[b] = load8((is_q ? gq : gk) + h * D, ln);
+          if (is_q ? p.qw != nullptr : p.kw != nullptr) rx[b] = load8((is_q ? q : k) + h * D, ln);
         }
+      }
+      if (s == s0) {
+        an.load(ln, p.cs + position(p, t) * p.R, p.R);
+        an.negate();
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         if (s + b >= s1) break;
         const int h = (s + b) * L::kHeads + ln.sub;
         const bool is_q = h < p.hq;
-        const V8 x = unpack(rx[b]);
-        V8 u = an.rotate(unpack(rg[b]), ln.partner);
-        const float ss = head_sum<LPH>(dot8(x, x));
-        const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), p.eps));
+        const V8 x = unpack(rx[b].a, rx[b].b);
+        V8 u = unpack(rg[b].a, rg[b].b);
+        an.rotate(u, ln.on);
+        const V8 wt = unpack(is_q ? wq.a : wk.a, is_q ? wq.b : wk.b);
         V8 wu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) wu.v[j] = __fmul_rn(u.v[j], is_q ? wq.v[j] : wk.v[j]);
-        const float m = head_sum<LPH>(dot8(wu, x));
+        for (int j = 0; j < 8; ++j) wu.v[j] = __fmul_rn(u.v[j], wt.v[j]);
+        const float ss = head_sum<LPH>(dot8(x, x)), m = head_sum<LPH>(dot8(wu, x));
         if (h < H && (is_q ? p.qw != nullptr : p.kw != nullptr)) {
+          const float r = rsqrtf(__fmaf_rn(ss, 1.0f / D, p.eps));
           const float f = __fmul_rn(__fmul_rn(r, r), __fmul_rn(m, 1.0f / D));
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float e = __fmul_rn(u.v[j], __fmul_rn(x.v[j], r));
-            if (is_q) aq.v[j] = __fadd_rn(aq.v[j], e);
-            else ak.v[j] = __fadd_rn(ak.v[j], e);
+            const float xr = __fmul_rn(x.v[j], r);
+            if (is_q) aq.v[j] = __fmaf_rn(u.v[j], xr, aq.v[j]);
+            else ak.v[j] = __fmaf_rn(u.v[j], xr, ak.v[j]);
             u.v[j] = __fmul_rn(r, __fmaf_rn(-x.v[j], f, wu.v[j]));
           }
         }
-        if (h < H) {
-          const int64_t at = (is_q ? h : h - p.hq) * D + ln.d0;
-          *reinterpret_cast<uint4*>((is_q ? p.qo + t * p.qo_st : p.ko + t * p.ko_st) + at) = pack(u);
-        }
+        if (h < H) store8((is_q ? qo : ko) + h * D, ln, u);
       }
     }
   }
@@ -256,8 +260,9 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const QkRopeParam
       ak.v[j] = __fadd_rn(ak.v[j], __shfl_xor_sync(kAll, ak.v[j], d));
     }
     if (ln.sub == 0) {
-      s_sum[warp][ln.d0 + j] = aq.v[j];
-      s_sum[warp][D + ln.d0 + j] = ak.v[j];
+      const int at = j < 4 ? ln.d0 + j : ln.d1 + j - 4;
+      s_sum[warp][at] = aq.v[j];
+      s_sum[warp][D + at] = ak.v[j];
     }
   }
   __syncthreads();
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const QkRopeParam
   const int c4 = threadIdx.x % kCols4, grp = threadIdx.x / kCols4;
   float4 a = make_float4(0, 0, 0, 0);
   const float4* rows = reinterpret_cast<const float4*>(p.ws);
-#pragma unroll 8
+#pragma unroll 16
   for (int i = grp; i < gridDim.x; i += kGroups) {
     const float4 v = __ldcg(rows + (int64_t)i * kCols4 + c4);
     a.x = __fadd_rn(a.x, v.x), a.y = __fadd_rn(a.y, v.y);
