@@ -13,7 +13,6 @@ only check and marshal arguments; ``include/nvfp4.h`` states what each computes.
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import math
 import struct
 
@@ -84,22 +83,12 @@ def declare(L: C.CDLL) -> None:
         getattr(L, name).restype = size
 
 
-def _on_device(fn):
-    """Run an entry point with the device of its first tensor current (no
-    device switch where it is current already: these calls are short)."""
-    @functools.wraps(fn)
-    def wrapper(*args, **kwargs):
-        x = args[0] if not isinstance(args[0], dict) else args[0]["k_codes"]
-        dev = x.get_device()
-        if dev == _current_device() or dev < 0:
-            return fn(*args, **kwargs)
-        with torch.cuda.device(dev):
-            return fn(*args, **kwargs)
-    return wrapper
+# The library launches on the current device. These calls are short, so an entry
+# point compares that with its first tensor's device and only calls itself again
+# under torch.cuda.device where they differ.
 
-
-def _current_device() -> int:
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+def _elsewhere(dev: int) -> bool:
+    return dev >= 0 and dev != torch._C._cuda_getDevice()
 
 
 def _stream(dev: int) -> int:
@@ -197,7 +186,6 @@ def _cache(c: dict, dev: int) -> tuple[bytes, int, int]:
 
 # ----------------------------------------------------------------- entries --
 
-@_on_device
 def nvfp4_kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor,
                   free_pages: torch.Tensor, page_size: int, tokens: int,
                   out: dict | None = None, status: torch.Tensor | None = None) -> dict:
@@ -206,12 +194,16 @@ def nvfp4_kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor,
     the front of `free_pages`. Returns {"table", "seq_lens", "q_start", "slots",
     "positions", "pages_used"}, allocated here unless `out` (an earlier return
     value) is passed."""
+    dev = cached.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_kv_plan(cached, new, table, free_pages, page_size, tokens, out, status)
     B = cached.shape[0]
     if table.dim() != 2:
         raise ValueError("table must be [requests, columns]")
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    device, dev, i32 = cached.device, cached.get_device(), torch.int32
+    device, i32 = cached.device, torch.int32
     ins = (_typed(cached, "cached", (B,), i32, dev), _typed(new, "new", (B,), i32, dev), B,
            _typed(table, "table", (B, table.shape[1]), i32, dev), table.shape[1], page_size,
            _typed(free_pages, "free_pages", (free_pages.numel(),), i32, dev), free_pages.numel(),
@@ -240,6 +232,14 @@ def nvfp4_kv_plan(cached: torch.Tensor, new: torch.Tensor, table: torch.Tensor,
     return out
 
 
+def _weight(w: torch.Tensor, name: str, dim: int, dev: int) -> int:
+    if w.dtype not in _BF16 or w.shape != (dim,):
+        raise ValueError(f"{name} must be bf16 [{dim}]")
+    if w.get_device() != dev or dev < 0 or not w.is_contiguous():
+        _refuse(w, name, None, _BF16, dev)
+    return w.data_ptr()
+
+
 def _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev) -> bytes:
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [tokens, heads, head_dim]")
@@ -249,17 +249,13 @@ def _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev) -> 
     if cos_sin.dtype is not torch.float32:
         raise TypeError(f"cos_sin must be torch.float32, got {cos_sin.dtype}")
     length, rotary = cos_sin.shape
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype not in _BF16 or w.shape != (D,)):
-            raise ValueError(f"{n} must be bf16 [{D}]")
-    return _QK.pack(T, hq, k.shape[1], D, rotary, int(interleaved), eps,
-                    _optional(q_weight, "q_weight", D, _BF16, dev),
-                    _optional(k_weight, "k_weight", D, _BF16, dev),
+    return _QK.pack(T, hq, k.shape[1], D, rotary, interleaved, eps,
+                    0 if q_weight is None else _weight(q_weight, "q_weight", D, dev),
+                    0 if k_weight is None else _weight(k_weight, "k_weight", D, dev),
                     _typed(positions, "positions", (T,), torch.int32, dev),
-                    _typed(cos_sin, "cos_sin", (length, rotary), torch.float32, dev), length)
+                    _typed(cos_sin, "cos_sin", cos_sin.shape, torch.float32, dev), length)
 
 
-@_on_device
 def nvfp4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
                        cos_sin: torch.Tensor, q_weight: torch.Tensor | None = None,
                        k_weight: torch.Tensor | None = None, eps: float = 1e-6,
@@ -271,6 +267,10 @@ def nvfp4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor
     may be apart) in one launch. cos_sin: fp32 [positions, rotary_dim], cosines
     then sines. Returns {"q", "k"}; q_out, k_out may be q and k themselves."""
     dev = q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps,
+                                      interleaved, q_out, k_out, status)
     cfg = _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev)
     (T, hq, D), hk = q.shape, k.shape[1]
     rq, rk = _rows(q, "q", T, hq, D, dev), _rows(k, "k", T, hk, D, dev)
@@ -302,7 +302,6 @@ def qk_norm_rope_workspace(device) -> torch.Tensor:
     return _workspace(_lib().nvfp4_qk_norm_rope_ws_bytes(), device)
 
 
-@_on_device
 def nvfp4_qk_norm_rope_bwd(gq_out: torch.Tensor, gk_out: torch.Tensor, q: torch.Tensor,
                            k: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
                            q_weight: torch.Tensor | None = None,
@@ -314,7 +313,12 @@ def nvfp4_qk_norm_rope_bwd(gq_out: torch.Tensor, gk_out: torch.Tensor, q: torch.
     inputs: {"gq", "gk", "gq_weight", "gk_weight"} (weight gradients fp32, None
     without the weight). workspace: from qk_norm_rope_workspace; a fresh one is
     cleared for the call when none is given."""
-    dev, device = q.get_device(), q.device
+    dev = q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_qk_norm_rope_bwd(gq_out, gk_out, q, k, positions, cos_sin, q_weight,
+                                          k_weight, eps, interleaved, workspace, gq, gk, status)
+    device = q.device
     cfg = _qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev)
     (T, hq, D), hk = q.shape, k.shape[1]
     ins = (_rows(gq_out, "gq_out", T, hq, D, dev), _rows(gk_out, "gk_out", T, hk, D, dev),
@@ -324,26 +328,33 @@ def nvfp4_qk_norm_rope_bwd(gq_out: torch.Tensor, gk_out: torch.Tensor, q: torch.
     if gk is None:
         gk = torch.empty((T, hk, D), dtype=k.dtype, device=device)
     f32 = torch.float32
-    gqw = None if q_weight is None else torch.empty(D, dtype=f32, device=device)
-    gkw = None if k_weight is None else torch.empty(D, dtype=f32, device=device)
+    gqw = gkw = None
+    if q_weight is not None:
+        gqw = torch.empty(D, dtype=f32, device=device)
+    if k_weight is not None:
+        gkw = torch.empty(D, dtype=f32, device=device)
     if workspace is None and (gqw is not None or gkw is not None):
         workspace = qk_norm_rope_workspace(device)
-    _check("nvfp4_qk_norm_rope_bwd", _lib().nvfp4_qk_norm_rope_bwd(
+    status_code = _lib().nvfp4_qk_norm_rope_bwd(
         cfg, *ins, _rows(gq, "gq", T, hq, D, dev), _rows(gk, "gk", T, hk, D, dev),
         0 if gqw is None else gqw.data_ptr(), 0 if gkw is None else gkw.data_ptr(),
         _optional(workspace, "workspace", 1, _I32, dev),
         0 if workspace is None else 4 * workspace.numel(),
-        _optional(status, "status", 1, _I32, dev), _stream(dev)))
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+    if status_code:
+        _check("nvfp4_qk_norm_rope_bwd", status_code)
     return {"gq": gq, "gk": gk, "gq_weight": gqw, "gk_weight": gkw}
 
 
-@_on_device
 def nvfp4_kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                     dequant: bool = False, status: torch.Tensor | None = None) -> dict:
     """Quantise K and V rows (bf16 [tokens, kv_heads, head_dim]; tokens may be
     apart) into the cache's slots (int64 [tokens], -1 = skip). Returns {"k",
     "v"}: with dequant the values the codes stand for (bf16), else None."""
     dev = cache["k_codes"].get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_kv_append(cache, k, v, slots, dequant, status)
     c, hk, D = _cache(cache, dev)
     T = k.shape[0]
     rk, rv = _rows(k, "k", T, hk, D, dev), _rows(v, "v", T, hk, D, dev)
@@ -352,9 +363,11 @@ def nvfp4_kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, slots: torch.
     if dequant:
         kd = torch.empty((T, hk, D), dtype=torch.bfloat16, device=k.device)
         vd = torch.empty((T, hk, D), dtype=torch.bfloat16, device=k.device)
-    _check("nvfp4_kv_append", _lib().nvfp4_kv_append(
+    status_code = _lib().nvfp4_kv_append(
         c, rk, rv, at, T, kd.data_ptr() if dequant else 0, vd.data_ptr() if dequant else 0,
-        _optional(status, "status", 1, _I32, dev), _stream(dev)))
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+    if status_code:
+        _check("nvfp4_kv_append", status_code)
     return {"k": kd, "v": vd}
 
 
@@ -364,7 +377,6 @@ def kv_attention_workspace(device) -> torch.Tensor:
     return _workspace(_lib().nvfp4_kv_attention_ws_bytes(), device)
 
 
-@_on_device
 def nvfp4_kv_attention(q: torch.Tensor, cache: dict, table: torch.Tensor, seq_lens: torch.Tensor,
                        q_start: torch.Tensor, max_q: int, scale: float | None = None,
                        window: int = 0, out: torch.Tensor | None = None,
@@ -376,7 +388,12 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: dict, table: torch.Tensor, seq_le
     bound of the requests' query rows. scale defaults to head_dim ** -0.5.
     workspace: from kv_attention_workspace; a fresh one is cleared for the call
     when none is given. Returns {"out", "lse"}."""
-    dev, device, i32 = q.get_device(), q.device, torch.int32
+    dev = q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_kv_attention(q, cache, table, seq_lens, q_start, max_q, scale, window,
+                                      out, lse, workspace, status)
+    device, i32 = q.device, torch.int32
     if q.dim() != 3 or table.dim() != 2:
         raise ValueError("q must be [tokens, q_heads, head_dim], table [requests, columns]")
     c, _, dim = _cache(cache, dev)
