@@ -46,6 +46,20 @@ constexpr int kItems = 4;      // items handed out ahead
 constexpr long long kWaitCycles = 2000000000;  // about a second
 constexpr uint32_t kNegInf = 0xFF800000u;
 
+__device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* dead,
+                                       int32_t* status) {
+  const long long t0 = clock64();
+  while (!mbar_try(b, parity)) {
+    if (*dead) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *dead = 1;
+      flag(status, kDevTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 struct Bars {
   uint64_t q_full[2];
   uint64_t s_full[2][2], p_full[2][2];  // [tile][S buffer]
@@ -59,7 +73,8 @@ struct Bars {
 template <int D>
 struct Smem {
   static constexpr int kTile = 128 * D * 2;  // bytes of a 128 x D f16 tile
-  static constexpr size_t kBytes = 2 * kTile + 4 * (size_t)kTile + 1024;  // + alignment
+  static constexpr int kOut = 8 * 32 * 64;       // 32 rows x 32 bf16 per softmax warp
+  static constexpr size_t kBytes = 2 * kTile + 4 * (size_t)kTile + kOut + 1024;  // + alignment
 };
 
 // A request this kernel takes: more rows than the other kernel does.
@@ -79,10 +94,10 @@ struct Tiles {
 };
 __device__ __forceinline__ Tiles block_tiles(const KvAttnParams& p, const Request& r, int pt) {
   const int last = min((pt + 1) * kRowsItem, r.n * p.G) - 1;
-  const int hi = r.len - r.n + last / p.G + 1;
+  const int hi = r.len - r.n + (int)fastdiv((uint32_t)last, p.by_group) + 1;
   int begin = 0;
   if (p.window > 0) {
-    const int low = r.len - r.n + pt * kRowsItem / p.G + 1 - min(p.window, r.len);
+    const int low = r.len - r.n + (int)fastdiv((uint32_t)(pt * kRowsItem), p.by_group) + 1 - min(p.window, r.len);
     begin = max(0, low - r.lo16) / kTileN;
   }
   return {begin, max(1, (hi - r.lo16 + kTileN - 1) / kTileN - begin)};
@@ -90,6 +105,7 @@ __device__ __forceinline__ Tiles block_tiles(const KvAttnParams& p, const Reques
 __device__ __forceinline__ int64_t request_tiles(const KvAttnParams& p, const Request& r) {
   int64_t c = 0;
   const int n = row_blocks(p, r);
+#pragma unroll 1
   for (int pt = 0; pt < n; ++pt) c += block_tiles(p, r, pt).count;
   return c * p.hk;
 }
@@ -109,8 +125,8 @@ struct Walk {
   int64_t skip;  // tiles before pos, counted from (b, h, pt)
   int b, h, pt, blocks;
   Request r;
-  __device__ void start(const KvAttnParams& p, int64_t first, int64_t end, int64_t per_cta, int b0,
-                        int64_t off) {
+  __device__ __forceinline__ void start(const KvAttnParams& p, int64_t first, int64_t end, int64_t per_cta, int b0,
+                        int64_t off, int64_t per_head) {
     pos = first;
     run = per_cta;
     last = end;
@@ -118,12 +134,12 @@ struct Walk {
     bool bad;
     r = many_rows(p, b, bad);
     blocks = row_blocks(p, r);
-    const int64_t per_head = request_tiles(p, r) / p.hk;
     h = (int)(off / per_head);
     skip = off - h * per_head;
     pt = 0;
   }
-  __device__ bool next(const KvAttnParams& p, Item& it) {
+  __device__ __forceinline__ bool next(const KvAttnParams& p, Item& it) {
+#pragma unroll 1
     while (pos < last) {
       if (pt == blocks) {
         pt = 0;
@@ -164,6 +180,110 @@ struct Walk {
   }
 };
 
+// Loads the item's query rows of one warp (rows 32 w .. + 31 of tile `tile`) into the
+// tile's shared memory, LPR lanes to a row, scaled to f16 in place; returns the score
+// factor of this lane's row. Short loops: code that runs once per item comes from far
+// away (unrolled, with the rows in registers, it took 9700 clocks an item).
+template <int D>
+__device__ __forceinline__ float load_queries(const KvAttnParams& p, const Item& x, uint8_t* dst,
+                                              int tile, int w, int lane) {
+  constexpr int LPR = D / 8, kPer = 32 / LPR;
+  const int sub = lane / LPR, ql = lane % LPR;
+  const int rows = x.r.n * p.G, first_row = x.row0 + tile * kRowsTile + w * 32;
+  const uint16_t* from = p.q + (int64_t)x.r.q0 * p.q_st + (int64_t)(x.h * p.G) * D + ql * 8;
+  dst += (ql >> 3) * (128 * 128) + w * 32 * 128;
+#pragma unroll 1
+  for (int i = sub; i < 32; i += kPer) {
+    const int rr = first_row + i;
+    const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
+    const bool in = rr < rows;  // the others become zeros
+    cp_async16_zfill(dst + i * 128 + (((ql & 7) ^ (i & 7)) << 4),
+                     in ? from + (int64_t)tk * p.q_st + hh * D : from, in ? 16 : 0);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  const float fk = p.scale * kLog2e * x.kg;
+  float f = 0.0f;
+#pragma unroll 2
+  for (int i = 0; i < 32; i += kPer) {
+    const int row = i + sub;
+    uint4* at = reinterpret_cast<uint4*>(dst + row * 128 + (((ql & 7) ^ (row & 7)) << 4));
+    const uint4 v = *at;
+    uint32_t m = absmax_bits4(v);
+#pragma unroll
+    for (int d = LPR / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+    if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
+    // 2^e brings the row's largest element to [2^13, 2^14)
+    const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
+    float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    float fr = fk * __uint_as_float((uint32_t)(127 - e) << 23);
+    if (fr < 0.0f) fr = -fr, up = -up;  // the running maximum needs f > 0, and a masked
+    fr = fmaxf(fr, 1.17549435e-38f);    // score (-inf) must stay -inf times f
+    *at = make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                     pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                     pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                     pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+    const float mine = __shfl_sync(kAll, fr, (lane % kPer) * LPR);
+    if (lane / kPer == i / kPer) f = mine;
+  }
+  fence_smem_async();
+  __syncwarp();
+  return f;
+}
+
+// Record of CTA c's part of an item that begins in CTA c0.
+__device__ __forceinline__ float* prefill_record(const KvAttnParams& p, int c, int c0) {
+  return p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
+}
+// Joins row ri of the records of CTAs c0 .. c1, in order.
+template <int D>
+__device__ __forceinline__ void join_rows(const KvAttnParams& p, int c0, int c1, int ri, bool live,
+                                          int64_t orow, float vg) {
+  __threadfence();
+  float mx = __uint_as_float(kNegInf);
+#pragma unroll 1
+  for (int c = c0; c <= c1; ++c)
+    mx = fmaxf(mx, __ldcg(prefill_record(p, c, c0) + kRowsItem * 128 + ri));
+  auto weight = [&](int c) {
+    const float mc = __ldcg(prefill_record(p, c, c0) + kRowsItem * 128 + ri);
+    return mc == __uint_as_float(kNegInf) ? 0.0f : ex2(mc - mx);
+  };
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = c0; c <= c1; ++c)
+    sum += weight(c) * __ldcg(prefill_record(p, c, c0) + kRowsItem * 129 + ri);
+  const float fo = sum == 0.0f ? 0.0f : vg / sum;
+  uint2* dst = reinterpret_cast<uint2*>(p.out) + orow * (D / 4);
+#pragma unroll 1
+  for (int d0 = 0; d0 < D / 4; d0 += 16) {  // 16 loads of 16 bytes in flight
+    float4 v[16];
+#pragma unroll
+    for (int d = 0; d < 16; ++d) v[d] = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int c = c0; c <= c1; ++c) {
+      const float w = weight(c);
+      const float4* q =
+          reinterpret_cast<const float4*>(prefill_record(p, c, c0)) + d0 * kRowsItem + ri;
+      float4 x[16];
+#pragma unroll
+      for (int d = 0; d < 16; ++d) x[d] = __ldcg(q + d * kRowsItem);
+      if (w != 0.0f)  // a part that saw nothing of this row holds no numbers
+#pragma unroll
+        for (int d = 0; d < 16; ++d) {
+          v[d].x = __fmaf_rn(x[d].x, w, v[d].x), v[d].y = __fmaf_rn(x[d].y, w, v[d].y);
+          v[d].z = __fmaf_rn(x[d].z, w, v[d].z), v[d].w = __fmaf_rn(x[d].w, w, v[d].w);
+        }
+    }
+    if (live)
+#pragma unroll
+      for (int d = 0; d < 16; ++d)
+        dst[d0 + d] = make_uint2(pack_bf16x2(v[d].x * fo, v[d].y * fo),
+                                 pack_bf16x2(v[d].z * fo, v[d].w * fo));
+  }
+  if (live && p.lse)
+    p.lse[orow] = sum == 0.0f ? __uint_as_float(kNegInf) : (mx - kBias + log2f(sum)) * kLn2;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnParams p,
                                                                  const int ctas) {
@@ -174,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   __shared__ volatile int s_dead;
   __shared__ int64_t s_scan[kThreads / 32];
   __shared__ int s_b0;
-  __shared__ int64_t s_off;
+  __shared__ int64_t s_off, s_per_head;
   __shared__ Walk s_walk;
   __shared__ Item s_item[kItems];
   // first cache row of every 16 keys of a tile: 16 neighbours never leave a page
@@ -184,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   uint8_t* sq = base;               // [2] Q tiles
   uint8_t* sk = base + 2 * kTile;   // [2] K tiles
   uint8_t* sv = base + 4 * kTile;   // [2] V tiles
+  uint8_t* so = base + 6 * kTile;   // results on their way out
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
 
@@ -191,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   const int share = (p.B + kThreads - 1) / kThreads;
   const int rb0 = min(tid * share, p.B), rb1 = min(rb0 + share, p.B);
   int64_t mine = 0;
+#pragma unroll 1
   for (int b = rb0; b < rb1; ++b) {
     bool bad;
     const Request r = many_rows(p, b, bad);
@@ -237,12 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   const int64_t first = (int64_t)blockIdx.x * run, last = min(first + run, total);
   if (first < last && incl - mine <= first && first < incl) {
     int64_t at = incl - mine;
+#pragma unroll 1
     for (int b = rb0; b < rb1; ++b) {
       bool bad;
       const int64_t c = request_tiles(p, many_rows(p, b, bad));
       if (first < at + c) {
         s_b0 = b;
         s_off = first - at;
+        s_per_head = c / p.hk;
         break;
       }
       at += c;
@@ -250,14 +374,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   }
 
   // ---- requests without keys -------------------------------------------------
+#pragma unroll 1
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     bool bad;
     const Request r = many_rows(p, b, bad);
     if (r.n == 0 || r.len > 0) continue;
     const int64_t rows = (int64_t)r.n * p.hq;
+#pragma unroll 1
     for (int64_t i = tid; i < rows * (D / 8); i += kThreads)
       reinterpret_cast<uint4*>(p.out)[(int64_t)r.q0 * p.hq * (D / 8) + i] = make_uint4(0, 0, 0, 0);
     if (p.lse)
+#pragma unroll 1
       for (int64_t i = tid; i < rows; i += kThreads)
         p.lse[(int64_t)r.q0 * p.hq + i] = __uint_as_float(kNegInf);
   }
@@ -272,17 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 
   // A wait with a limit (kWaitCycles); false once the CTA gave up.
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    if (mbar_try(b, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try(b, parity)) {
-      if (s_dead) return false;
-      if (clock64() - t0 > kWaitCycles) {
-        s_dead = 1;
-        flag(p.status, kDevTimeout);
-        return false;
-      }
-    }
-    return true;
+    return mbar_try(b, parity) || wait_long(b, parity, &s_dead, p.status);
   };
   // the same for a whole warp, whose lanes go on together
   auto wait_warp = [&](uint64_t* b, uint32_t parity) -> bool {
@@ -310,75 +427,98 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     const int tile = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane offset in a TMEM address
     const uint32_t ts = t_s(tile) + lanes, to = t_o(tile) + lanes;
-    // Loads the item's query rows of this warp into the tile, LPR lanes to a row,
-    // scaled to f16; returns the score factor of this thread's row. The products
-    // with the rows that were there are done: their last scores have been seen.
-    constexpr int LPR = D / 8, kPer = 32 / LPR;
-    const int sub = lane / LPR, ql = lane % LPR;
-    auto load_q = [&](const Item& x) -> float {
-      const int rows = x.r.n * p.G, first_row = x.row0 + tile * kRowsTile + (warp & 3) * 32;
-      const float fk = p.scale * kLog2e * x.kg;
-      float f = 0.0f;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        constexpr int U = 16 / kPer;
-        uint4 raw[U];
+    uint32_t n = 0;  // steps of 64 keys done by this tile
+    // The item being worked on: what its result needs, too, which is written when the
+    // next item's query rows have been loaded (while the last P V runs).
+    float m = 0.0f, l = 0.0f, f = 0.0f, vg = 0.0f;
+    int row0 = 0, rows = 0, tk = 0, q0 = 0, h_now = 0, c0 = 0, c1 = 0;
+    bool live = false, open = false, ok = true;
+    while (ok) {
+      const bool have = next(it), mine_now = have && tile * kRowsTile < it->rows;
+      // (the products with the query rows that were there are done: their last scores
+      // have been seen)
+      if (mine_now) {
+        f = load_queries<D>(p, *it, sq + tile * kTile, tile, warp & 3, lane);
+        if (lane == 0) mbar_arrive(&bar.q_full[tile]);
+      }
+      if (open) {
+        open = false;
+        // -- the last item's result: the whole row, or a record of this CTA's part of it
+        if (!(ok = wait_warp(&bar.o_done[tile], (n - 1) & 1))) break;
+        fence_after();
+        uint32_t s[32];
+        const int64_t orow = (int64_t)(q0 + tk) * p.hq + h_now * p.G + (row0 + row - tk * p.G);
+        if (c0 == c1) {
+          const float fo = l == 0.0f ? 0.0f : vg / l;
+          // Rows leave four lanes to a row, 64 bytes at a time, by way of shared memory
+          // (a thread's own row would go out in 16-byte pieces, half a sector each).
+          uint8_t* mine_so = so + warp * (32 * 64);
+          uint4* to_row[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int rr = first_row + half * 16 + u * kPer + sub;
-          raw[u] = make_uint4(0, 0, 0, 0);
-          if (rr < rows) {
-            const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
-            raw[u] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(x.r.q0 + tk) * p.q_st +
-                                                     (int64_t)(x.h * p.G + hh) * D + ql * 8);
+          for (int q = 0; q < 4; ++q) {
+            const int rr = row0 + (warp & 3) * 32 + q * 8 + (lane >> 2);
+            const int rt = (int)fastdiv((uint32_t)rr, p.by_group);
+            const int64_t at = (int64_t)(q0 + rt) * p.hq + h_now * p.G + (rr - rt * p.G);
+            to_row[q] = rr < rows ? reinterpret_cast<uint4*>(p.out) + at * (D / 8) + (lane & 3) : nullptr;
+          }
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_ld32(to + 32 * c, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float* x = reinterpret_cast<const float*>(s) + 8 * i;
+              *reinterpret_cast<uint4*>(mine_so + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(pack_bf16x2(x[0] * fo, x[1] * fo), pack_bf16x2(x[2] * fo, x[3] * fo),
+                             pack_bf16x2(x[4] * fo, x[5] * fo), pack_bf16x2(x[6] * fo, x[7] * fo));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int row32 = q * 8 + (lane >> 2);
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  mine_so + row32 * 64 + (((lane & 3) ^ ((row32 >> 1) & 3)) << 4));
+              if (to_row[q]) to_row[q][4 * c] = v;
+            }
+            __syncwarp();
+          }
+          if (live && p.lse)
+            p.lse[orow] =
+                l == 0.0f ? __uint_as_float(kNegInf) : (m - kBias + log2f(l)) * kLn2;
+        } else {
+          // [D / 4][256 rows][4], then maxima and sums
+          float* rec = prefill_record(p, blockIdx.x, c0);
+          const int ri = tile * kRowsTile + row;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_ld32(to + 32 * c, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(rec)[(8 * c + i) * kRowsItem + ri] =
+                  make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+          }
+          rec[kRowsItem * 128 + ri] = m;
+          rec[kRowsItem * 129 + ri] = l;
+          // a row is written by the same warp of every CTA: a ticket per warp
+          __threadfence();
+          __syncwarp();
+          uint32_t* ticket = p.tickets + kAttnMaxCtas + 8 * c0 + warp;
+          uint32_t mine_ticket = 0;
+          if (lane == 0) mine_ticket = atomicAdd(ticket, 1u);
+          if (__shfl_sync(kAll, mine_ticket, 0) == (uint32_t)(c1 - c0)) {
+            join_rows<D>(p, c0, c1, ri, live, orow, vg);
+            if (lane == 0) *ticket = 0;
           }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int row32 = half * 16 + u * kPer;  // + sub: the row inside the warp's 32
-          const int row = (warp & 3) * 32 + row32 + sub;
-          const uint4 v = raw[u];
-          uint32_t m = absmax_bits4(v);
-#pragma unroll
-          for (int d = LPR / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
-          if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
-          // 2^e brings the row's largest element to [2^13, 2^14)
-          const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
-          float up = __uint_as_float((uint32_t)(127 + e) << 23);
-          float fr = fk * __uint_as_float((uint32_t)(127 - e) << 23);
-          if (fr < 0.0f) fr = -fr, up = -up;  // the running maximum needs f > 0, and a masked
-          fr = fmaxf(fr, 1.17549435e-38f);    // score (-inf) must stay -inf times f
-          *reinterpret_cast<uint4*>(sq + tile * kTile + (ql >> 3) * (128 * 128) + row * 128 +
-                                    (((ql & 7) ^ (row & 7)) << 4)) =
-              make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                         pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                         pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                         pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
-          const float mine_f = __shfl_sync(kAll, fr, (lane % kPer) * LPR);
-          if (lane / kPer == row32 / kPer) f = mine_f;
-        }
       }
-      fence_smem_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.q_full[tile]);
-      return f;
-    };
-
-    uint32_t n = 0;  // steps of 64 keys done by this tile
-    bool ok = true, have = next(it);
-    float f = 0.0f;
-    auto mine_of = [&](const Item& x) { return tile * kRowsTile < x.rows; };
-    if (have && mine_of(*it)) f = load_q(*it);
-    while (ok && have) {
-      if (!mine_of(*it)) {
-        have = next(it);
-        if (have && mine_of(*it)) f = load_q(*it);
-        continue;
-      }
+      if (!have) break;
+      if (!mine_now) continue;
       const Request r = it->r;
-      const int row0 = it->row0 + tile * kRowsTile, rows = r.n * p.G;
-      const int tk = (int)fastdiv((uint32_t)(row0 + row), p.by_group);
-      const bool live = row0 + row < rows;
+      row0 = it->row0 + tile * kRowsTile, rows = r.n * p.G;
+      tk = (int)fastdiv((uint32_t)(row0 + row), p.by_group);
+      live = row0 + row < rows;
+      q0 = r.q0, h_now = it->h, vg = it->vg, c0 = it->c0, c1 = it->c1;
       // the row sees keys [low, low + span)
       const int lim = live ? r.len - r.n + tk + 1 : 0;
       const int low = p.window > 0 ? lim - min(p.window, r.len) : 0;
@@ -389,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       const int safe_lo = p.window > 0 ? r.len - r.n + (int)fastdiv((uint32_t)last_row, p.by_group) +
                                              1 - min(p.window, r.len)
                                        : 0;
-      float m = __uint_as_float(kNegInf), l = 0.0f;
+      m = __uint_as_float(kNegInf), l = 0.0f;
       const int steps = 2 * (it->t1 - it->t0);
       int key0 = r.lo16 + it->t0 * kTileN;
 
@@ -467,105 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (lane == 0) mbar_arrive(&bar.p_full[tile][sb]);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      if (!ok) break;
-
-      // -- the next item's query rows, while the last P V runs
-      const int hh = row0 + row - tk * p.G;
-      const float vg = it->vg;
-      const int64_t orow = (int64_t)(r.q0 + tk) * p.hq + it->h * p.G + hh;
-      const int c0 = it->c0, c1 = it->c1;
-      have = next(it);
-      if (have && mine_of(*it)) f = load_q(*it);
-
-      // -- result: the whole row, or a record of this CTA's part of it
-      if (!(ok = wait_warp(&bar.o_done[tile], (n - 1) & 1))) break;
-      fence_after();
-      uint32_t s[32];
-      if (c0 == c1) {
-        const float fo = l == 0.0f ? 0.0f : vg / l;
-        uint4* dst = reinterpret_cast<uint4*>(p.out) + orow * (D / 8);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          tmem_ld32(to + 32 * c, s);
-          tmem_wait_ld();
-          if (live)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* x = reinterpret_cast<const float*>(s) + 8 * i;
-              dst[4 * c + i] = make_uint4(
-                  pack_bf16x2(x[0] * fo, x[1] * fo), pack_bf16x2(x[2] * fo, x[3] * fo),
-                  pack_bf16x2(x[4] * fo, x[5] * fo), pack_bf16x2(x[6] * fo, x[7] * fo));
-            }
-        }
-        if (live && p.lse)
-          p.lse[orow] =
-              l == 0.0f ? __uint_as_float(kNegInf) : (m - kBias + log2f(l)) * kLn2;
-      } else {
-        // [D / 4][256 rows][4], then maxima and sums
-        float* rec = p.part + ((int64_t)blockIdx.x * 2 + (blockIdx.x == c0 ? 1 : 0)) * kPrefillRecord;
-        const int ri = tile * kRowsTile + row;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          tmem_ld32(to + 32 * c, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            reinterpret_cast<uint4*>(rec)[(8 * c + i) * kRowsItem + ri] =
-                make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
-        }
-        rec[kRowsItem * 128 + ri] = m;
-        rec[kRowsItem * 129 + ri] = l;
-        // a row is written by the same warp of every CTA: a ticket per warp
-        __threadfence();
-        __syncwarp();
-        uint32_t* ticket = p.tickets + kAttnMaxCtas + 8 * c0 + warp;
-        uint32_t mine_ticket = 0;
-        if (lane == 0) mine_ticket = atomicAdd(ticket, 1u);
-        if (__shfl_sync(kAll, mine_ticket, 0) == (uint32_t)(c1 - c0)) {
-          __threadfence();
-          auto record = [&](int c) {
-            return p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
-          };
-          float mx = __uint_as_float(kNegInf);
-          for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(record(c) + kRowsItem * 128 + ri));
-          float sum = 0.0f;
-          auto weight = [&](int c) {
-            const float mc = __ldcg(record(c) + kRowsItem * 128 + ri);
-            return mc == __uint_as_float(kNegInf) ? 0.0f : ex2(mc - mx);
-          };
-          for (int c = c0; c <= c1; ++c) sum += weight(c) * __ldcg(record(c) + kRowsItem * 129 + ri);
-          const float fo = sum == 0.0f ? 0.0f : vg / sum;
-          uint2* dst = reinterpret_cast<uint2*>(p.out) + orow * (D / 4);
-#pragma unroll 1
-          for (int d0 = 0; d0 < D / 4; d0 += 16) {  // 16 loads of 16 bytes in flight
-            float4 v[16];
-#pragma unroll
-            for (int d = 0; d < 16; ++d) v[d] = make_float4(0, 0, 0, 0);
-            for (int c = c0; c <= c1; ++c) {
-              const float w = weight(c);
-              const float4* q = reinterpret_cast<const float4*>(record(c)) + d0 * kRowsItem + ri;
-              float4 x[16];
-#pragma unroll
-              for (int d = 0; d < 16; ++d) x[d] = __ldcg(q + d * kRowsItem);
-              if (w != 0.0f)  // a part that saw nothing of this row holds no numbers
-#pragma unroll
-                for (int d = 0; d < 16; ++d) {
-                  v[d].x = __fmaf_rn(x[d].x, w, v[d].x), v[d].y = __fmaf_rn(x[d].y, w, v[d].y);
-                  v[d].z = __fmaf_rn(x[d].z, w, v[d].z), v[d].w = __fmaf_rn(x[d].w, w, v[d].w);
-                }
-            }
-            if (live)
-#pragma unroll
-              for (int d = 0; d < 16; ++d)
-                dst[d0 + d] = make_uint2(pack_bf16x2(v[d].x * fo, v[d].y * fo),
-                                         pack_bf16x2(v[d].z * fo, v[d].w * fo));
-          }
-          if (live && p.lse)
-            p.lse[orow] =
-                sum == 0.0f ? __uint_as_float(kNegInf) : (mx - kBias + log2f(sum)) * kLn2;
-          if (lane == 0) *ticket = 0;
-        }
-      }
+      open = true;
     }
   } else if (warp < 12) {
     // ==== dequantise ============================================================
@@ -744,18 +786,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       __syncwarp();
     } else if (warp == 13) {
       // ==== items ================================================================
-      if (lane == 0) {
-        s_walk.start(p, first, last, run, s_b0, s_off);
-        bool more = true;
-        for (uint32_t i = 0; more; ++i) {
-          if (!wait(&bar.item_free[i % kItems], ((i / kItems) & 1) ^ 1)) break;
-          Item& x = s_item[i % kItems];
+      if (lane == 0) s_walk.start(p, first, last, run, s_b0, s_off, s_per_head);
+      bool more = true;
+      for (uint32_t i = 0; more; ++i) {
+        if (!wait_warp(&bar.item_free[i % kItems], ((i / kItems) & 1) ^ 1)) break;
+        Item& x = s_item[i % kItems];
+        if (lane == 0) {
           more = s_walk.next(p, x);
           if (!more) x.t1 = 0;
           mbar_arrive(&bar.item_full[i % kItems]);
         }
+        more = __shfl_sync(kAll, more, 0);
+        __syncwarp();
+        if (more) {
+          // its query rows on their way to L2: they are loaded between two items, where
+          // nothing hides their latency
+          constexpr int kLines = D * 2 / 128;
+          for (int u = lane; u < x.rows * kLines; u += 32) {
+            const int rr = x.row0 + u / kLines;
+            const int tk = (int)fastdiv((uint32_t)rr, p.by_group);
+            const uint16_t* at = p.q + (int64_t)(x.r.q0 + tk) * p.q_st +
+                                 (int64_t)(x.h * p.G + rr - tk * p.G) * D + u % kLines * 64;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
     } else if (warp == 14) {
       // ==== cache rows: lane g looks up keys 16 g .. 16 g + 15 of a tile ==========
       uint32_t n = 0;
