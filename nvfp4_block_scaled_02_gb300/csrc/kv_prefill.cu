@@ -181,50 +181,50 @@ struct Walk {
 };
 
 // Loads the item's query rows of one warp (rows 32 w .. + 31 of tile `tile`) into the
-// tile's shared memory, LPR lanes to a row, scaled to f16 in place; returns the score
-// factor of this lane's row. Short loops: code that runs once per item comes from far
-// away (unrolled, with the rows in registers, it took 9700 clocks an item).
+// tile's shared memory, LPR lanes to a row, and scales them to f16 in place, a lane to a
+// row; returns the score factor of this lane's row. Short loops: code that runs once per
+// item comes from far away (unrolled, with the rows in registers and their maxima by way
+// of shuffles, it took 9700 clocks an item).
 template <int D>
 __device__ __forceinline__ float load_queries(const KvAttnParams& p, const Item& x, uint8_t* dst,
                                               int tile, int w, int lane) {
   constexpr int LPR = D / 8, kPer = 32 / LPR;
-  const int sub = lane / LPR, ql = lane % LPR;
   const int rows = x.r.n * p.G, first_row = x.row0 + tile * kRowsTile + w * 32;
-  const uint16_t* from = p.q + (int64_t)x.r.q0 * p.q_st + (int64_t)(x.h * p.G) * D + ql * 8;
-  dst += (ql >> 3) * (128 * 128) + w * 32 * 128;
-#pragma unroll 1
-  for (int i = sub; i < 32; i += kPer) {
-    const int rr = first_row + i;
-    const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
-    const bool in = rr < rows;  // the others become zeros
-    cp_async16_zfill(dst + i * 128 + (((ql & 7) ^ (i & 7)) << 4),
-                     in ? from + (int64_t)tk * p.q_st + hh * D : from, in ? 16 : 0);
+  dst += w * 32 * 128;
+  // chunk c of row i
+  auto at = [&](int i, int c) { return dst + (c >> 3) * (128 * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4); };
+  {
+    const int c = lane % LPR;
+    const uint16_t* from = p.q + (int64_t)x.r.q0 * p.q_st + (int64_t)(x.h * p.G) * D + c * 8;
+#pragma unroll 4
+    for (int j = 0; j < 32; j += kPer) {
+      const int i = j + lane / LPR, rr = first_row + i;
+      const int tk = (int)fastdiv((uint32_t)rr, p.by_group), hh = rr - tk * p.G;
+      const bool in = rr < rows;  // the others become zeros
+      cp_async16_zfill(at(i, c), in ? from + (int64_t)tk * p.q_st + hh * D : from, in ? 16 : 0);
+    }
   }
   cp_async_commit();
   cp_async_wait<0>();
-  const float fk = p.scale * kLog2e * x.kg;
-  float f = 0.0f;
-#pragma unroll 2
-  for (int i = 0; i < 32; i += kPer) {
-    const int row = i + sub;
-    uint4* at = reinterpret_cast<uint4*>(dst + row * 128 + (((ql & 7) ^ (row & 7)) << 4));
-    const uint4 v = *at;
-    uint32_t m = absmax_bits4(v);
-#pragma unroll
-    for (int d = LPR / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
-    if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
-    // 2^e brings the row's largest element to [2^13, 2^14)
-    const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
-    float up = __uint_as_float((uint32_t)(127 + e) << 23);
-    float fr = fk * __uint_as_float((uint32_t)(127 - e) << 23);
-    if (fr < 0.0f) fr = -fr, up = -up;  // the running maximum needs f > 0, and a masked
-    fr = fmaxf(fr, 1.17549435e-38f);    // score (-inf) must stay -inf times f
-    *at = make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                     pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                     pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                     pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
-    const float mine = __shfl_sync(kAll, fr, (lane % kPer) * LPR);
-    if (lane / kPer == i / kPer) f = mine;
+  __syncwarp();
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int c = 0; c < LPR; ++c) m = max(m, absmax_bits4(*reinterpret_cast<const uint4*>(at(lane, c))));
+  if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
+  // 2^e brings the row's largest element to [2^13, 2^14)
+  const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);
+  float up = __uint_as_float((uint32_t)(127 + e) << 23);
+  float f = p.scale * kLog2e * x.kg * __uint_as_float((uint32_t)(127 - e) << 23);
+  if (f < 0.0f) f = -f, up = -up;   // the running maximum needs f > 0, and a masked
+  f = fmaxf(f, 1.17549435e-38f);    // score (-inf) must stay -inf times f
+#pragma unroll 4
+  for (int c = 0; c < LPR; ++c) {
+    uint4* q = reinterpret_cast<uint4*>(at(lane, c));
+    const uint4 v = *q;
+    *q = make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                    pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                    pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                    pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
   }
   fence_smem_async();
   __syncwarp();
