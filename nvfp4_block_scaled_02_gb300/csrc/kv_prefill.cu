@@ -235,53 +235,11 @@ __device__ __forceinline__ float load_queries(const KvAttnParams& p, const Item&
 __device__ __forceinline__ float* prefill_record(const KvAttnParams& p, int c, int c0) {
   return p.part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * kPrefillRecord;
 }
-// Joins row ri of the records of CTAs c0 .. c1, in order.
-template <int D>
-__device__ __forceinline__ void join_rows(const KvAttnParams& p, int c0, int c1, int ri, bool live,
-                                          int64_t orow, float vg) {
-  __threadfence();
-  float mx = __uint_as_float(kNegInf);
-#pragma unroll 1
-  for (int c = c0; c <= c1; ++c)
-    mx = fmaxf(mx, __ldcg(prefill_record(p, c, c0) + kRowsItem * 128 + ri));
-  auto weight = [&](int c) {
-    const float mc = __ldcg(prefill_record(p, c, c0) + kRowsItem * 128 + ri);
-    return mc == __uint_as_float(kNegInf) ? 0.0f : ex2(mc - mx);
-  };
-  float sum = 0.0f;
-#pragma unroll 1
-  for (int c = c0; c <= c1; ++c)
-    sum += weight(c) * __ldcg(prefill_record(p, c, c0) + kRowsItem * 129 + ri);
-  const float fo = sum == 0.0f ? 0.0f : vg / sum;
-  uint2* dst = reinterpret_cast<uint2*>(p.out) + orow * (D / 4);
-#pragma unroll 1
-  for (int d0 = 0; d0 < D / 4; d0 += 16) {  // 16 loads of 16 bytes in flight
-    float4 v[16];
-#pragma unroll
-    for (int d = 0; d < 16; ++d) v[d] = make_float4(0, 0, 0, 0);
-#pragma unroll 1
-    for (int c = c0; c <= c1; ++c) {
-      const float w = weight(c);
-      const float4* q =
-          reinterpret_cast<const float4*>(prefill_record(p, c, c0)) + d0 * kRowsItem + ri;
-      float4 x[16];
-#pragma unroll
-      for (int d = 0; d < 16; ++d) x[d] = __ldcg(q + d * kRowsItem);
-      if (w != 0.0f)  // a part that saw nothing of this row holds no numbers
-#pragma unroll
-        for (int d = 0; d < 16; ++d) {
-          v[d].x = __fmaf_rn(x[d].x, w, v[d].x), v[d].y = __fmaf_rn(x[d].y, w, v[d].y);
-          v[d].z = __fmaf_rn(x[d].z, w, v[d].z), v[d].w = __fmaf_rn(x[d].w, w, v[d].w);
-        }
-    }
-    if (live)
-#pragma unroll
-      for (int d = 0; d < 16; ++d)
-        dst[d0 + d] = make_uint2(pack_bf16x2(v[d].x * fo, v[d].y * fo),
-                                 pack_bf16x2(v[d].z * fo, v[d].w * fo));
-  }
-  if (live && p.lse)
-    p.lse[orow] = sum == 0.0f ? __uint_as_float(kNegInf) : (mx - kBias + log2f(sum)) * kLn2;
+// Weight of CTA c's part in row ri of the whole, whose maximum is m.
+__device__ __forceinline__ float part_weight(const KvAttnParams& p, int c, int c0, int ri,
+                                             float m) {
+  const float mc = __ldcg(prefill_record(p, c, c0) + kRowsItem * 128 + ri);
+  return mc == __uint_as_float(kNegInf) ? 0.0f : ex2(mc - m);
 }
 
 template <int D>
@@ -446,57 +404,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         // -- the last item's result: the whole row, or a record of this CTA's part of it
         if (!(ok = wait_warp(&bar.o_done[tile], (n - 1) & 1))) break;
         fence_after();
-        uint32_t s[32];
-        const int64_t orow = (int64_t)(q0 + tk) * p.hq + h_now * p.G + (row0 + row - tk * p.G);
-        if (c0 == c1) {
-          const float fo = l == 0.0f ? 0.0f : vg / l;
-          // Rows leave four lanes to a row, 64 bytes at a time, by way of shared memory
-          // (a thread's own row would go out in 16-byte pieces, half a sector each).
-          uint8_t* mine_so = so + warp * (32 * 64);
-          uint4* to_row[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int rr = row0 + (warp & 3) * 32 + q * 8 + (lane >> 2);
-            const int rt = (int)fastdiv((uint32_t)rr, p.by_group);
-            const int64_t at = (int64_t)(q0 + rt) * p.hq + h_now * p.G + (rr - rt * p.G);
-            to_row[q] = rr < rows ? reinterpret_cast<uint4*>(p.out) + at * (D / 8) + (lane & 3) : nullptr;
-          }
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            tmem_ld32(to + 32 * c, s);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* x = reinterpret_cast<const float*>(s) + 8 * i;
-              *reinterpret_cast<uint4*>(mine_so + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                  make_uint4(pack_bf16x2(x[0] * fo, x[1] * fo), pack_bf16x2(x[2] * fo, x[3] * fo),
-                             pack_bf16x2(x[4] * fo, x[5] * fo), pack_bf16x2(x[6] * fo, x[7] * fo));
-            }
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int row32 = q * 8 + (lane >> 2);
-              const uint4 v = *reinterpret_cast<const uint4*>(
-                  mine_so + row32 * 64 + (((lane & 3) ^ ((row32 >> 1) & 3)) << 4));
-              if (to_row[q]) to_row[q][4 * c] = v;
-            }
-            __syncwarp();
-          }
-          if (live && p.lse)
-            p.lse[orow] =
-                l == 0.0f ? __uint_as_float(kNegInf) : (m - kBias + log2f(l)) * kLn2;
-        } else {
+        float s[32];
+        const int ri = tile * kRowsTile + row;
+        bool write = true;
+        if (c0 != c1) {
           // [D / 4][256 rows][4], then maxima and sums
           float* rec = prefill_record(p, blockIdx.x, c0);
-          const int ri = tile * kRowsTile + row;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
-            tmem_ld32(to + 32 * c, s);
+            tmem_ld32(to + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s));
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(rec)[(8 * c + i) * kRowsItem + ri] =
-                  make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+              reinterpret_cast<float4*>(rec)[(8 * c + i) * kRowsItem + ri] =
+                  make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
           }
           rec[kRowsItem * 128 + ri] = m;
           rec[kRowsItem * 129 + ri] = l;
@@ -506,9 +427,82 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           uint32_t* ticket = p.tickets + kAttnMaxCtas + 8 * c0 + warp;
           uint32_t mine_ticket = 0;
           if (lane == 0) mine_ticket = atomicAdd(ticket, 1u);
-          if (__shfl_sync(kAll, mine_ticket, 0) == (uint32_t)(c1 - c0)) {
-            join_rows<D>(p, c0, c1, ri, live, orow, vg);
+          write = __shfl_sync(kAll, mine_ticket, 0) == (uint32_t)(c1 - c0);
+          if (write) {  // the last CTA to get here joins the parts, in order
+            __threadfence();
             if (lane == 0) *ticket = 0;
+            m = __uint_as_float(kNegInf), l = 0.0f;
+#pragma unroll 1
+            for (int c = c0; c <= c1; ++c)
+              m = fmaxf(m, __ldcg(prefill_record(p, c, c0) + kRowsItem * 128 + ri));
+#pragma unroll 1
+            for (int c = c0; c <= c1; ++c)
+              l += part_weight(p, c, c0, ri, m) *
+                   __ldcg(prefill_record(p, c, c0) + kRowsItem * 129 + ri);
+          }
+        }
+        if (write) {
+          // Rows leave four lanes to a row, 64 bytes at a time, by way of shared memory
+          // (a thread's own row would go out in 16-byte pieces, half a sector each).
+          const float fo = l == 0.0f ? 0.0f : vg / l;
+          uint8_t* mine_so = so + warp * (32 * 64);
+          // rows of the output past this request's first, -1 where there is none
+          const int to_row = live ? tk * p.hq + h_now * p.G + (row0 + row - tk * p.G) : -1;
+          if (live && p.lse)
+            p.lse[(int64_t)q0 * p.hq + to_row] =
+                l == 0.0f ? __uint_as_float(kNegInf) : (m - kBias + log2f(l)) * kLn2;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            if (c0 == c1) {
+              tmem_ld32(to + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s));
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] = 0.0f;
+#pragma unroll 1
+              for (int part = c0; part <= c1; part += 2) {  // two parts' loads in flight
+                float4 x[2][8];
+                float wt[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int from = min(part + k, c1);
+                  const float4* q = reinterpret_cast<const float4*>(prefill_record(p, from, c0)) +
+                                    8 * c * kRowsItem + ri;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) x[k][i] = __ldcg(q + i * kRowsItem);
+                  wt[k] = part + k > c1 ? 0.0f : part_weight(p, from, c0, ri, m);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  if (wt[k] != 0.0f)  // a part that saw nothing of this row holds no numbers
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      s[4 * i] = __fmaf_rn(x[k][i].x, wt[k], s[4 * i]);
+                      s[4 * i + 1] = __fmaf_rn(x[k][i].y, wt[k], s[4 * i + 1]);
+                      s[4 * i + 2] = __fmaf_rn(x[k][i].z, wt[k], s[4 * i + 2]);
+                      s[4 * i + 3] = __fmaf_rn(x[k][i].w, wt[k], s[4 * i + 3]);
+                    }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float* x = s + 8 * i;
+              *reinterpret_cast<uint4*>(mine_so + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(pack_bf16x2(x[0] * fo, x[1] * fo), pack_bf16x2(x[2] * fo, x[3] * fo),
+                             pack_bf16x2(x[4] * fo, x[5] * fo), pack_bf16x2(x[6] * fo, x[7] * fo));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int row32 = q * 8 + (lane >> 2);
+              const int at = __shfl_sync(kAll, to_row, row32);
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  mine_so + row32 * 64 + (((lane & 3) ^ ((row32 >> 1) & 3)) << 4));
+              if (at >= 0)
+                reinterpret_cast<uint4*>(p.out)[((int64_t)q0 * p.hq + at) * (D / 8) + 4 * c +
+                                                (lane & 3)] = v;
+            }
+            __syncwarp();
           }
         }
       }
