@@ -121,6 +121,7 @@ struct KvAttnParams {
   uint16_t* out;
   float* lse;
   int32_t few_rows;        // requests with at most so many rows per KV head go to kv_attn.cu
+  int32_t over_rows;       // ... those with more than so many, in one launch of it
   uint32_t* tickets;       // [kAttnTickets], zero between calls
   float* part;             // partial results, two records per CTA
   int32_t* status;
@@ -135,7 +136,7 @@ constexpr int kAttnTickets = kAttnMaxCtas + 8 * kPrefillMaxCtas;
 constexpr size_t kAttnPartBytes =
     (size_t)4 * std::max(2 * kAttnMaxCtas * kAttnRecord, 2 * kPrefillMaxCtas * kPrefillRecord);
 constexpr size_t kAttnWsBytes = (size_t)4 * kAttnTickets + kAttnPartBytes;
-cudaError_t launch_kv_few(const KvAttnParams& p, int D, cudaStream_t st);
+cudaError_t launch_kv_few(KvAttnParams p, int D, cudaStream_t st);
 cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, cudaStream_t st);
 
 }  // namespace nvfp4

@@ -25,7 +25,16 @@
 // An item cut between CTAs leaves a record (out, maximum, sum) per CTA in the
 // workspace, and the CTA that takes the item's last ticket joins the records
 // in order. Inside a CTA the warps take tiles in turn and join at the item's
-// end.
+// end. (With a CTA per item a call would last as long as its longest item does in one
+// CTA; cut evenly, 64 ragged requests run at the rate of 64 equal ones.)
+//
+// What bounds it: DRAM and the conversions together. A tile of 16 keys is 2304 bytes
+// and about 300 warp instructions, many of them conversions and byte moves on the ALU
+// pipe, which is half busy (issue slots 64%) at 78% of the measured copy rate. Measured, one row per
+// request, 8 KV heads, groups of 4, D = 128: 64 requests x 8192 tokens 110 us (5.50
+// TB/s, 81% of the measured copy rate); 64 ragged ones, 672 MB in all, 128 us (78%);
+// 256 x 500 tokens 46 us (48%: an item is 8 tiles per warp and each costs its set-up
+// and join); 4 requests of 300 to 1100 tokens 13.5 us (latency).
 //
 // Tile layout (m16n8k16, K or V as the 16-row operand, query rows as the 8
 // columns). Lane (g, t) = (lane / 4, lane % 4). Which token a K row index
@@ -51,7 +60,8 @@ constexpr int kStages = 4;  // tiles in flight per warp (cp.async groups)
 // A request this kernel takes.
 __device__ __forceinline__ Request few_rows(const KvAttnParams& p, int b, bool& bad) {
   Request r = request(p, b, bad);
-  if ((int64_t)r.n * p.G > p.few_rows) r.n = r.tiles = 0;
+  const int64_t rows = (int64_t)r.n * p.G;
+  if (rows <= p.over_rows || rows > p.few_rows) r.n = r.tiles = 0;
   return r;
 }
 
@@ -173,11 +183,16 @@ __device__ __noinline__ void join_records(const KvAttnParams& p, int q0, int h, 
   }
 }
 
-// CTAs resident per SM. Three leave 168 registers a thread and four 128: at D = 128
-// the loads and conversions of a tile overlap better with three (64 x 8192 tokens,
-// 8 KV heads: 112 us against 121), at D = 64 four are better (74 us against 78).
+// CTAs per SM that the compiler keeps registers for; as many run as then fit. For up
+// to 8 rows at D = 128 a bound of three is best: 128 registers are used, so four run,
+// but the loads and conversions of a tile overlap better than under a bound of four
+// (64 requests x 8192 tokens, 8 KV heads: 110 us, against 126 with four and 121 with
+// two; held to three resident ones it is 140). At D = 64 four: 72 us, against 77 with
+// three and 85 with five. Up to 16 rows: at D = 128 two (four rows a request: 156 us,
+// against 163 with three, and 359 with four, which spills), at D = 64 three (93 us,
+// against 105 with two and 106 with four).
 template <int D, int NT>
-constexpr int kCtasPerSm = D == 64 && NT == 1 ? 4 : 3;
+constexpr int kCtasPerSm = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
@@ -680,10 +695,25 @@ cudaError_t launch_t(const KvAttnParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_kv_few(const KvAttnParams& p, int D, cudaStream_t st) {
-  const bool one = (int64_t)p.max_q * p.G <= 8;
-  if (D == 128) return one ? launch_t<128, 1>(p, st) : launch_t<128, 2>(p, st);
-  return one ? launch_t<64, 1>(p, st) : launch_t<64, 2>(p, st);
+// Requests of up to 8 rows and of 9 to 16 differ in the columns of their products (one
+// row per request, 64 x 8192 tokens: 110 us with 8 columns, 152 with 16). Where a call
+// may hold prompts besides (more than 16 rows), requests of both kinds are to be
+// expected and each kind gets a launch (62 single rows at 8192 tokens with two prompts of
+// 300: 143 us, against 188 in one; an empty launch adds 2 us to prompts alone); drafted
+// tokens alone (16 rows at most) share the wider one.
+cudaError_t launch_kv_few(KvAttnParams p, int D, cudaStream_t st) {
+  const int64_t most = (int64_t)p.max_q * p.G;
+  auto one = [&] { return D == 128 ? launch_t<128, 1>(p, st) : launch_t<64, 1>(p, st); };
+  auto two = [&] { return D == 128 ? launch_t<128, 2>(p, st) : launch_t<64, 2>(p, st); };
+  p.over_rows = 0;
+  if (most <= 8) return one();
+  if (most <= kAttnRows) return two();
+  p.few_rows = 8;
+  const cudaError_t e = one();
+  if (e != cudaSuccess) return e;
+  p.over_rows = 8;
+  p.few_rows = kAttnRows;
+  return two();
 }
 
 }  // namespace nvfp4
