@@ -383,7 +383,9 @@ NVFP4_API nvfp4_status nvfp4_mx_quantize(const nvfp4_config* cfg, const void* x,
  * encodings: blocks of 16 along head_dim, E4M3 block scales, one FP32 outer
  * scale per KV head and tensor, g = amax / (6 M) as everywhere in this
  * library. The amax values are fixed when the cache is set up (calibrated:
- * tokens arrive over time and share them); larger values saturate. */
+ * tokens arrive over time and share them); larger values saturate.
+ * pages * page_size * kv_heads must be below 2^32 (rows are counted in 32
+ * bits; their byte offsets in 64). */
 typedef struct {
   uint8_t* k_codes;      /* [pages][kv_heads][page_size][head_dim/2]           */
   uint8_t* k_scales;     /* [pages][kv_heads][page_size][head_dim/16]          */
@@ -534,7 +536,8 @@ typedef struct {
  * Data errors: NVFP4_DEV_BAD_INDEX for a page outside the cache (page 0 stands
  * in for it), a seq_len past the table or q_start out of order or past
  * `tokens`, or more than max_q rows in a request (such a request is skipped);
- * NVFP4_DEV_NONFINITE_INPUT for NaN or Inf in q; NVFP4_DEV_BAD_AMAX.
+ * NVFP4_DEV_NONFINITE_INPUT for NaN or Inf in q; NVFP4_DEV_BAD_AMAX;
+ * NVFP4_DEV_TIMEOUT (results and workspace are then not valid).
  * Errors: NULL pointers, sizes out of range, head counts, head_dim, misaligned
  * pointers, a scale that is not finite (NVFP4_ERR_ENUM), and those of the
  * workspace (as nvfp4_amax_ws). */

@@ -30,11 +30,11 @@
 //
 // What bounds it: DRAM and the conversions together. A tile of 16 keys is 2304 bytes
 // and about 300 warp instructions, many of them conversions and byte moves on the ALU
-// pipe, which is half busy (issue slots 64%) at 78% of the measured copy rate. Measured, one row per
-// request, 8 KV heads, groups of 4, D = 128: 64 requests x 8192 tokens 110 us (5.50
-// TB/s, 81% of the measured copy rate); 64 ragged ones, 672 MB in all, 128 us (78%);
-// 256 x 500 tokens 46 us (48%: an item is 8 tiles per warp and each costs its set-up
-// and join); 4 requests of 300 to 1100 tokens 13.5 us (latency).
+// pipe, which is half busy (issue slots 64%) at 78% of the measured copy rate. Measured,
+// one row per request, 8 KV heads, groups of 4, D = 128: 64 requests x 8192 tokens 110
+// us (5.50 TB/s, 81% of that rate); 64 ragged ones, 672 MB in all, 128 us (78%); 256 x
+// 500 tokens 46 us (48%: an item is 8 tiles per warp and each costs its set-up and join);
+// 4 requests of 300 to 1100 tokens 13.5 us (latency).
 //
 // Tile layout (m16n8k16, K or V as the 16-row operand, query rows as the 8
 // columns). Lane (g, t) = (lane / 4, lane % 4). Which token a K row index

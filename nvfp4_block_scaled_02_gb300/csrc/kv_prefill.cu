@@ -25,6 +25,21 @@
 // per CTA; an item cut between CTAs is joined by the CTA that takes its last
 // ticket, in order.
 //
+// What bounds it: 4 D flops per query row and key on the tensor cores. 64 keys for
+// both tiles take 1600 clocks: 1280 of MMAs (1024 by their flops; with 64 keys per
+// product the operands' way out of shared memory sets the rate of Q K^T, 48 clocks
+// against 32) and a softmax of 1200 beside them, which wait for one another at times.
+// From one item to the next both tiles stand still (queries, first scores, last P V,
+// result: about 12000 clocks for an item of 34 key tiles). Prompts of 1500 to 2048
+// tokens behind 3000 to 10000 (4 requests, 32 query heads on 8, D = 128; 585 GFLOP): 445
+// us, 1.31 PFLOP/s, 68% of the measured cuBLAS rate; 300 tokens alone, of one request:
+// 30 us, all of it latency.
+//
+// Why 64 keys per product and two S per tile: with one S of 128 columns per tile the
+// softmax and the MMAs of a tile take turns and it took 545 us where this form then took
+// 515. Why short loops outside the step: the kernel has to stay in the instruction
+// cache; with everything unrolled (195 KB of code, now 87) it took 497 us.
+//
 // Every wait has a limit: when it runs out the CTA sets NVFP4_DEV_TIMEOUT, its
 // other waits return at once, and it frees its tensor memory and ends.
 #include "kv_attn.cuh"
@@ -47,7 +62,7 @@ constexpr long long kWaitCycles = 2000000000;  // about a second
 constexpr uint32_t kNegInf = 0xFF800000u;
 
 __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* dead,
-                                       int32_t* status) {
+                                          int32_t* status) {
   const long long t0 = clock64();
   while (!mbar_try(b, parity)) {
     if (*dead) return false;
@@ -97,7 +112,8 @@ __device__ __forceinline__ Tiles block_tiles(const KvAttnParams& p, const Reques
   const int hi = r.len - r.n + (int)fastdiv((uint32_t)last, p.by_group) + 1;
   int begin = 0;
   if (p.window > 0) {
-    const int low = r.len - r.n + (int)fastdiv((uint32_t)(pt * kRowsItem), p.by_group) + 1 - min(p.window, r.len);
+    const int low = r.len - r.n + (int)fastdiv((uint32_t)(pt * kRowsItem), p.by_group) + 1 -
+                    min(p.window, r.len);
     begin = max(0, low - r.lo16) / kTileN;
   }
   return {begin, max(1, (hi - r.lo16 + kTileN - 1) / kTileN - begin)};
@@ -125,8 +141,8 @@ struct Walk {
   int64_t skip;  // tiles before pos, counted from (b, h, pt)
   int b, h, pt, blocks;
   Request r;
-  __device__ __forceinline__ void start(const KvAttnParams& p, int64_t first, int64_t end, int64_t per_cta, int b0,
-                        int64_t off, int64_t per_head) {
+  __device__ __forceinline__ void start(const KvAttnParams& p, int64_t first, int64_t end,
+                                        int64_t per_cta, int b0, int64_t off, int64_t per_head) {
     pos = first;
     run = per_cta;
     last = end;
@@ -192,7 +208,9 @@ __device__ __forceinline__ float load_queries(const KvAttnParams& p, const Item&
   const int rows = x.r.n * p.G, first_row = x.row0 + tile * kRowsTile + w * 32;
   dst += w * 32 * 128;
   // chunk c of row i
-  auto at = [&](int i, int c) { return dst + (c >> 3) * (128 * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4); };
+  auto at = [&](int i, int c) {
+    return dst + (c >> 3) * (128 * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4);
+  };
   {
     const int c = lane % LPR;
     const uint16_t* from = p.q + (int64_t)x.r.q0 * p.q_st + (int64_t)(x.h * p.G) * D + c * 8;
@@ -209,7 +227,8 @@ __device__ __forceinline__ float load_queries(const KvAttnParams& p, const Item&
   __syncwarp();
   uint32_t m = 0;
 #pragma unroll 4
-  for (int c = 0; c < LPR; ++c) m = max(m, absmax_bits4(*reinterpret_cast<const uint4*>(at(lane, c))));
+  for (int c = 0; c < LPR; ++c)
+    m = max(m, absmax_bits4(*reinterpret_cast<const uint4*>(at(lane, c))));
   if (m >= 0x7F80u) flag(p.status, NVFP4_DEV_NONFINITE_INPUT_BIT);
   // 2^e brings the row's largest element to [2^13, 2^14)
   const int e = min(max(13 - ((int)(m >> 7) - 127), -126), 126);

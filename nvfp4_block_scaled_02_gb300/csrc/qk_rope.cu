@@ -12,7 +12,11 @@
 // either way a pair never leaves its lane, four angles serve eight values, and the
 // rotation needs no shuffle. A warp takes several heads of one token in a row, so
 // that the token's angles stay in registers. Both directions are bound by DRAM: 4
-// (forward) and 6 (backward) bytes per value.
+// (forward) and 6 (backward) bytes per value. Measured at 40 heads of 128, normed:
+// forward 8192 tokens 29.9 us (5.75 TB/s, 85% of the measured copy rate), 32 tokens 2.0
+// us; gradient 8192 tokens 54.7 us (4.68 TB/s, 69%), 65536 tokens 368 us (82%): about 9
+// us of a call go into the weights' gradients once, over warps, CTAs and then in the
+// last CTA, whatever the number of tokens.
 #include "kv.h"
 
 namespace nvfp4 {
