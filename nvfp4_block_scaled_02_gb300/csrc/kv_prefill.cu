@@ -51,8 +51,8 @@ namespace {
 
 constexpr int kThreads = 512;  // 4 warpgroups
 // Registers per thread: the softmax keeps a whole row of scores. Two softmax
-// warpgroups, one that dequantises, one that issues: 2 x 184 + 80 + 64 = 4 x 128.
-constexpr int kRegsSoftmax = 184, kRegsDequant = 80, kRegsMma = 64;
+// warpgroups, one that dequantises, one that issues: 2 x 184 + 88 + 56 = 4 x 128.
+constexpr int kRegsSoftmax = 184, kRegsDequant = 88, kRegsMma = 56;
 static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsMma <= 4 * 128, "the block's registers");
 constexpr int kTileN = 128;    // keys per tile (dequantised together)
 constexpr int kStepN = 64;     // keys per product
