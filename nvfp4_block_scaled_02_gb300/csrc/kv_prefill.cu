@@ -21,8 +21,8 @@
 // codes into 32 f16 values each, in the 128-byte-swizzled layout the tensor
 // cores read (K rows along k, V rows along n).
 //
-// Work split: as in kv_attn.cu, the items' key tiles are cut into equal runs, one
-// per CTA; an item cut between CTAs is joined by the CTA that takes its last
+// Work split: as in kv_attn.cu, the items' key tiles, and what an item costs beside
+// them, are cut into equal runs, one per CTA; an item cut between CTAs is joined by the CTA that takes its last
 // ticket, in order.
 //
 // What bounds it: 4 D flops per query row and key on the tensor cores. 64 keys for
@@ -31,14 +31,16 @@
 // against 32) and a softmax of 1200 beside them, which wait for one another at times.
 // From one item to the next both tiles stand still (queries, first scores, last P V,
 // result: about 12000 clocks for an item of 34 key tiles). Prompts of 1500 to 2048
-// tokens behind 3000 to 10000 (4 requests, 32 query heads on 8, D = 128; 585 GFLOP): 445
-// us, 1.31 PFLOP/s, 68% of the measured cuBLAS rate; 300 tokens alone, of one request:
-// 30 us, all of it latency.
+// tokens behind 3000 to 10000 (4 requests, 32 query heads on 8, D = 128; 585 GFLOP): 413
+// us, 1.42 PFLOP/s, 74% of the measured cuBLAS rate; one prompt of 8192 tokens: 405 us,
+// 1.36 PFLOP/s; one of 300: 26 us, all of it latency.
 //
 // Why 64 keys per product and two S per tile: with one S of 128 columns per tile the
 // softmax and the MMAs of a tile take turns and it took 545 us where this form then took
-// 515. Why short loops outside the step: the kernel has to stay in the instruction
-// cache; with everything unrolled (195 KB of code, now 87) it took 497 us.
+// 515. Why one warpgroup that dequantises: two of them (640 threads) leave the softmax 152
+// registers and took 462 us where one takes 413. Why short loops outside the step: the kernel has to stay in the instruction
+// cache; with everything unrolled (195 KB of code, now 87) it took 497 us
+// where it then took 445.
 //
 // Every wait has a limit: when it runs out the CTA sets NVFP4_DEV_TIMEOUT, its
 // other waits return at once, and it frees its tensor memory and ends.
@@ -58,6 +60,10 @@ constexpr int kTileN = 128;    // keys per tile (dequantised together)
 constexpr int kStepN = 64;     // keys per product
 constexpr int kRowsTile = 128, kRowsItem = 256;
 constexpr int kItems = 4;      // items handed out ahead
+// What an item costs beside its tiles (queries, first scores, result), in tiles: without
+// it the CTA whose run holds the most short items ends last (one prompt of 8192 tokens:
+// 510 us with 0, 441 with 2, 405 with 4, 413 with 6; 16 prompts of 512: 102, 101, 92, 98).
+constexpr int kItemCost = 4;
 constexpr long long kWaitCycles = 2000000000;  // about a second
 constexpr uint32_t kNegInf = 0xFF800000u;
 
@@ -118,11 +124,13 @@ __device__ __forceinline__ Tiles block_tiles(const KvAttnParams& p, const Reques
   }
   return {begin, max(1, (hi - r.lo16 + kTileN - 1) / kTileN - begin)};
 }
-__device__ __forceinline__ int64_t request_tiles(const KvAttnParams& p, const Request& r) {
+// A run is counted in units: kItemCost for the item (nothing runs in them), then one
+// per tile.
+__device__ __forceinline__ int64_t request_units(const KvAttnParams& p, const Request& r) {
   int64_t c = 0;
   const int n = row_blocks(p, r);
 #pragma unroll 1
-  for (int pt = 0; pt < n; ++pt) c += block_tiles(p, r, pt).count;
+  for (int pt = 0; pt < n; ++pt) c += block_tiles(p, r, pt).count + kItemCost;
   return c * p.hk;
 }
 
@@ -134,11 +142,11 @@ struct Item {
   int c0, c1;     // the CTAs that share it
 };
 
-// The items of this CTA's run [pos, last) of tiles, in the same order in every
+// The items of this CTA's run [pos, last) of units, in the same order in every
 // warp: row blocks inside heads inside requests.
 struct Walk {
   int64_t pos, last, run;
-  int64_t skip;  // tiles before pos, counted from (b, h, pt)
+  int64_t skip;  // units before pos, counted from (b, h, pt)
   int b, h, pt, blocks;
   Request r;
   __device__ __forceinline__ void start(const KvAttnParams& p, int64_t first, int64_t end,
@@ -169,27 +177,30 @@ struct Walk {
         continue;
       }
       const Tiles t = block_tiles(p, r, pt);
-      if (skip >= t.count) {
-        skip -= t.count;
+      const int units = t.count + kItemCost;
+      if (skip >= units) {
+        skip -= units;
         ++pt;
         continue;
       }
-      const int count = (int)min((int64_t)t.count - skip, last - pos);
+      const int64_t item = pos - skip;
+      const int from = (int)skip, count = (int)min((int64_t)units - skip, last - pos);
+      pos += count;
+      skip += count;
+      if (from + count <= kItemCost) continue;  // none of its tiles
       it.r = r;
       it.b = b;
       it.h = h;
       it.row0 = pt * kRowsItem;
       it.rows = min(kRowsItem, r.n * p.G - it.row0);
-      it.t0 = t.begin + (int)skip;
-      it.t1 = it.t0 + count;
-      it.c0 = (int)((pos - skip) / run);
-      it.c1 = (int)((pos - skip + t.count - 1) / run);
+      it.t0 = t.begin + max(from - kItemCost, 0);
+      it.t1 = t.begin + from + count - kItemCost;
+      it.c0 = (int)((item + kItemCost) / run);
+      it.c1 = (int)((item + units - 1) / run);
       const SliceScale ks = slice_scale(p.k_amax[h], p.M), vs = slice_scale(p.v_amax[h], p.M);
       if (ks.bad || vs.bad) flag(p.status, NVFP4_DEV_BAD_AMAX_BIT);
       it.kg = ks.g;
       it.vg = vs.g;
-      pos += count;
-      skip += count;
       return true;
     }
     return false;
@@ -294,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     bool bad;
     const Request r = many_rows(p, b, bad);
     if (bad && blockIdx.x == 0) flag(p.status, kDevBadIndex);
-    mine += request_tiles(p, r);
+    mine += request_units(p, r);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -339,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll 1
     for (int b = rb0; b < rb1; ++b) {
       bool bad;
-      const int64_t c = request_tiles(p, many_rows(p, b, bad));
+      const int64_t c = request_units(p, many_rows(p, b, bad));
       if (first < at + c) {
         s_b0 = b;
         s_off = first - at;
