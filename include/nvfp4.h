@@ -538,9 +538,9 @@ typedef struct {
  * `tokens`, or more than max_q rows in a request (such a request is skipped);
  * NVFP4_DEV_NONFINITE_INPUT for NaN or Inf in q; NVFP4_DEV_BAD_AMAX;
  * NVFP4_DEV_TIMEOUT (results and workspace are then not valid).
- * Errors: NULL pointers, sizes out of range, head counts, head_dim, misaligned
- * pointers, a scale that is not finite (NVFP4_ERR_ENUM), and those of the
- * workspace (as nvfp4_amax_ws). */
+ * Errors: NULL pointers, sizes out of range (more than 2^30 requests among
+ * them), head counts, head_dim, misaligned pointers, a scale that is not finite
+ * (NVFP4_ERR_ENUM), and those of the workspace (as nvfp4_amax_ws). */
 NVFP4_API size_t nvfp4_kv_attention_ws_bytes(void);
 NVFP4_API nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache,
                                           const nvfp4_attention_config* cfg, nvfp4_rows q,

@@ -239,7 +239,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const nvfp4_attenti
   if (e != NVFP4_OK) return e;
   if (!cfg) return NVFP4_ERR_NULL;
   const int64_t group = cfg->q_heads / std::max(cache->kv_heads, 1);
-  if (cfg->requests < 0 || cfg->requests >= kMaxI32 || cfg->table_cols < 0 ||
+  if (cfg->requests < 0 || cfg->requests > (1 << 30) || cfg->table_cols < 0 ||
       cfg->table_cols > kMaxI32 || cfg->tokens < 0 || cfg->tokens > kMaxI32 || cfg->max_q < 0 ||
       cfg->window < 0 || cfg->q_heads < 1 || cfg->q_heads > kMaxHeads ||
       cfg->q_heads % cache->kv_heads != 0 || cfg->max_q * group > kMaxI32 - 1024 ||

@@ -37,10 +37,11 @@
 //
 // Why 64 keys per product and two S per tile: with one S of 128 columns per tile the
 // softmax and the MMAs of a tile take turns and it took 545 us where this form then took
-// 515. Why one warpgroup that dequantises: two of them (640 threads) leave the softmax 152
-// registers and took 462 us where one takes 413. Why short loops outside the step: the kernel has to stay in the instruction
-// cache; with everything unrolled (195 KB of code, now 87) it took 497 us
-// where it then took 445.
+// 515. Why one warpgroup that dequantises: two of them (640 threads) leave the softmax
+// 152 registers and took 462 us where one takes 413. Why K and V are handed over 128 keys
+// at a time: 64 at a time (finer barriers, the same buffers) took 517 us where this takes
+// 413. Why short loops outside the step: the kernel has to stay in the instruction cache;
+// with everything unrolled (195 KB of code, now 87) it took 497 us where it then took 445.
 //
 // Every wait has a limit: when it runs out the CTA sets NVFP4_DEV_TIMEOUT, its
 // other waits return at once, and it frees its tensor memory and ends.
@@ -125,13 +126,25 @@ __device__ __forceinline__ Tiles block_tiles(const KvAttnParams& p, const Reques
   return {begin, max(1, (hi - r.lo16 + kTileN - 1) / kTileN - begin)};
 }
 // A run is counted in units: kItemCost for the item (nothing runs in them), then one
-// per tile.
-__device__ __forceinline__ int64_t request_units(const KvAttnParams& p, const Request& r) {
+// per tile. Those of the request's row blocks first, first + step, ..., all heads:
+__device__ __forceinline__ int64_t request_units(const KvAttnParams& p, const Request& r,
+                                                 int first, int step) {
   int64_t c = 0;
   const int n = row_blocks(p, r);
 #pragma unroll 1
-  for (int pt = 0; pt < n; ++pt) c += block_tiles(p, r, pt).count + kItemCost;
+  for (int pt = first; pt < n; pt += step) c += block_tiles(p, r, pt).count + kItemCost;
   return c * p.hk;
+}
+
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(kAll, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
 }
 
 struct Item {
@@ -297,22 +310,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
 
   // ---- this CTA's run -------------------------------------------------------
-  const int share = (p.B + kThreads - 1) / kThreads;
-  const int rb0 = min(tid * share, p.B), rb1 = min(rb0 + share, p.B);
+  // `per` threads to a request (one to several requests where there are many)
+  int per = 32;
+  while (per > 1 && (int64_t)p.B * per > kThreads) per >>= 1;
+  const int share = (p.B - 1) / (kThreads / per) + 1;
+  const int rb0 = min(tid / per * share, p.B), rb1 = min(rb0 + share, p.B);
   int64_t mine = 0;
 #pragma unroll 1
   for (int b = rb0; b < rb1; ++b) {
     bool bad;
     const Request r = many_rows(p, b, bad);
     if (bad && blockIdx.x == 0) flag(p.status, kDevBadIndex);
-    mine += request_units(p, r);
+    mine += request_units(p, r, tid % per, per);
   }
-  int64_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(kAll, incl, d);
-    if (lane >= d) incl += o;
-  }
+  for (int d = per >> 1; d > 0; d >>= 1) mine += __shfl_xor_sync(kAll, mine, d);
+  if (tid % per != 0) mine = 0;  // the group's first thread has the sum
+  int64_t incl = warp_scan(mine);
   if (lane == 31) s_scan[warp] = incl;
   if (tid == 0) {
     s_dead = 0;
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll 1
     for (int b = rb0; b < rb1; ++b) {
       bool bad;
-      const int64_t c = request_units(p, many_rows(p, b, bad));
+      const int64_t c = share == 1 ? mine : request_units(p, many_rows(p, b, bad), 0, 1);
       if (first < at + c) {
         s_b0 = b;
         s_off = first - at;

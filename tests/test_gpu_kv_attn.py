@@ -226,3 +226,25 @@ def test_rows_no_request_owns_are_left_alone():
     nv.nvfp4_kv_attention(pad, *rest, out=out, lse=lse)
     want = _go(s)
     assert torch.equal(out[:3], want["out"]) and (out[3:] == 7).all() and (lse[3:] == 7).all()
+
+
+@pytest.mark.parametrize("requests", [15, 17, 40, 130, 700])
+def test_batches_of_every_kind_of_request(requests):
+    """Single rows, up to 8, 9 to 16 and more rows per KV head, empty requests, one without
+    keys and rows before the first key in one call: fewer and more requests than
+    threads share the work of finding them."""
+    r = np.random.default_rng(requests)
+    new = np.resize([1, 0, 3, 17, 5, 20, 8, 2, 33, 1, 140], requests)
+    total = new + r.integers(0, 60, requests)
+    total[4] = 0
+    total[3::11] = 10  # 17 rows, 10 keys
+    _check(_go(_state(new, total, 2, 1, 64, 16, 5)), _ref(_state(new, total, 2, 1, 64, 16, 5), 64 ** -0.5, 0))
+
+
+@pytest.mark.parametrize("window", [0, 300])
+def test_a_long_prompt_among_short_ones(window):
+    """Items of very different lengths: the runs are cut inside long ones and hold many
+    short ones."""
+    new, total = [1100, 17, 40, 1, 300, 18], [1500, 17, 45, 900, 300, 2000]
+    s = _state(new, total, 8, 2, 128, 32, 9)
+    _check(_go(s, window=window), _ref(s, 128 ** -0.5, window))
