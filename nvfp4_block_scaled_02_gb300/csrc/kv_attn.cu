@@ -20,7 +20,7 @@
 // 2^(kBias + kSlack) is far from f16's largest value.
 //
 // Work split. A query row block (the rows of one request that share a KV head)
-// and its tiles of 16 tokens form an item; all items' tiles, one after the
+// and its tiles of 16 tokens form an item; all items' costs and tiles, one after the
 // other, are cut into equal runs, one per CTA, whatever the requests' lengths.
 // An item cut between CTAs leaves a record (out, maximum, sum) per CTA in the
 // workspace, and the CTA that takes the item's last ticket joins the records
@@ -32,9 +32,9 @@
 // and about 300 warp instructions, many of them conversions and byte moves on the ALU
 // pipe, which is half busy (issue slots 64%) at 78% of the measured copy rate. Measured,
 // one row per request, 8 KV heads, groups of 4, D = 128: 64 requests x 8192 tokens 110
-// us (5.50 TB/s, 81% of that rate); 64 ragged ones, 672 MB in all, 128 us (78%); 256 x
-// 500 tokens 46 us (48%: an item is 8 tiles per warp and each costs its set-up and join);
-// 4 requests of 300 to 1100 tokens 13.5 us (latency).
+// us (5.50 TB/s, 81% of that rate); 64 ragged ones, 672 MB in all, 120 us (83%); 256 x
+// 500 tokens 45 us (50%: an item is 8 tiles per warp and each costs its set-up and join);
+// 4 requests of 300 to 1100 tokens 10.2 us (latency).
 //
 // Tile layout (m16n8k16, K or V as the 16-row operand, query rows as the 8
 // columns). Lane (g, t) = (lane / 4, lane % 4). Which token a K row index
@@ -56,6 +56,12 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+// What an item costs beside its tiles (set-up and joins), in tiles. Without it the CTAs
+// whose runs hold the most short items end last (256 requests of 16 to 16384 tokens, log-
+// uniform: 188 us with 0, 161 with 8, 140 with 16, 139 with 24; 200 of 300 with 16 of
+// 8192: 68, 57, 56, 60), and short items are cut for nothing (4 requests of 300 to 1100:
+// 13.5 us with 0, 10.5 with the others).
+constexpr int kItemCost = 16;
 constexpr int kStages = 4;  // tiles in flight per warp (cp.async groups)
 // A request this kernel takes.
 __device__ __forceinline__ Request few_rows(const KvAttnParams& p, int b, bool& bad) {
@@ -63,6 +69,11 @@ __device__ __forceinline__ Request few_rows(const KvAttnParams& p, int b, bool& 
   const int64_t rows = (int64_t)r.n * p.G;
   if (rows <= p.over_rows || rows > p.few_rows) r.n = r.tiles = 0;
   return r;
+}
+
+// A run is counted in units: kItemCost for an item, then one per tile.
+__device__ __forceinline__ int units(const Request& r) {
+  return r.tiles > 0 ? r.tiles + kItemCost : 0;
 }
 
 template <int D>
@@ -187,7 +198,7 @@ __device__ __noinline__ void join_records(const KvAttnParams& p, int q0, int h, 
 // to 8 rows at D = 128 a bound of three is best: 128 registers are used, so four run,
 // but the loads and conversions of a tile overlap better than under a bound of four
 // (64 requests x 8192 tokens, 8 KV heads: 110 us, against 126 with four and 121 with
-// two; held to three resident ones it is 140). At D = 64 four: 72 us, against 77 with
+// two; held to three resident ones it is 140). At D = 64 four: 75 us, against 76 with
 // three and 85 with five. Up to 16 rows: at D = 128 two (four rows a request: 156 us,
 // against 163 with three, and 359 with four, which spills), at D = 64 three (93 us,
 // against 105 with two and 106 with four).
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     bool bad;
     const Request r = few_rows(p, b, bad);
     if (bad && blockIdx.x == 0) flag(p.status, kDevBadIndex);
-    mine += (int64_t)r.tiles * p.hk;
+    mine += (int64_t)units(r) * p.hk;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -238,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     if (w < warp) incl += s_scan[w];
     total += s_scan[w];
   }
-  // equal runs, 8 tiles (two per warp) at least
+  // equal runs, 8 units at least
   const int64_t run = max((total + ctas - 1) / ctas, (int64_t)(2 * kWarps));
   const int64_t first = (int64_t)blockIdx.x * run, last = min(first + run, total);
   if (first < last && incl - mine <= first && first < incl) {
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     for (int b = rb0; b < rb1; ++b) {
       bool bad;
       const Request r = few_rows(p, b, bad);
-      const int64_t c = (int64_t)r.tiles * p.hk;
+      const int64_t c = (int64_t)units(r) * p.hk;
       if (first < at + c) {
         s_b0 = b;
         s_off = first - at;
@@ -277,29 +288,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
   seg.b = s_b0;
   bool bad0;
   seg.r = few_rows(p, seg.b, bad0);
-  seg.h = (int)(s_off / seg.r.tiles);
-  seg.t0 = (int)(s_off - (int64_t)seg.h * seg.r.tiles);
-  seg.t1 = (int)min((int64_t)seg.r.tiles, seg.t0 + (last - pos));
-  pos += seg.t1 - seg.t0;
+  seg.h = (int)(s_off / units(seg.r));
+  auto take = [&](Segment& s, int from) -> bool {  // its tiles from unit `from` on; any?
+    const int more = (int)min((int64_t)units(s.r) - from, last - pos);
+    pos += more;
+    s.t0 = max(from - kItemCost, 0);
+    s.t1 = from + more - kItemCost;
+    return s.t1 > s.t0;
+  };
   auto next = [&](Segment& s) -> bool {  // the one after s, which it replaces
     if (pos >= last) return false;
-    if (s.t1 == s.r.tiles) {
-      s.t1 = 0;
-      if (++s.h == p.hk) {
-        s.h = 0;
-        do {
-          if (++s.b >= p.B) return false;
-          bool bad;
-          s.r = few_rows(p, s.b, bad);
-        } while (s.r.tiles == 0);
-      }
+    if (++s.h == p.hk) {
+      s.h = 0;
+      do {
+        if (++s.b >= p.B) return false;
+        bool bad;
+        s.r = few_rows(p, s.b, bad);
+      } while (s.r.tiles == 0);
     }
-    s.t0 = s.t1;
-    s.t1 = (int)min((int64_t)s.r.tiles, s.t0 + (last - pos));
-    pos += s.t1 - s.t0;
-    return true;
+    return take(s, 0);
   };
-
+  // (false: the run ends before its only item's tiles begin)
+  if (!take(seg, (int)(s_off - (int64_t)seg.h * units(seg.r)))) return;
   // A segment's tile j is this warp's when j = t0 + warp mod 4. Lane l holds the
   // cache row of the first key of its l-th tile from `from` on: one table look-up
   // for 32 tiles, well before the copies that need it.
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     const Request r = seg.r;
     const int h = seg.h, t0 = seg.t0, t1 = seg.t1;
     if (!kAhead) load_q(seg);
-    const int64_t item_first = pos - (t1 - t0) - t0, item_last = item_first + r.tiles - 1;
+    const int64_t item_first = pos - t1, item_last = item_first + r.tiles - 1;  // its tiles' units
     const int nrows = r.n * p.G;
     Segment cur = seg;
     have = next(seg);
