@@ -14,7 +14,7 @@
 // that the token's angles stay in registers. Both directions are bound by DRAM: 4
 // (forward) and 6 (backward) bytes per value. Measured at 40 heads of 128, normed:
 // forward 8192 tokens 29.9 us (5.75 TB/s, 85% of the measured copy rate), 32 tokens 2.0
-// us; gradient 8192 tokens 54.7 us (4.68 TB/s, 69%), 65536 tokens 368 us (82%): about 9
+// us; gradient 8192 tokens 54.5 us (4.69 TB/s, 69%), 65536 tokens 365 us (83%): about 5
 // us of a call go into the weights' gradients once, over warps, CTAs and then in the
 // last CTA, whatever the number of tokens.
 #include "kv.h"
@@ -25,7 +25,10 @@ namespace {
 
 constexpr int kThreads = 256;      // forward
 constexpr int kWarps = kThreads / 32;
-constexpr int kThreadsBwd = 512;   // one CTA per SM: half the rows of sums to add up at the end
+// Gradient: one CTA per SM (half the rows of sums to add up at the end), with 128
+// registers a thread for four heads in flight (8192 tokens: 54.5 us; two in flight 62;
+// 384 threads 63; 640, 768 and 1024 spill: 59 to 82).
+constexpr int kThreadsBwd = 512;
 constexpr int kWarpsBwd = kThreadsBwd / 32;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kBatch = 4;  // steps whose loads are in flight together
