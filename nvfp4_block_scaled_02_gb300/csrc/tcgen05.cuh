@@ -106,7 +106,7 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// ------------------------------------------------------- register budget ---
+// ------------------------------------------------------- register shares ---
 // A warpgroup's share of the registers that the block was launched with.
 template <int N>
 __device__ __forceinline__ void more_registers() {
