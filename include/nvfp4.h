@@ -510,10 +510,12 @@ NVFP4_API nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, nvfp4_rows k
  * window. Query head h reads KV head h / (q_heads / kv_heads).
  *   out = softmax(scale * q . K^T) V,  lse = log(sum(exp(scale * q . K^T)))
  * A row that sees no key (an empty request, or n > seq_len) gets out = 0 and
- * lse = -infinity. What the cache holds past seq_len or outside the window
- * does not matter, NaN scale bytes included. Accumulation, softmax statistics
- * and partial results are fp32; K and V enter the products exactly, the
- * probabilities rounded to f16. */
+ * lse = -infinity. What the cache holds past seq_len, and of the keys that a
+ * row does not see, does not matter to that row, NaN scale bytes included. A row
+ * that sees a key whose V has a NaN scale gets NaN in the 16 values of that
+ * block; with a NaN scale in its K, everywhere and in lse. Accumulation, softmax
+ * statistics and partial results are fp32; K and V enter the products exactly,
+ * the probabilities rounded to f16. */
 typedef struct {
   const int32_t* block_table;  /* int32 [requests][table_cols]                   */
   const int32_t* seq_len;      /* int32 [requests]                               */

@@ -31,10 +31,10 @@
 // What bounds it: DRAM and the conversions together. A tile of 16 keys is 2304 bytes
 // and about 300 warp instructions, many of them conversions and byte moves on the ALU
 // pipe, which is half busy (issue slots 64%) at 78% of the measured copy rate. Measured,
-// one row per request, 8 KV heads, groups of 4, D = 128: 64 requests x 8192 tokens 110
-// us (5.50 TB/s, 81% of that rate); 64 ragged ones, 672 MB in all, 120 us (83%); 256 x
+// one row per request, 8 KV heads, groups of 4, D = 128: 64 requests x 8192 tokens 109
+// us (5.54 TB/s, 82% of that rate); 64 ragged ones, 672 MB in all, 121 us (82%); 256 x
 // 500 tokens 45 us (50%: an item is 8 tiles per warp and each costs its set-up and join);
-// 4 requests of 300 to 1100 tokens 10.2 us (latency).
+// 4 requests of 300 to 1100 tokens 9.8 us (latency).
 //
 // Tile layout (m16n8k16, K or V as the 16-row operand, query rows as the 8
 // columns). Lane (g, t) = (lane / 4, lane % 4). Which token a K row index
@@ -46,6 +46,7 @@
 // 8x8 transpose between lanes. Two V bytes of neighbouring tokens are merged
 // to (even nibbles) and (odd nibbles) before conversion, so that a converted
 // pair holds one dimension of two tokens, as the operand wants.
+#include <cmath>
 #include <cstddef>
 
 #include "kv_attn.cuh"
@@ -194,14 +195,50 @@ __device__ __noinline__ void join_records(const KvAttnParams& p, int q0, int h, 
   }
 }
 
+// NaN into the outputs of the rows that see a key with a NaN scale in the block of V that
+// this lane holds, among the keys of this warp's tiles of a segment. `dst`: row 2 t of the
+// warp's outputs in shared memory. Rare, and kept out of the tile loop's registers: the
+// cache is read again.
+template <int D, int NT>
+__device__ __noinline__ void put_nan(const KvAttnParams& p, float* dst, const Segment& s) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int block = g / (128 / D), nrows = s.r.n * p.G;
+  uint32_t hit = 0;  // bit 2 nt + i: row 8 nt + 2 t + i
+#pragma unroll 1
+  for (int j = s.t0 + (threadIdx.x >> 5); j < s.t1; j += kWarps) {
+    const int tok = s.r.lo16 + j * 16, pg = (int)fastdiv((uint32_t)tok, p.by_page);
+    int64_t page = p.table[(int64_t)s.b * p.cols + pg];
+    if (page < 0 || page >= p.pages) page = 0;
+    const uint64_t row = (uint64_t)((page * p.hk + s.h) * p.P + (tok - pg * p.P));
+#pragma unroll 1
+    for (int key = tok; key < min(tok + 16, s.r.len); ++key) {
+      if ((p.vs[(row + (key - tok)) * (D / 16) + block] & 0x7F) != 0x7F) continue;
+#pragma unroll 1
+      for (int c = 0; c < 2 * NT; ++c) {
+        const int rr = (c >> 1) * 8 + 2 * t + (c & 1);
+        const int lim = s.r.len - s.r.n + (int)fastdiv((uint32_t)rr, p.by_group) + 1;
+        if (rr < nrows && key < lim && (p.window == 0 || key >= lim - min(p.window, s.r.len)))
+          hit |= 1u << c;
+      }
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < 2 * NT; ++c)
+    if (hit >> c & 1)
+      for (int q = g * (D / 32); q < (g + 1) * (D / 32); ++q)
+        *reinterpret_cast<float4*>(dst + ((c >> 1) * 8 + (c & 1)) * kJoinRow<D> + join_at<D>(q)) =
+            make_float4(NAN, NAN, NAN, NAN);
+}
+
 // CTAs per SM that the compiler keeps registers for; as many run as then fit. For up
-// to 8 rows at D = 128 a bound of three is best: 128 registers are used, so four run,
-// but the loads and conversions of a tile overlap better than under a bound of four
-// (64 requests x 8192 tokens, 8 KV heads: 110 us, against 126 with four and 121 with
-// two; held to three resident ones it is 140). At D = 64 four: 75 us, against 76 with
-// three and 85 with five. Up to 16 rows: at D = 128 two (four rows a request: 156 us,
-// against 163 with three, and 359 with four, which spills), at D = 64 three (93 us,
-// against 105 with two and 106 with four).
+// to 8 rows at D = 128 a bound of three is best (145 registers): the loads and
+// conversions of a tile overlap better than under a bound of four (64 requests x 8192
+// tokens, 8 KV heads: 109 us, against 122 with four, and 113 to 117 held to 160 to 136
+// registers). At D = 64 four: 75 us, against 76 with three and 85 with five. Up to 16
+// rows: at D = 128 two (four rows a request: 153 us, against 163 with three, and 359
+// with four, which spills), at D = 64 three (95 us, against 105 with two and 106 with
+// four). Loading an item's queries under the one before it took registers from the tile
+// loop and was no faster (64 x 8192: 112 us).
 template <int D, int NT>
 constexpr int kCtasPerSm = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
 
@@ -221,6 +258,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
   __shared__ int s_b0;
   __shared__ int64_t s_off;
   __shared__ uint32_t s_ticket;
+  __shared__ int s_nan[kWarps];  // a warp has left NaN blocks of V out of its products
+  __shared__ Segment s_seg[kWarps];  // ... of this segment
 
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(kAll, tid >> 5, 0);
@@ -242,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     if (lane >= d) incl += o;
   }
   if (lane == 31) s_scan[warp] = incl;
+  if (lane == 0) s_nan[warp] = 0;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
@@ -381,9 +421,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
 
   // The query rows of a segment's item as they are in memory (column n of row tile
   // nt is row 8 nt + n = (token, head of the group)), and its heads' amax.
-  // Loaded an item ahead where the registers allow it: two row tiles would spill, and
-  // at D = 64 the fourth CTA is worth more (73 us against 77).
-  constexpr bool kAhead = NT == 1 && D == 128;
   uint4 raw[NT][DQ / 8];
   float k_amax = 0.0f, v_amax = 0.0f;
   auto load_q = [&](const Segment& s) {
@@ -402,7 +439,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
   };
 
   uint32_t rows = look_up(seg, seg.t0 + warp);
-  if (kAhead) load_q(seg);
   begin(seg, rows);
   bool have = true;
   while (have) {
@@ -410,10 +446,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     // while this one's results are joined
     const Request r = seg.r;
     const int h = seg.h, t0 = seg.t0, t1 = seg.t1;
-    if (!kAhead) load_q(seg);
+    load_q(seg);
     const int64_t item_first = pos - t1, item_last = item_first + r.tiles - 1;  // its tiles' units
     const int nrows = r.n * p.G;
-    Segment cur = seg;
+    if (lane == 0) s_seg[warp] = seg;
+    __syncwarp();
     have = next(seg);
     uint32_t next_rows = have ? look_up(seg, seg.t0 + warp) : 0;
 
@@ -450,7 +487,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
         lim[nt][i] = rr < nrows ? r.len - r.n + (int)fastdiv((uint32_t)rr, p.by_group) + 1 : 0;
       }
     }
-    if (kAhead && have) load_q(seg);  // the next item's
     const int lim_min = r.len - r.n + 1;  // keys below are seen by every row
     const int low_max = p.window > 0 ? r.len - min(p.window, r.len) : 0;  // and from here on
     float o[NT][KS][4];
@@ -472,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
     // ---- tiles --------------------------------------------------------------
     uint32_t at = 0, fill = (kStages - 1) * kStageBytes;  // stages read and filled now
     int ahead = kStages - 1;                              // this warp's tiles copied so far
-    uint32_t more_rows = look_up(cur, t0 + warp + 32 * kWarps);  // its tiles 32 .. 63
+    uint32_t more_rows = look_up(s_seg[warp], t0 + warp + 32 * kWarps);  // its tiles 32 .. 63
     int tok = r.lo16 + (t0 + warp) * 16;
     const int tok_end = r.lo16 + t1 * 16, tok_fill = tok_end - (kStages - 1) * kWarps * 16;
     for (; tok < tok_end; tok += kWarps * 16) {
@@ -482,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
       fill = at;  // the next one to fill is the one read now
       if ((++ahead & 31) == 0) {
         rows = more_rows;
-        more_rows = look_up(cur, t0 + warp + (ahead + 32) * kWarps);
+        more_rows = look_up(s_seg[warp], t0 + warp + (ahead + 32) * kWarps);
       }
       cp_async_wait<kStages - 1>();
       __syncwarp();
@@ -589,10 +625,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
           }
           vb[i] = lds8(vs_ld + at + 4 * i * (D / 16));
         }
-        if (edge) {  // bytes past the request may hold anything, a NaN scale included
+        // Bytes past the request may hold anything. And a NaN block of a key that some row
+        // does not see would reach that row as 0 x NaN: it leaves the product, and the rows
+        // that see it get the NaN at the end.
+        if (edge) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) {
             if (tok + 4 * i + t >= r.len) vb[i] = 0;
+            if ((vb[i] & 0x7Fu) == 0x7Fu) vb[i] = 0, s_nan[warp] = 1;
+          }
         }
         const uint32_t f01 = scales2(__byte_perm(vb[0], vb[1], 0x0040));
         const uint32_t f23 = scales2(__byte_perm(vb[2], vb[3], 0x0040));
@@ -644,6 +685,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, NT>)
           *reinterpret_cast<float4*>(dst + join_at<D>(g * (D / 32) + c / 2)) =
               make_float4(o[nt][c][i], o[nt][c][i + 2], o[nt][c + 1][i], o[nt][c + 1][i + 2]);
       }
+    if (s_nan[warp]) {
+      put_nan<D, NT>(p, s_o + (warp * kRows + 2 * t) * kJoinRow<D>, s_seg[warp]);
+      __syncwarp();
+      if (lane == 0) s_nan[warp] = 0;
+    }
     __syncthreads();
     const int c0 = (int)(item_first / run), c1 = (int)(item_last / run);  // CTAs of the item
     const bool whole = c0 == c1;
@@ -706,7 +752,7 @@ cudaError_t launch_t(const KvAttnParams& p, cudaStream_t st) {
 }  // namespace
 
 // Requests of up to 8 rows and of 9 to 16 differ in the columns of their products (one
-// row per request, 64 x 8192 tokens: 110 us with 8 columns, 152 with 16). Where a call
+// row per request, 64 x 8192 tokens: 109 us with 8 columns, 152 with 16). Where a call
 // may hold prompts besides (more than 16 rows), requests of both kinds are to be
 // expected and each kind gets a launch (62 single rows at 8192 tokens with two prompts of
 // 300: 143 us, against 188 in one; an empty launch adds 2 us to prompts alone); drafted

@@ -31,15 +31,16 @@
 // against 32) and a softmax of 1200 beside them, which wait for one another at times.
 // From one item to the next both tiles stand still (queries, first scores, last P V,
 // result: about 12000 clocks for an item of 34 key tiles). Prompts of 1500 to 2048
-// tokens behind 3000 to 10000 (4 requests, 32 query heads on 8, D = 128; 585 GFLOP): 413
-// us, 1.42 PFLOP/s, 74% of the measured cuBLAS rate; one prompt of 8192 tokens: 405 us,
-// 1.36 PFLOP/s; one of 300: 26 us, all of it latency.
+// tokens behind 3000 to 10000 (4 requests, 32 query heads on 8, D = 128; 585 GFLOP): 417
+// us, 1.40 PFLOP/s, 73% of the measured cuBLAS rate; one prompt of 8192 tokens: 398 us,
+// 1.38 PFLOP/s; one of 300: 26 us, all of it latency. Leaving NaN blocks of V out (put_nan)
+// costs 5 us of the 417, and 3% where 32 rows wait for the de-quantisation.
 //
 // Why 64 keys per product and two S per tile: with one S of 128 columns per tile the
 // softmax and the MMAs of a tile take turns and it took 545 us where this form then took
 // 515. Why one warpgroup that dequantises: two of them (640 threads) leave the softmax
-// 152 registers and took 462 us where one takes 413. Why K and V are handed over 128 keys
-// at a time: 64 at a time (finer barriers, the same buffers) took 517 us where this takes
+// 152 registers and took 462 us where one took 413. Why K and V are handed over 128 keys
+// at a time: 64 at a time (finer barriers, the same buffers) took 517 us where this took
 // 413. Why short loops outside the step: the kernel has to stay in the instruction cache;
 // with everything unrolled (195 KB of code, now 87) it took 497 us where it then took 445.
 //
@@ -80,6 +81,13 @@ __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile
     }
   }
   return true;
+}
+
+// 0xFFFF in every half of an f16x2 that is a number.
+__device__ __forceinline__ uint32_t numbers2(uint32_t a) {
+  uint32_t r;
+  asm("set.eq.u32.f16x2 %0, %1, %1;" : "=r"(r) : "r"(a));
+  return r;
 }
 
 struct Bars {
@@ -153,6 +161,7 @@ struct Item {
   float kg, vg;   // outer scales of K and V
   int t0, t1;     // this CTA's tiles, counted from key lo16
   int c0, c1;     // the CTAs that share it
+  int nan_lo, nan_hi;  // keys of those tiles where V has a NaN scale lie in [nan_lo, nan_hi]
 };
 
 // The items of this CTA's run [pos, last) of units, in the same order in every
@@ -210,6 +219,8 @@ struct Walk {
       it.t1 = t.begin + from + count - kItemCost;
       it.c0 = (int)((item + kItemCost) / run);
       it.c1 = (int)((item + units - 1) / run);
+      it.nan_lo = INT32_MAX;
+      it.nan_hi = -1;
       const SliceScale ks = slice_scale(p.k_amax[h], p.M), vs = slice_scale(p.v_amax[h], p.M);
       if (ks.bad || vs.bad) flag(p.status, NVFP4_DEV_BAD_AMAX_BIT);
       it.kg = ks.g;
@@ -283,6 +294,60 @@ __device__ __forceinline__ float part_weight(const KvAttnParams& p, int c, int c
                                              float m) {
   const float mc = __ldcg(prefill_record(p, c, c0) + kRowsItem * 128 + ri);
   return mc == __uint_as_float(kNegInf) ? 0.0f : ex2(mc - m);
+}
+
+// The cache row of a request's key.
+__device__ __forceinline__ uint32_t cache_row(const KvAttnParams& p, const int32_t* table, int h,
+                                              int key) {
+  const int pg = p.page_shift >= 0 ? key >> p.page_shift : (int)fastdiv((uint32_t)key, p.by_page);
+  int64_t page = table[pg];
+  if (page < 0 || page >= p.pages) {
+    page = 0;
+    flag(p.status, kDevBadIndex);
+  }
+  return (uint32_t)((page * p.hk + h) * p.P + (key - pg * p.P));
+}
+
+// NaN into the output columns (tensor memory, at `to`) of the 16-value blocks of V whose
+// scale is NaN in a key that this lane's row sees: keys [low, low + span) among the item's
+// nan_lo .. nan_hi. Such blocks are left out of the product, where they would reach every
+// row as 0 x NaN. For whole warps; `done` is the barrier of the item's last product.
+template <int D>
+__device__ __noinline__ bool put_nan(const KvAttnParams& p, const Item& x, int low, uint32_t span,
+                                     uint32_t to, uint64_t* done, uint32_t parity,
+                                     volatile int* dead) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* table = p.table + (int64_t)x.b * p.cols;
+  uint32_t seen = 0;  // a bit per block
+#pragma unroll 1
+  for (int first = x.nan_lo; first <= x.nan_hi; first += 32) {
+    uint32_t bits = 0;
+    if (first + lane <= x.nan_hi) {
+      const uint8_t* at = p.vs + (uint64_t)cache_row(p, table, x.h, first + lane) * (D / 16);
+#pragma unroll 1
+      for (int i = 0; i < D / 16; ++i) bits |= (uint32_t)((at[i] & 0x7F) == 0x7F) << i;
+    }
+    uint32_t some = __ballot_sync(kAll, bits != 0);
+    while (some) {
+      const int src = __ffs(some) - 1;
+      const uint32_t b = __shfl_sync(kAll, bits, src);
+      if ((uint32_t)(first + src - low) < span) seen |= b;
+      some &= some - 1;
+    }
+  }
+  if (!__all_sync(kAll, wait_long(done, parity, dead, p.status))) return false;
+  fence_after();
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t o[16];
+    tmem_ld16(to + 16 * c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = seen >> c & 1 ? 0x7FFFFFFFu : o[i];
+    tmem_st16(to + 16 * c, o);
+  }
+  tmem_wait_st();
+  return true;
 }
 
 template <int D>
@@ -644,6 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (lane == 0) mbar_arrive(&bar.p_full[tile][sb]);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
+      // (a P V of the item's last tile is done: its V was stored and looked at)
+      if (ok && it->nan_hi >= 0)
+        ok = put_nan<D>(p, *it, low, span, to, &bar.o_done[tile], (n - 1) & 1, &s_dead);
       open = true;
     }
   } else if (warp < 12) {
@@ -690,22 +758,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           }
         }
       };
-      auto store = [&](uint8_t* dst, const uint4 (&c)[kRowsPer], const uint32_t (&b)[kRowsPer]) {
+      auto store = [&](uint8_t* dst, const uint4 (&c)[kRowsPer], const uint32_t (&b)[kRowsPer],
+                       bool v) {
+        uint32_t nan = 0;
 #pragma unroll
         for (int i = 0; i < kRowsPer; ++i) {
           const int row = rbase + kRowStep * i;
-          const uint32_t sc = scales2(b[i]);
+          uint32_t sc = scales2(b[i]);
+          // In P V a NaN block would reach rows that do not see its key, as 0 x NaN: it is
+          // left out, and the rows that see it get the NaN at the item's end.
+          if (v) {
+            const uint32_t number = numbers2(sc);
+            sc &= number;
+            nan |= ~number;
+          }
           const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t fs = __byte_perm(sc, 0, k < 2 ? 0x1010 : 0x3232);
-            uint32_t v[4];
-            codes8(words[k], v);
+            uint32_t x[4];
+            codes8(words[k], x);
             const int c16 = chunk * 4 + k;
             *reinterpret_cast<uint4*>(dst + (c16 >> 3) * (128 * 128) + row * 128 +
                                       (((c16 & 7) ^ (row & 7)) << 4)) =
-                make_uint4(h2mul(v[0], fs), h2mul(v[1], fs), h2mul(v[2], fs), h2mul(v[3], fs));
+                make_uint4(h2mul(x[0], fs), h2mul(x[1], fs), h2mul(x[2], fs), h2mul(x[3], fs));
           }
+        }
+        if (nan) {
+          atomicMin(&s_item[(items - 1) % kItems].nan_lo, tok);
+          atomicMax(&s_item[(items - 1) % kItems].nan_hi, min(tok + kRowStep * (kRowsPer - 1), len - 1));
         }
         fence_smem_async();
         __syncwarp();
@@ -719,11 +800,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         const bool more = j + 1 < t1;
         if (more && !(ok = locate(n + 1, tok + kTileN))) break;
         if (!(ok = wait_warp(&bar.k_free[st], par))) break;
-        store(sk + st * kTile, ck, bk);
+        store(sk + st * kTile, ck, bk, false);
         if (lane == 0) mbar_arrive(&bar.k_full[st]);
         if (more) load(p.kc, p.ks, ck, bk);
         if (!(ok = wait_warp(&bar.v_free[st], par))) break;
-        store(sv + st * kTile, cv, bv);
+        store(sv + st * kTile, cv, bv, true);
         if (lane == 0) mbar_arrive(&bar.v_full[st]);
         if (more) load(p.vc, p.vs, cv, bv);
       }
@@ -860,14 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         for (int j = it->t0; j < t1; ++j, ++n, key += kTileN) {
           uint32_t row = 0;
           if (lane < kTileN / 16 && key < len) {
-            const int pg = p.page_shift >= 0 ? key >> p.page_shift
-                                             : (int)fastdiv((uint32_t)key, p.by_page);
-            int64_t page = table[pg];
-            if (page < 0 || page >= p.pages) {
-              page = 0;
-              flag(p.status, kDevBadIndex);
-            }
-            row = (uint32_t)((page * p.hk + h) * p.P + (key - pg * p.P));
+            row = cache_row(p, table, h, key);
           }
           if (!(ok = wait_warp(&bar.rows_free[n % kItems], ((n / kItems) & 1) ^ 1))) break;
           if (lane < kTileN / 16) s_rows[n % kItems][lane] = row;
