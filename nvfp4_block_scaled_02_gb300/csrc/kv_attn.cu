@@ -172,11 +172,15 @@ __device__ __noinline__ void join_records(const KvAttnParams& p, int q0, int h, 
         mc[u] = __ldcg(rec + kAttnRows * 128 + rr);
         lc[u] = __ldcg(rec + kAttnRows * 129 + rr);
         x[u] = __ldcg(reinterpret_cast<const float4*>(rec + rr * D + 4 * q));
-        if (c + u > c1) mc[u] = __int_as_float(0xFF800000);
+        if (c + u > c1) mc[u] = __int_as_float(0xFF800000), lc[u] = 0.0f;
       }
       float mn = mx;
 #pragma unroll
-      for (int u = 0; u < U; ++u) mn = fmaxf(mn, mc[u]);
+      for (int u = 0; u < U; ++u) {
+        mn = fmaxf(mn, mc[u]);
+        // a part without a maximum: its sum is 0, or NaN where its scores are
+        if (mc[u] == __int_as_float(0xFF800000)) sum += lc[u];
+      }
       if (mn == __int_as_float(0xFF800000)) continue;
       const float a = ex2(mx - mn);
       sum *= a;

@@ -155,3 +155,24 @@ def test_a_token_appended_with_nan_leaves_with_the_window():
         got, want = got.clone(), want.clone()
         got[sees, 1, 16:32] = want[sees, 1, 16:32] = 0
         assert torch.equal(got, want), (first, last)
+
+
+@pytest.mark.parametrize("new", [1, 2, 30])
+@pytest.mark.parametrize("total", [60, 12000])
+@pytest.mark.parametrize("what", ["every key", "a query"])
+def test_rows_whose_scores_are_all_nan(new, total, what):
+    """NaN, not the 0 and -infinity of a row that sees no key, in one CTA and where
+    several share the keys."""
+    s = plain._state([new, 1], [total, 50], 8, 2, 128, 64, seed=total + new)
+    if what == "every key":
+        pg = s["table"][0, : -(-total // 64)]
+        s["cache"]["k_scales"][pg, 1] = 0x7F
+        rows, heads = slice(0, new), slice(4, 8)
+    else:
+        s["q"][new - 1, 5, 77] = float("nan")
+        rows, heads = slice(new - 1, new), slice(5, 6)
+    got = nv.nvfp4_kv_attention(*plain._dev(s))
+    o, z = got["out"].float().cpu(), got["lse"].cpu()
+    assert torch.isnan(o[rows, heads]).all() and torch.isnan(z[rows, heads]).all()
+    o[rows, heads], z[rows, heads] = 0, 0
+    assert torch.isfinite(o).all() and torch.isfinite(z).all()
