@@ -172,23 +172,22 @@ __device__ __noinline__ void join_records(const KvAttnParams& p, int q0, int h, 
         mc[u] = __ldcg(rec + kAttnRows * 128 + rr);
         lc[u] = __ldcg(rec + kAttnRows * 129 + rr);
         x[u] = __ldcg(reinterpret_cast<const float4*>(rec + rr * D + 4 * q));
-        if (c + u > c1) mc[u] = __int_as_float(0xFF800000), lc[u] = 0.0f;
+        if (c + u > c1) mc[u] = __int_as_float(0xFF800000);
       }
       float mn = mx;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        mn = fmaxf(mn, mc[u]);
-        // a part without a maximum: its sum is 0, or NaN where its scores are
-        if (mc[u] == __int_as_float(0xFF800000)) sum += lc[u];
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, mc[u]);
+      if (mn == __int_as_float(0xFF800000)) {  // sums of 0, or NaN where the scores are
+#pragma unroll
+        for (int u = 0; u < U; ++u) sum += lc[u];
+        continue;
       }
-      if (mn == __int_as_float(0xFF800000)) continue;
       const float a = ex2(mx - mn);
       sum *= a;
       v.x *= a, v.y *= a, v.z *= a, v.w *= a;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (mc[u] == __int_as_float(0xFF800000)) continue;
-        const float e = ex2(mc[u] - mn);
+        const float e = ex2(mc[u] - mn);  // 0 without a maximum: a NaN stays
         sum = __fmaf_rn(lc[u], e, sum);
         v.x = __fmaf_rn(x[u].x, e, v.x), v.y = __fmaf_rn(x[u].y, e, v.y);
         v.z = __fmaf_rn(x[u].z, e, v.z), v.w = __fmaf_rn(x[u].w, e, v.w);
