@@ -582,14 +582,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                  if (wt[k] != 0.0f)  // a part that saw nothing of this row holds no numbers
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                      s[4 * i] = __fmaf_rn(x[k][i].x, wt[k], s[4 * i]);
-                      s[4 * i + 1] = __fmaf_rn(x[k][i].y, wt[k], s[4 * i + 1]);
-                      s[4 * i + 2] = __fmaf_rn(x[k][i].z, wt[k], s[4 * i + 2]);
-                      s[4 * i + 3] = __fmaf_rn(x[k][i].w, wt[k], s[4 * i + 3]);
-                    }
+                  for (int i = 0; i < 8; ++i) {  // (a weight of 0 leaves a NaN)
+                    s[4 * i] = __fmaf_rn(x[k][i].x, wt[k], s[4 * i]);
+                    s[4 * i + 1] = __fmaf_rn(x[k][i].y, wt[k], s[4 * i + 1]);
+                    s[4 * i + 2] = __fmaf_rn(x[k][i].z, wt[k], s[4 * i + 2]);
+                    s[4 * i + 3] = __fmaf_rn(x[k][i].w, wt[k], s[4 * i + 3]);
+                  }
               }
             }
 #pragma unroll

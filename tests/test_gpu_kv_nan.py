@@ -122,6 +122,21 @@ def test_in_keys_and_values(shape, window):
     _test(s, window, [(b, mid, 0, 1)], [(b, last, hk - 1, D // 16 - 1), (b, max(0, mid - 40), 0, 0)])
 
 
+@pytest.mark.parametrize("new", [1, 30])
+def test_a_part_with_a_vanishing_weight(new):
+    """The NaN lies in a part of the keys (another CTA's) whose weight in the whole
+    is 0 in 32 bits: the formula still gives NaN."""
+    D, P, L = 128, 64, 12000
+    s = plain._state([new], [L], 8, 1, D, P, seed=60 + new)
+    pg = s["table"][0, : -(-L // P)]
+    s["cache"]["k_scales"][pg, 0] = 0x38       # 1
+    s["cache"]["k_codes"][pg, 0] = 0x22        # 1
+    s["cache"]["k_codes"][pg[:2], 0] = 0x77    # 6: the first 128 keys
+    s["cache"]["k_amax"][:] = 6 * 448
+    s["q"] = torch.full_like(s["q"], 4.0)      # scores of 45 and 271: a weight of 2^-326
+    _test(s, 0, [], [(0, L - new - 200, 0, 3)])
+
+
 def test_a_token_appended_with_nan_leaves_with_the_window():
     """A V row with a NaN goes into the cache (and is flagged): rows see it until their
     window has passed it, and never before its position."""
