@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) qk_rope_bwd_kernel(const QkRop
           const float r = rsqrtf(__fmaf_rn(v[0], 1.0f / D, p.eps));
           const V8 xr = scale(x, r);
           if (ok) sum = fma(u, xr, sum);  // (a head that is not there may have r infinite)
-          // r (w u - x r^2 mean(w u x)) = r w u - (x r) (r^2 mean)
-          u = fma(xr, -__fmul_rn(__fmul_rn(r, r), __fmul_rn(v[1], 1.0f / D)), scale(wu, r));
+          // r (w u - x r^2 mean(w u x)) = r w u - (x r) (r mean) r: r^2 may be past fp32
+          u = fma(xr, -__fmul_rn(__fmul_rn(__fmul_rn(v[1], 1.0f / D), r), r), scale(wu, r));
         }
         if (ok) store8<IL>(out + (s + b) * (L::kHeads * D), ln, u);
       }
