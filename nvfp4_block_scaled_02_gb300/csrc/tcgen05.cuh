@@ -37,15 +37,6 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
                : "=r"(ok) : "r"(smem_addr(b)), "r"(parity) : "memory");
   return ok != 0;
 }
-// The same without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(smem_addr(b)), "r"(parity) : "memory");
-  return ok != 0;
-}
 
 // ---------------------------------------------------------- tensor memory --
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
