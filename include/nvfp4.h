@@ -515,7 +515,9 @@ NVFP4_API nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, nvfp4_rows k
  * that sees a key whose V has a NaN scale gets NaN in the 16 values of that
  * block; with a NaN scale in its K, everywhere and in lse. Accumulation, softmax
  * statistics and partial results are fp32; K and V enter the products exactly,
- * the probabilities rounded to f16. */
+ * the probabilities, as parts of the row's largest, rounded to f16 (below 2^-31
+ * to 0). Scores scale * q . k may be up to 2^21 in magnitude: beyond that their
+ * fp32 rounding is several powers of e, and out may overflow. */
 typedef struct {
   const int32_t* block_table;  /* int32 [requests][table_cols]                   */
   const int32_t* seq_len;      /* int32 [requests]                               */

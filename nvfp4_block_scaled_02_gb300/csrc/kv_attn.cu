@@ -8,7 +8,7 @@
 // [2^-10, 2688], so it is exact in f16; g_k goes into the softmax scale and
 // g_v into the final division. A query row is multiplied by a power of two
 // that puts its largest element in [2^13, 2^14): its bf16 elements are then
-// exact in f16 down to 2^-27 of that one, and off by at most 2^-39 of it below.
+// exact in f16 down to 2^-27 of that one, and off by at most 2^-38 of it below.
 // Scores, maxima, sums and outputs are fp32. The probabilities are rounded to
 // f16 for the second product (2^-11 relative; the sum that divides them is
 // taken before rounding), times 2^kBias so that they stay normal down to

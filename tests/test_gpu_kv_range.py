@@ -5,6 +5,7 @@ import torch
 
 import kv_ref
 import nvfp4_block_scaled_02_gb300 as nv
+import test_gpu_kv_attn as plain
 from test_gpu_qk_rope import _inputs, _np
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +31,27 @@ def test_norm_gradient_of_tiny_heads_without_eps(D, il):
         # 15 or 5 rows and the roundings of a term
         assert (np.abs(_np(got[f"g{name}_weight"]) - gw) <= 2.0 ** -19 * np.abs(_np(gy)).max()
                 * 2 * gy.shape[0] * gy.shape[1]).all(), name
+
+
+@pytest.mark.parametrize("new,total", [([1, 2], [700, 12000]), ([40], [700]), ([30], [12000])])
+@pytest.mark.parametrize("size", [2.0 ** e for e in (8, 10, 12, 13)])
+def test_large_scores(new, total, size):
+    """Scores of up to 2^21, where fp32 holds them to a quarter: the rows are nearly one key's V.
+    The bounds of test_gpu_kv_attn.py allow for the scores' error, which is above 1 here, so
+    that the output is only held to the range of the values: a mean of them, rounded to bf16
+    (and the probabilities to f16)."""
+    s = plain._state(new, total, 8, 2, 128, 64, seed=int(np.log2(size)), q_size=size)
+    got = nv.nvfp4_kv_attention(*plain._dev(s), scale=0.5)
+    _, lse, _, a, _ = plain._ref(s, 0.5, 0)
+    assert np.abs(lse).max() < 2.0 ** 21
+    o, z = got["out"].double().cpu().numpy(), got["lse"].double().cpu().numpy()
+    assert (np.abs(z - lse) <= 2.0 ** -18 * a + 2.0 ** -19 + 2.0 ** -22 * np.abs(lse)).all()
+    c = s["cache"]
+    for b in range(len(new)):
+        pg = s["table"][b, : -(-total[b] // 64)]
+        rows = slice(s["q_start"][b], s["q_start"][b + 1])
+        for h in range(2):
+            v = np.abs(kv_ref.decode(c["v_codes"][pg, h].reshape(-1, 64)[: total[b]],
+                                     c["v_scales"][pg, h].reshape(-1, 8)[: total[b]],
+                                     float(c["v_amax"][h]) / (6 * 448))).max(0)
+            assert (np.abs(o[rows, 4 * h: 4 * h + 4]) <= v * (1 + 2.0 ** -7)).all(), (b, h)
