@@ -8,8 +8,9 @@
 // the head's constants (a division, two reciprocals) are worked out once. Bound by
 // DRAM and issue together: 2 bytes read, 0.5625 (+ 2 with the de-quantised rows) written
 // per value, and the encoder's instructions keep 77% of the issue slots busy. 16381
-// tokens of 8 heads of 128 with de-quantised rows: 31.0 us, 4.94 TB/s (73% of the
-// measured copy rate); one token of 48 requests: 1.9 us.
+// tokens of 8 heads of 128 with de-quantised rows: 30.1 us, 5.08 TB/s (75% of the
+// measured copy rate), without 26.7 us (48%: the same instructions, fewer bytes), with 4/6
+// 41.6 and 39.5 us; one token of 48 requests: 2.0 us.
 #include "encode.cuh"
 #include "kv.h"
 

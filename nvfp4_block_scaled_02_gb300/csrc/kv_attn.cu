@@ -29,8 +29,8 @@
 // CTA; cut evenly, 64 ragged requests run at the rate of 64 equal ones.)
 //
 // What bounds it: DRAM and the conversions together. A tile of 16 keys is 2304 bytes
-// and about 300 warp instructions, many of them conversions and byte moves on the ALU
-// pipe, which is half busy (issue slots 64%) at 78% of the measured copy rate. Measured,
+// and about 280 warp instructions, many of them conversions and byte moves on the ALU
+// pipe, which is nearly half busy (issue slots 59%) at 79% of the measured copy rate. Measured,
 // one row per request, 8 KV heads, groups of 4, D = 128: 64 requests x 8192 tokens 109
 // us (5.54 TB/s, 82% of that rate); 64 ragged ones, 672 MB in all, 121 us (82%); 256 x
 // 500 tokens 45 us (50%: an item is 8 tiles per warp and each costs its set-up and join);

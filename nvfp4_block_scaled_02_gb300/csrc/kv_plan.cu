@@ -12,7 +12,7 @@
 // another one writes.
 //
 // Bound by latency (a few KB to a few MB move): 5.0 us for 64 requests with one new
-// token each, 8.1 us for 1500 requests and 2.7 MB of results.
+// token each, 7.8 us for 1500 requests (two passes of 1024) and 2.7 MB of results.
 #include "kv.h"
 
 namespace nvfp4 {

@@ -13,10 +13,11 @@
 // rotation needs no shuffle. A warp takes several heads of one token in a row, so
 // that the token's angles stay in registers. Both directions are bound by DRAM: 4
 // (forward) and 6 (backward) bytes per value. Measured at 40 heads of 128, normed:
-// forward 8192 tokens 29.9 us (5.75 TB/s, 85% of the measured copy rate), 32 tokens 2.0
-// us; gradient 8192 tokens 54.5 us (4.69 TB/s, 69%), 65536 tokens 365 us (83%): about 5
-// us of a call go into the weights' gradients once, over warps, CTAs and then in the
-// last CTA, whatever the number of tokens.
+// forward 8192 tokens 29.3 us (5.87 TB/s, 87% of the measured copy rate), 32 tokens 2.0
+// us; gradient 8192 tokens 53.8 us (4.76 TB/s, 70%), 65536 tokens 366 us (83%). The two
+// lie 5.4 ns per token apart, 85% of the copy rate, and leave about 10 us of a call that do
+// not depend on the tokens: its start, and the weights' gradients over warps, CTAs and
+// then in the last CTA.
 #include "kv.h"
 
 namespace nvfp4 {

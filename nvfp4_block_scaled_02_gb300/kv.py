@@ -265,7 +265,8 @@ def nvfp4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor
     """RMS norm of every head (where its weight is given) and rotation of q
     [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim] (bf16; tokens
     may be apart) in one launch. cos_sin: fp32 [positions, rotary_dim], cosines
-    then sines. Returns {"q", "k"}; q_out, k_out may be q and k themselves."""
+    then sines. Returns {"q", "k"}; q_out, k_out may be q and k themselves. Nothing is
+    recorded for autograd: nvfp4_qk_norm_rope_bwd gives the gradient."""
     dev = q.get_device()
     if _elsewhere(dev):
         with torch.cuda.device(dev):
