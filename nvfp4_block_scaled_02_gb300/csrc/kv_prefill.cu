@@ -42,7 +42,8 @@
 // 152 registers and took 462 us where one took 413. Why K and V are handed over 128 keys
 // at a time: 64 at a time (finer barriers, the same buffers) took 517 us where this took
 // 413. Why short loops outside the step: the kernel has to stay in the instruction cache;
-// with everything unrolled (195 KB of code, now 87) it took 497 us where it then took 445.
+// with everything unrolled (195 KB of code, then 87, now 95) it took 497 us where it then
+// took 445.
 //
 // Every wait has a limit: when it runs out the CTA sets NVFP4_DEV_TIMEOUT, its
 // other waits return at once, and it frees its tensor memory and ends.
