@@ -551,6 +551,75 @@ NVFP4_API nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache,
                                           void* out, float* lse, void* workspace, size_t ws_bytes,
                                           int32_t* status, void* stream);
 
+/* ---- the quantised linear layer -------------------------------------------
+ * End-to-End 4-Bit Training, the quantised-linear-layer figure: FPROP multiplies
+ * NVFP4 activations (one outer scale per token) with NVFP4 weights (one per
+ * expert), DGRAD and WGRAD multiply MXFP8 operands. The pages name the products
+ * and leave them to a library; these take the encodings as this library writes
+ * them, without a change of layout.
+ *
+ * Rows are grouped by expert: group e owns rows group_start[e] ..
+ * group_start[e+1]-1 (int32 [groups + 1] on the device; NULL: one group of all
+ * rows), any number of them, none included. At most 1024 groups.
+ *
+ * A product's operand: the row encoding of a matrix. */
+typedef struct {
+  const uint8_t* codes;  /* [rows][cols/2]                                      */
+  const uint8_t* scales; /* [rows][cols/16], E4M3                               */
+  const float* amax;     /* fp32 [amax_count]: the amax of the outer scales     */
+  int64_t amax_count;
+  float scale_max;       /* M of the outer scale; 0 = 448                       */
+} nvfp4_operand;
+
+/* out[t][n] = sum over k of a[t][k] * b[e][n][k], e the group of row t: bf16
+ * [rows][out_cols]. a: [rows][cols] with one amax (amax_count 1) or one for each
+ * row (as nvfp4_quantize_per_token gives it); b: [groups][out_cols][cols] with
+ * one for each group. cols % 32 == 0. Products are exact, sums fp32, with one
+ * rounding to bf16 at the end; the order of a sum depends on the sizes and the
+ * device only, so that the same inputs give the same bits. Rows that no group
+ * owns are not written.
+ * workspace: device memory, >= nvfp4_grouped_matmul_ws_bytes() bytes, 16-byte
+ * aligned, ALL ZERO before its first use; every call leaves its counters zero
+ * again. It serves one call (of any of the three products) at a time.
+ * Data errors: NVFP4_DEV_BAD_INDEX for group_start out of order or outside [0,
+ * rows] (such a group is left out), NVFP4_DEV_BAD_AMAX, NVFP4_DEV_TIMEOUT
+ * (results and workspace are then not valid). NaN scale bytes give NaN.
+ * Errors: NULL pointers, sizes out of range (rows, groups * out_cols and cols up
+ * to 2^31 - 4097, 2^26 tiles of 256 x 128 results), cols % 32, amax_count,
+ * scale_max negative or not finite (NVFP4_ERR_ENUM), buffers that are not
+ * 16-byte aligned (amax, group_start, status: 4), and those of the workspace (as
+ * nvfp4_amax_ws). */
+NVFP4_API size_t nvfp4_grouped_matmul_ws_bytes(void);
+NVFP4_API nvfp4_status nvfp4_grouped_matmul(const nvfp4_operand* a, const nvfp4_operand* b,
+                                            int64_t rows, int64_t groups, int64_t out_cols,
+                                            int64_t cols, const int32_t* group_start, void* out,
+                                            void* workspace, size_t ws_bytes, int32_t* status,
+                                            void* stream);
+
+/* The same with MXFP8 operands as nvfp4_mx_quantize and nvfp4_requant_transpose
+ * write them (codes [rows][cols] E4M3, scales [rows][cols/32] E8M0): DGRAD, with
+ * a the output's gradient and b every expert's transposed weights. */
+NVFP4_API nvfp4_status nvfp4_mx_grouped_matmul(const uint8_t* a_codes, const uint8_t* a_scales,
+                                               const uint8_t* b_codes, const uint8_t* b_scales,
+                                               int64_t rows, int64_t groups, int64_t out_cols,
+                                               int64_t cols, const int32_t* group_start, void* out,
+                                               void* workspace, size_t ws_bytes, int32_t* status,
+                                               void* stream);
+
+/* WGRAD: out[e][n][k] = sum over the rows t of group e of g[n][t] * x[k][t], with
+ * g [out_rows][rows] and x [out_cols][rows] in MXFP8 (column encodings of the
+ * output's gradient and of the activations: blocks of 32 along the rows). rows
+ * % 32 == 0 and every entry of group_start a multiple of 32 (pad an expert's rows
+ * with zeros): another one is NVFP4_DEV_BAD_INDEX, and its groups' results are
+ * not written. A group without rows gets zeros. out: bf16, or fp32 with out_fp32
+ * = 1, [groups][out_rows][out_cols]. Otherwise as nvfp4_mx_grouped_matmul. */
+NVFP4_API nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint8_t* g_scales,
+                                              const uint8_t* x_codes, const uint8_t* x_scales,
+                                              int64_t rows, int64_t groups, int64_t out_rows,
+                                              int64_t out_cols, const int32_t* group_start,
+                                              void* out, int32_t out_fp32, void* workspace,
+                                              size_t ws_bytes, int32_t* status, void* stream);
+
 /* ---- diagnostics: the device codecs element by element -------------------
  * For exhaustive checks of the conversions the kernels use. op:
  *   0: out[i] = E2M1 RNE code of in[i]

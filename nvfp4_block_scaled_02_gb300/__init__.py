@@ -33,6 +33,8 @@ __all__ = [
     "DEV_TIMEOUT",
     "alloc_kv_cache", "kv_attention_workspace", "nvfp4_kv_append", "nvfp4_kv_attention",
     "nvfp4_kv_plan", "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_bwd", "qk_norm_rope_workspace",
+    "grouped_matmul_workspace", "nvfp4_grouped_matmul", "nvfp4_mx_grouped_matmul",
+    "nvfp4_mx_grouped_wgrad",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -140,6 +142,7 @@ def lib() -> C.CDLL:
                          "nvfp4_scale_grad_bwd", "nvfp4_codec_probe", "nvfp4_sr_bits"):
                 getattr(L, name).restype = C.c_int
             kv.declare(L)
+            linear.declare(L)
             _lib = L
     return _lib
 
@@ -647,3 +650,6 @@ from . import kv  # noqa: E402  (the cache operators use the marshalling above)
 from .kv import (alloc_kv_cache, kv_attention_workspace, nvfp4_kv_append,  # noqa: E402
                  nvfp4_kv_attention, nvfp4_kv_plan, nvfp4_qk_norm_rope, nvfp4_qk_norm_rope_bwd,
                  qk_norm_rope_workspace)
+from . import linear  # noqa: E402  (the linear layer's operators use kv's checks)
+from .linear import (grouped_matmul_workspace, nvfp4_grouped_matmul,  # noqa: E402
+                     nvfp4_mx_grouped_matmul, nvfp4_mx_grouped_wgrad)

@@ -1,0 +1,546 @@
+// matmul.cu -- products of block-scaled matrices on tcgen05, grouped by expert.
+#include "matmul.h"
+#include "tcgen05.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kEpilogueWarps = 8;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleWarps = 3;
+constexpr int kThreads = (kEpilogueWarps + 2 + kScaleWarps) * 32;
+constexpr int kTileF = 128, kTileC = 256;
+constexpr int kStageRow = 128;                 // code bytes of a row in a stage: one swizzle line
+constexpr int kFBytes = kTileF * kStageRow;
+constexpr int kBoxC = 32;                      // columns of one copy
+constexpr int kMaxStages = 12;
+constexpr int kRing = 216 * 1024;              // bytes of the ring of stages
+constexpr int kSmem = kRing + 1024;            // and its alignment
+// Tensor memory: two accumulators of 256 columns that share 96, scales twice.
+constexpr int kAcc1 = 160, kScales = 416, kScalesEach = 48;
+constexpr long long kWaitCycles = 2000000000;  // about a second
+
+__device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* dead,
+                                          int32_t* status) {
+  const long long t0 = clock64();
+  while (!mbar_try(b, parity)) {
+    if (*dead) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *dead = 1;
+      flag(status, NVFP4_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// `valid` bytes (0 to 4) from p on, the others 0; [base, end) is the array, base 16-byte aligned.
+__device__ __forceinline__ uint32_t bytes4(const uint8_t* p, int valid, const uint8_t* end) {
+  if (valid <= 0) return 0;
+  valid = min(valid, 4);
+  const uint32_t off = (uint32_t)((uintptr_t)p & 3);
+  const uint8_t* a = p - off;
+  auto word = [&](const uint8_t* q) {
+    if (q + 4 <= end) return __ldg(reinterpret_cast<const uint32_t*>(q));
+    uint32_t w = 0;
+    for (int i = 0; i < 3; ++i)
+      if (q + i < end) w |= (uint32_t)q[i] << (8 * i);
+    return w;
+  };
+  const uint32_t lo = word(a), hi = off + valid > 4 ? word(a + 4) : 0;
+  const uint32_t v = __funnelshift_r(lo, hi, 8 * off);
+  return valid >= 4 ? v : v & ((1u << (8 * valid)) - 1);
+}
+
+template <int KIND>
+struct Kind {
+  static constexpr bool kFp4 = KIND == kMatmulNvfp4;
+  static constexpr bool kWgrad = KIND == kMatmulMxWgrad;
+  static constexpr int kStageK = kFp4 ? 256 : 128;  // values of a row in a stage
+  static constexpr int kStepK = kFp4 ? 64 : 32;     // values of a product
+  static constexpr int kStageSf = kFp4 ? 16 : 4;    // scale bytes of a row in a stage
+  static constexpr int kSfBlock = 128 * kStageSf;   // scale bytes of 128 rows in a stage
+};
+
+// What one CTA does at a time: features f0 .. of a group times some of its
+// columns, over stages k0 .. k1 - 1 of the sum.
+struct Work {
+  int g, f0, c0, cols;      // group, first feature, first column, columns
+  int64_t f_row, c_row;     // rows of the two matrices
+  int64_t k_at;             // first value of the sum
+  int steps;                // products of the whole sum
+  int k0, k1;
+  int tile, part, parts;
+};
+
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full, acc_free, end;
+  uint32_t tmem;
+  volatile int dead;
+  int last;
+  int scan[kThreads / 32], most[kThreads / 32];
+  int tile[kMatmulMaxGroups + 1];  // a group's first tile
+  float scale[2][kTileC];          // outer scales of a tile's columns
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__ CUtensorMap c_map,
+              const MatmulParams p) {
+  using T = Kind<KIND>;
+  pdl_begin();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared s;
+  uint8_t* ring = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
+  const int f_tiles = (p.N + kTileF - 1) / kTileF;
+  const int64_t rows_all = T::kWgrad ? p.K : p.c_rows;
+
+  // ---- the groups' tiles -----------------------------------------------------
+  // a thread to `share` groups, then a scan over the threads
+  const int share = (p.E + kThreads - 1) / kThreads;
+  const int e0 = min(tid * share, p.E), e1 = min(e0 + share, p.E);
+  int mine = 0, most = 0;
+  for (int e = e0; e < e1; ++e) {
+    int64_t a = p.start ? p.start[e] : 0, b = p.start ? p.start[e + 1] : rows_all;
+    bool bad = a < 0 || b < a || b > rows_all;
+    if (T::kWgrad) bad = bad || (a | b) % 32 != 0;
+    if (bad) {
+      if (blockIdx.x == 0) flag(p.status, NVFP4_DEV_BAD_INDEX);
+      a = b = 0;
+    }
+    const int cols = T::kWgrad ? p.C : (int)(b - a);
+    const int c_tiles = (cols + kTileC - 1) / kTileC;
+    if (c_tiles > 0) most = max(most, (cols + c_tiles - 1) / c_tiles);
+    s.tile[e] = mine;
+    if (!bad) mine += c_tiles * f_tiles;
+  }
+  int incl = mine;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kAll, incl, d);
+    if (lane >= d) incl += o;
+  }
+  most = __reduce_max_sync(kAll, most);
+  if (lane == 31) s.scan[warp] = incl;
+  if (lane == 0) s.most[warp] = most;
+  if (tid == 0) {
+    s.dead = 0;
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&s.full[i], 1 + kScaleWarps);
+      mbar_init(&s.empty[i], 1);
+    }
+    mbar_init(&s.acc_full, 1);
+    mbar_init(&s.acc_free, kEpilogueWarps);
+    mbar_init(&s.end, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  int before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s.scan[w];
+    total += s.scan[w];
+    most = max(most, s.most[w]);
+  }
+  for (int e = e0; e < e1; ++e) s.tile[e] += before;
+  if (tid == 0) s.tile[p.E] = total;
+  // parts of a tile's sum, for more CTAs than tiles
+  const int split = max(1, min((int)gridDim.x / max(total, 1), 16));
+  const int items = total * split;
+  if ((int)blockIdx.x >= items) return;
+  if (warp == kMmaWarp) tmem_alloc(&s.tmem, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s.tmem;
+
+  // a stage: features' codes, columns' codes, features' scales, columns' scales
+  const int c_boxes = (most + kBoxC - 1) / kBoxC;
+  const int c_blocks = (most + 127) / 128;
+  const int sf_at = kFBytes + c_boxes * kBoxC * kStageRow;
+  const int stage_bytes = (sf_at + (1 + c_blocks) * T::kSfBlock + 1023) & ~1023;
+  const int stages = min(kRing / stage_bytes, kMaxStages);
+
+  auto work_of = [&](int item, Work& w) -> bool {
+    w.tile = item / split;
+    w.part = item - w.tile * split;
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.tile[mid] <= w.tile) lo = mid;
+      else hi = mid;
+    }
+    w.g = lo;
+    const int r = w.tile - s.tile[lo], ct = r / f_tiles;
+    w.f0 = (r - ct * f_tiles) * kTileF;
+    const int row = p.start ? __ldg(p.start + lo) : 0;
+    const int rows = p.start ? __ldg(p.start + lo + 1) - row : (int)rows_all;
+    const int cols = T::kWgrad ? p.C : rows;
+    const int c_tiles = (cols + kTileC - 1) / kTileC, size = (cols + c_tiles - 1) / c_tiles;
+    w.c0 = ct * size;
+    w.cols = min(size, cols - w.c0);
+    const int64_t sum = T::kWgrad ? rows : p.K;
+    w.k_at = T::kWgrad ? row : 0;
+    w.f_row = (T::kWgrad ? 0 : (int64_t)lo * p.N) + w.f0;
+    w.c_row = (T::kWgrad ? 0 : row) + w.c0;
+    w.steps = (int)((sum + T::kStepK - 1) / T::kStepK);
+    const int n = (int)((sum + T::kStageK - 1) / T::kStageK);
+    w.parts = min(split, max(1, n / 2));
+    w.k0 = (int)((int64_t)n * w.part / w.parts);
+    w.k1 = (int)((int64_t)n * (w.part + 1) / w.parts);
+    return w.part < w.parts && w.cols > 0;
+  };
+  auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+    return mbar_try(b, parity) || wait_long(b, parity, &s.dead, p.status);
+  };
+  auto wait_warp = [&](uint64_t* b, uint32_t parity) -> bool {
+    return __all_sync(kAll, wait(b, parity));
+  };
+
+  if (warp < kEpilogueWarps) {
+    // ==== results ==============================================================
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t acc_lane = tmem + ((uint32_t)quarter << 21);
+    int done = 0, tiles = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+      Work w;
+      if (!work_of(item, w)) continue;
+      float* sc = s.scale[tiles++ & 1];
+      float gf = 1.0f;
+      if constexpr (T::kFp4) {
+        const SliceScale f = slice_scale(p.f_amax[w.g], p.f_M);
+        gf = f.g;
+        bool bad = f.bad;
+        if (tid < w.cols) {
+          const SliceScale c = slice_scale(p.c_amax[p.c_amax_each ? w.c_row + tid : 0], p.c_M);
+          sc[tid] = c.g;
+          bad = bad || c.bad;
+        }
+        if (bad) flag(p.status, NVFP4_DEV_BAD_AMAX);
+        asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+      }
+      const bool sum = w.k1 > w.k0;  // false: a sum over nothing
+      const int buf = done & 1;
+      if (sum) {
+        // (after a timeout the results are not valid, but every barrier is still met)
+        wait_warp(&s.acc_full, done & 1);
+        fence_after();
+      }
+      const uint32_t acc = acc_lane + (buf ? kAcc1 : 0);
+      const int f = w.f0 + quarter * 32 + lane;
+      float* part = p.part + (int64_t)item * kMatmulPart + quarter * 32 + lane;
+      // the result of column c and the next ones, for the lane's feature
+      auto put = [&](int c, float (&v)[32]) {
+        if constexpr (T::kFp4) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], sc[c + i < w.cols ? c + i : 0]), gf);
+        }
+        const int64_t row0 = T::kWgrad ? (int64_t)w.g * p.C + w.c0 : w.c_row;
+        if (p.out_f32) {
+          float* o = static_cast<float*>(p.out) + (row0 + c) * p.N + f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < w.cols && f < p.N) o[(int64_t)i * p.N] = v[i];
+        } else if (p.N % 2 == 0) {
+          // neighbouring lanes swap, so that each stores two features of one column
+          const int odd = lane & 1;
+          uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                    (row0 + c + odd) * p.N + (f & ~1));
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint32_t a = pack_bf16x2(v[i], v[i + 1]), b = __shfl_xor_sync(kAll, a, 1);
+            const uint32_t x = __byte_perm(a, b, odd ? 0x3276u : 0x5410u);
+            if (c + i + odd < w.cols && f < p.N) o[(int64_t)i * p.N / 2] = x;
+          }
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + c) * p.N + f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < w.cols && f < p.N)
+              o[(int64_t)i * p.N] = (uint16_t)pack_bf16x2(v[i], 0.0f);
+        }
+      };
+      // the columns that the two accumulators share leave first
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        if (i == 3 && sum) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.acc_free);
+        }
+        const int chunk = buf ? i : 7 - i;
+        if ((chunk & 1) != half || chunk * 32 >= w.cols) continue;
+        uint32_t r[32];
+        if (sum) {
+          tmem_ld32(acc + chunk * 32, r);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0;
+        }
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        if (w.parts > 1) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (chunk * 32 + j < w.cols) part[(chunk * 32 + j) * 128] = v[j];
+        } else {
+          put(chunk * 32, v);
+        }
+      }
+      if (sum) ++done;
+      if (w.parts > 1) {
+        // the CTA that takes the tile's last ticket adds the parts in order
+        __threadfence();
+        asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+        if (tid == 0) s.last = atomicAdd(&p.tickets[w.tile], 1u) == (uint32_t)w.parts - 1;
+        asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+        if (s.last) {
+          __threadfence();
+          const float* all = p.part + (int64_t)w.tile * split * kMatmulPart + quarter * 32 + lane;
+#pragma unroll 1
+          for (int chunk = half; chunk * 32 < w.cols; chunk += 2) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+#pragma unroll 1
+            for (int q = 0; q < w.parts; ++q) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (chunk * 32 + j < w.cols)
+                  v[j] = __fadd_rn(v[j], __ldcg(all + (int64_t)q * kMatmulPart + (chunk * 32 + j) * 128));
+            }
+            put(chunk * 32, v);
+          }
+          if (tid == 0) p.tickets[w.tile] = 0;
+        }
+      }
+    }
+  } else if (warp == kCopyWarp) {
+    // ==== codes: one lane to a box ==============================================
+    uint32_t n = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+      Work w;
+      if (!work_of(item, w)) continue;
+      const int boxes = (w.cols + kBoxC - 1) / kBoxC;
+      const int x0 = (int)(T::kFp4 ? 0 : w.k_at);
+      for (int k = w.k0; k < w.k1; ++k, ++n) {
+        const uint32_t st = n % stages;
+        if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
+        const uint32_t dst = smem_addr(ring + st * stage_bytes);
+        if (lane == 0) {
+          mbar_expect(&s.full[st], kFBytes + boxes * kBoxC * kStageRow);
+          tma_load(dst, &f_map, x0 + k * kStageRow, (int)w.f_row, &s.full[st]);
+        }
+        __syncwarp();
+        if (lane < boxes)
+          tma_load(dst + kFBytes + lane * kBoxC * kStageRow, &c_map, x0 + k * kStageRow,
+                   (int)w.c_row + lane * kBoxC, &s.full[st]);
+      }
+    }
+    if (!ok) {
+      // given up: copies in flight land before the CTA ends (milliseconds are many times enough)
+      const long long t0 = clock64();
+      while (clock64() - t0 < 20000000) {
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ==== products ==============================================================
+    uint32_t n = 0, tiles = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+      Work w;
+      if (!work_of(item, w)) continue;
+      if (w.k1 <= w.k0) continue;
+      const int n16 = (w.cols + 15) & ~15, blocks = (w.cols + 127) >> 7;
+      const uint32_t acc = tmem + (tiles & 1 ? kAcc1 : 0);
+      if (tiles > 0 && !(ok = wait_warp(&s.acc_free, (tiles - 1) & 1))) break;
+      fence_after();
+      for (int k = w.k0; k < w.k1; ++k, ++n) {
+        const uint32_t st = n % stages;
+        if (!(ok = wait_warp(&s.full[st], (n / stages) & 1))) break;
+        fence_after();
+        if (elect_one()) {
+          const uint32_t at = smem_addr(ring + st * stage_bytes);
+          const uint32_t sf = tmem + kScales + (n & 1) * kScalesEach;
+          const uint32_t sf16 = (at + sf_at) >> 4;
+          constexpr int kPer = T::kFp4 ? 4 : 1;  // scale columns groups per stage
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            copy_scales(sf + 4 * j, scale_desc(sf16 + j * 32));
+            copy_scales(sf + 16 + 8 * j, scale_desc(sf16 + T::kSfBlock / 16 + j * 32));
+            if (blocks > 1)
+              copy_scales(sf + 16 + 8 * j + 4, scale_desc(sf16 + 2 * T::kSfBlock / 16 + j * 32));
+          }
+          const uint64_t df = smem_desc(at >> 4, 16), dc = smem_desc((at + kFBytes) >> 4, 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (k * 4 + j >= w.steps) break;
+            const bool add = k > w.k0 || j > 0;
+            if constexpr (T::kFp4)
+              mma_nvfp4(acc, df + 2 * j, dc + 2 * j, nvfp4_mma_desc(n16), sf + 4 * j,
+                        sf + 16 + 8 * j, add);
+            else
+              mma_mxfp8(acc, df + 2 * j, dc + 2 * j, mxfp8_mma_desc(n16, j), sf, sf + 16, add);
+          }
+          mma_commit(&s.empty[st]);
+          if (k + 1 == w.k1) mma_commit(&s.acc_full);
+        }
+        __syncwarp();
+      }
+      ++tiles;
+    }
+    // nothing is in flight when the tensor memory is freed
+    if (elect_one()) {
+      mma_commit(&s.end);
+      const long long t0 = clock64();
+      while (!mbar_try(&s.end, 0) && clock64() - t0 < kWaitCycles) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ==== scales: a warp to 128 rows, lane l to rows l, l + 32, l + 64, l + 96 ====
+    const int block = warp - kScaleWarp;  // 0 features, 1 and 2 columns
+    const uint8_t* base = block == 0 ? p.f_sf : p.c_sf;
+    const int64_t rows = block == 0 ? p.f_rows : p.c_rows;
+    const uint8_t* end = base + rows * p.sf_stride;
+    const bool wide = T::kFp4 && p.sf_stride % 16 == 0;
+    constexpr int kWords = T::kStageSf / 4, kAhead = T::kFp4 ? 3 : 4;
+    // the stage to fetch next
+    int item = blockIdx.x, k = 0;
+    Work w{};
+    bool have = false;
+    auto advance = [&]() {
+      while (!have || k >= w.k1) {
+        if (have) item += gridDim.x;
+        have = false;
+        if (item >= items) return false;
+        if (!work_of(item, w)) {
+          item += gridDim.x;
+          continue;
+        }
+        have = true;
+        k = w.k0;
+      }
+      return true;
+    };
+    uint32_t v[kAhead][4][kWords];
+    bool there[kAhead];
+    auto fetch = [&](uint32_t (&d)[4][kWords]) -> bool {
+      if (!advance()) return false;
+      const int64_t row0 = block == 0 ? w.f_row : w.c_row + 128 * (block - 1);
+      const int64_t at = w.k_at / 32 + (int64_t)k * T::kStageSf;
+      const int valid = (int)min(p.sf_stride - at, (int64_t)T::kStageSf);
+      const bool any = block == 0 || 128 * (block - 1) < w.cols;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + 32 * i + lane;
+        const uint8_t* q = base + row * p.sf_stride + at;
+        const bool in = any && row < rows;
+        if constexpr (T::kFp4) {
+          if (wide) {
+            const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
+            d[i][0] = x.x, d[i][1] = x.y, d[i][2] = x.z, d[i][3] = x.w;
+            continue;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j)
+          d[i][j] = in ? bytes4(q + 4 * j, valid - 4 * j, end) : 0;
+      }
+      ++k;
+      return true;
+    };
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) there[a] = fetch(v[a]);
+    bool go = true;
+    for (uint32_t n = 0; go;) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (!go) break;
+        if (!there[a]) {
+          go = false;
+          break;
+        }
+        const uint32_t st = n % stages;
+        if (!(go = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
+        if (block <= c_blocks) {
+          uint4* dst = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
+                                                block * T::kSfBlock) + lane;
+#pragma unroll
+          for (int j = 0; j < kWords; ++j)
+            dst[32 * j] = make_uint4(v[a][0][j], v[a][1][j], v[a][2][j], v[a][3][j]);
+          fence_smem_async();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.full[st]);
+        ++n;
+        there[a] = fetch(v[a]);
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, 512);
+}
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's function that makes tensor maps (the library links the runtime alone).
+EncodeTiled encode_tiled() {
+  static const EncodeTiled f = [] {
+    void* at = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      at = nullptr;
+    return reinterpret_cast<EncodeTiled>(at);
+  }();
+  return f;
+}
+
+// rows x bytes, boxes of `box` rows of one swizzle line; false if it cannot be made
+bool make_map(CUtensorMap* m, const uint8_t* at, int64_t bytes, int64_t rows, int box) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bytes};
+  const cuuint32_t sizes[2] = {kStageRow, (cuuint32_t)box}, steps[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(at), dims, strides, sizes,
+           steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KIND>
+cudaError_t launch_t(const MatmulParams& p, const CUtensorMap& f, const CUtensorMap& c,
+                     cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(matmul_kernel<KIND>, kSmem, ready);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_smem(matmul_kernel<KIND>, dim3(std::min(sm_count(), kMatmulMaxCtas)),
+                         dim3(kThreads), kSmem, st, f, c, p);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul(int kind, const MatmulParams& p, const uint8_t* f_codes,
+                          const uint8_t* c_codes, cudaStream_t st) {
+  CUtensorMap f{}, c{};
+  const int64_t bytes = kind == kMatmulNvfp4 ? p.K / 2 : p.K;
+  // without rows to sum over no copy is made: a weights' gradient of zeros
+  if (bytes > 0 && (!make_map(&f, f_codes, bytes, p.f_rows, kTileF) ||
+                    !make_map(&c, c_codes, bytes, p.c_rows, kBoxC)))
+    return cudaErrorInvalidValue;
+  switch (kind) {
+    case kMatmulNvfp4: return launch_t<kMatmulNvfp4>(p, f, c, st);
+    case kMatmulMx: return launch_t<kMatmulMx>(p, f, c, st);
+    default: return launch_t<kMatmulMxWgrad>(p, f, c, st);
+  }
+}
+
+}  // namespace nvfp4

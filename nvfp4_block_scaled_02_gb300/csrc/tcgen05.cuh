@@ -1,5 +1,6 @@
-// tcgen05.cuh -- the few Blackwell tensor-core, tensor-memory and mbarrier
-// instructions the attention kernel uses, as inline PTX.
+// tcgen05.cuh -- the few Blackwell tensor-core, tensor-memory, tensor-map and
+// mbarrier instructions that the attention and matrix product kernels use, as
+// inline PTX.
 #pragma once
 #include <cstdint>
 
@@ -142,6 +143,61 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_addr(b))
+               : "memory");
+}
+
+// ------------------------------------- products with a scale per block -----
+// Descriptor of the scales of 128 rows on their way to tensor memory: 32 lines
+// of 16 bytes, line l holds the four bytes of rows l, l + 32, l + 64, l + 96.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr16) {
+  return (uint64_t)addr16 | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+}
+// Those 512 bytes into four columns of tensor memory (the same in each quarter
+// of its lanes). Products issued after it by the same thread read them.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+               : "memory");
+}
+// E2M1 x E2M1, a UE4M3 scale per 16 (K = 64), and E4M3 x E4M3, a UE8M0 scale per
+// 32 (K = 32); M = 128, fp32 accumulators. byte: which of a column's four scale
+// bytes the MXFP8 product takes.
+__host__ __device__ constexpr uint32_t nvfp4_mma_desc(int n) {
+  return 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+__host__ __device__ constexpr uint32_t mxfp8_mma_desc(int n, int byte) {
+  return (uint32_t)byte << 4 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(128 >> 4) << 24 |
+         (uint32_t)byte << 29;
+}
+__device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
+                                          uint32_t sa, uint32_t sb, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+               "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a),
+               "l"(b), "r"(desc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+               : "memory");
+}
+__device__ __forceinline__ void mma_mxfp8(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
+                                          uint32_t sa, uint32_t sb, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+               "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a),
+               "l"(b), "r"(desc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+               : "memory");
+}
+
+// ------------------------------------------------------------ tensor maps ---
+// One arrival, and the phase waits for so many more bytes of copies.
+__device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("{\n\t.reg .b64 t;\n\t"
+               "mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(smem_addr(b)),
+               "r"(bytes)
+               : "memory");
+}
+// A box of a two-dimensional map, its first value at (x, y), to shared memory.
+__device__ __forceinline__ void tma_load(uint32_t dst, const void* map, int x, int y, uint64_t* b) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+               "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y),
+               "r"(smem_addr(b))
                : "memory");
 }
 

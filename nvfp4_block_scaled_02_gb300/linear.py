@@ -1,0 +1,221 @@
+"""Binding of the quantised linear layer's operators: products of NVFP4 and MXFP8
+encodings grouped by expert. Like the package's other entry points these only
+check and marshal arguments; ``include/nvfp4.h`` states what each computes.
+
+    a = nvfp4_quantize_per_token(x, Config(), dequant=False)
+    y = nvfp4_grouped_matmul(a, a["row_amax"], w, w_amax, group_start, workspace=ws)
+"""
+from __future__ import annotations
+
+import ctypes as C
+import struct
+
+import torch
+
+from . import Config, SCALE_E4M3, _check, _i32, _i64, _vp
+from .kv import _BF16, _I32, _elsewhere, _lib, _optional, _refuse, _stream, _typed, _workspace
+
+_F32 = (torch.float32,)
+_U8 = (torch.uint8, torch.int8)
+
+
+class _Operand(C.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("amax", _vp), ("amax_count", _i64),
+                ("scale_max", C.c_float)]
+
+
+_OPERAND = struct.Struct("@3Pqf4x")
+assert _OPERAND.size == C.sizeof(_Operand)
+
+
+def declare(L: C.CDLL) -> None:
+    """Argument types of the library's entry points of this module."""
+    size = C.c_size_t
+    L.nvfp4_grouped_matmul.argtypes = [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, size, _vp,
+                                       _vp]
+    L.nvfp4_mx_grouped_matmul.argtypes = [_vp] * 4 + [_i64] * 4 + [_vp, _vp, _vp, size, _vp, _vp]
+    L.nvfp4_mx_grouped_wgrad.argtypes = [_vp] * 4 + [_i64] * 4 + [_vp, _vp, _i32, _vp, size, _vp,
+                                                                  _vp]
+    for name in ("nvfp4_grouped_matmul", "nvfp4_mx_grouped_matmul", "nvfp4_mx_grouped_wgrad"):
+        getattr(L, name).restype = C.c_int
+    L.nvfp4_grouped_matmul_ws_bytes.argtypes = []
+    L.nvfp4_grouped_matmul_ws_bytes.restype = size
+
+
+def grouped_matmul_workspace(device) -> torch.Tensor:
+    """A zeroed workspace for the three grouped products, for calls of any size:
+    it serves one call at a time and is allocated and cleared once."""
+    return _workspace(_lib().nvfp4_grouped_matmul_ws_bytes(), device)
+
+
+def _bytes(t: torch.Tensor, name: str, n: int, dev: int) -> int:
+    """An encoding's array of exactly n bytes."""
+    if t.dtype not in _U8 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _refuse(t, name, None, _U8, dev)
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} bytes; the call needs {n}")
+    return t.data_ptr()
+
+
+def _rows_of(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """Rows and bytes per row of an encoding's codes."""
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be [rows, bytes] or [slices, rows, bytes]")
+    width = t.shape[-1]
+    return (t.numel() // width if width else 0), width
+
+
+def _groups_of(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """Groups, rows of a group and bytes per row of the weights' codes."""
+    if t.dim() == 2:
+        return 1, t.shape[0], t.shape[1]
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, bytes] or [groups, rows, bytes]")
+    return tuple(t.shape)
+
+
+def _starts(start: torch.Tensor | None, groups: int, dev: int) -> int:
+    if start is None:
+        if groups != 1:
+            raise ValueError(f"group_start is needed with {groups} groups")
+        return 0
+    return _typed(start, "group_start", (groups + 1,), torch.int32, dev)
+
+
+def _result(out, shape, dtypes, device, dev: int):
+    if out is None:
+        out = torch.empty(shape, dtype=dtypes[0], device=device)
+        return out, out.data_ptr()
+    if out.dtype not in dtypes or out.shape != shape or out.get_device() != dev or (
+            not out.is_contiguous()):
+        _refuse(out, "out", shape, dtypes, dev)
+    return out, out.data_ptr()
+
+
+def _ws(workspace, device, dev: int):
+    if workspace is None:
+        workspace = grouped_matmul_workspace(device)
+    return workspace, _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel()
+
+
+def _outer_max(cfg: Config | None, name: str) -> float:
+    if cfg is None:
+        return 0.0
+    if cfg.scale_fmt != SCALE_E4M3:
+        raise ValueError(f"{name}: the products take E4M3 block scales only")
+    return cfg.scale_max or (256.0 if cfg.four_over_six else 448.0)
+
+
+def nvfp4_grouped_matmul(a: dict, a_amax: torch.Tensor, b: dict, b_amax: torch.Tensor,
+                         group_start: torch.Tensor | None = None, a_cfg: Config | None = None,
+                         b_cfg: Config | None = None, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 [rows, out_cols]: the NVFP4 rows of `a` (a row encoding: "codes" and
+    "scales") times the weights of each row's group, `b` ("codes" [groups, out_cols,
+    cols/2], or [out_cols, cols/2] for one group). a_amax: fp32 [1] or [rows] (as
+    nvfp4_quantize_per_token's row_amax); b_amax: fp32 [groups]. group_start: int32
+    [groups + 1]; rows outside of it are left as they are in `out` (unset in a fresh
+    one). a_cfg, b_cfg: how the operands were encoded (Four-Over-Six and scale_max set
+    the outer scale). workspace: from grouped_matmul_workspace; a fresh one is cleared
+    for the call when none is given."""
+    ac, bc = a["codes"], b["codes"]
+    dev = ac.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_grouped_matmul(a, a_amax, b, b_amax, group_start, a_cfg, b_cfg, out,
+                                        workspace, status)
+    T, half = _rows_of(ac, "a codes")
+    E, N, bhalf = _groups_of(bc, "b codes")
+    if half != bhalf:
+        raise ValueError(f"a has rows of {2 * half} values, b of {2 * bhalf}")
+    n = a_amax.numel()
+    if n != 1 and n != T:
+        raise ValueError(f"a_amax holds {n} elements; the call needs 1 or {T}")
+    pa = _OPERAND.pack(_bytes(ac, "a codes", T * half, dev),
+                       _bytes(a["scales"], "a scales", T * half // 8, dev),
+                       _optional(a_amax, "a_amax", n, _F32, dev), n, _outer_max(a_cfg, "a_cfg"))
+    if b_amax.numel() != E:
+        raise ValueError(f"b_amax holds {b_amax.numel()} elements; the call needs {E}")
+    pb = _OPERAND.pack(_bytes(bc, "b codes", E * N * half, dev),
+                       _bytes(b["scales"], "b scales", E * N * half // 8, dev),
+                       _optional(b_amax, "b_amax", E, _F32, dev), E, _outer_max(b_cfg, "b_cfg"))
+    start = _starts(group_start, E, dev)
+    out, to = _result(out, (T, N), _BF16, ac.device, dev)
+    workspace, ws, ws_bytes = _ws(workspace, ac.device, dev)
+    code = _lib().nvfp4_grouped_matmul(
+        pa, pb, T, E, N, 2 * half, start, to, ws, ws_bytes,
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+    if code:
+        _check("nvfp4_grouped_matmul", code)
+    return out
+
+
+def nvfp4_mx_grouped_matmul(a: dict, b: dict, group_start: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None,
+                            status: torch.Tensor | None = None) -> torch.Tensor:
+    """nvfp4_grouped_matmul with MXFP8 operands (as nvfp4_mx_quantize and
+    nvfp4_requant_transpose give them): `a` "codes" [rows, cols], `b` "codes" [groups,
+    out_cols, cols]."""
+    ac, bc = a["codes"], b["codes"]
+    dev = ac.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_mx_grouped_matmul(a, b, group_start, out, workspace, status)
+    T, K = _rows_of(ac, "a codes")
+    E, N, bk = _groups_of(bc, "b codes")
+    if K != bk:
+        raise ValueError(f"a has rows of {K} values, b of {bk}")
+    ins = (_bytes(ac, "a codes", T * K, dev), _bytes(a["scales"], "a scales", T * K // 32, dev),
+           _bytes(bc, "b codes", E * N * K, dev),
+           _bytes(b["scales"], "b scales", E * N * K // 32, dev))
+    start = _starts(group_start, E, dev)
+    out, to = _result(out, (T, N), _BF16, ac.device, dev)
+    workspace, ws, ws_bytes = _ws(workspace, ac.device, dev)
+    code = _lib().nvfp4_mx_grouped_matmul(
+        *ins, T, E, N, K, start, to, ws, ws_bytes,
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+    if code:
+        _check("nvfp4_mx_grouped_matmul", code)
+    return out
+
+
+def nvfp4_mx_grouped_wgrad(g: dict, x: dict, group_start: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None,
+                           out_dtype: torch.dtype = torch.bfloat16,
+                           workspace: torch.Tensor | None = None,
+                           status: torch.Tensor | None = None) -> torch.Tensor:
+    """Every group's weight gradient [groups, out_rows, out_cols] (bf16 or fp32): the
+    sum over the group's rows of g's times x's values, both MXFP8 column encodings
+    ("codes" [out_rows, rows] and [out_cols, rows], as nvfp4_mx_quantize's "col").
+    Every entry of group_start is a multiple of 32."""
+    gc, xc = g["codes"], x["codes"]
+    dev = gc.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_mx_grouped_wgrad(g, x, group_start, out, out_dtype, workspace, status)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bf16 or fp32, got {out_dtype}")
+    (sn, N, T), (sk, K, xt) = _groups_of(gc, "g codes"), _groups_of(xc, "x codes")
+    if sn != 1 or sk != 1:
+        raise ValueError("g and x must be one matrix each")
+    if T != xt:
+        raise ValueError(f"g has {T} rows, x {xt}")
+    E = 1 if group_start is None else group_start.numel() - 1
+    if E < 0:
+        raise ValueError("group_start must hold groups + 1 entries")
+    ins = (_bytes(gc, "g codes", N * T, dev), _bytes(g["scales"], "g scales", N * T // 32, dev),
+           _bytes(xc, "x codes", K * T, dev), _bytes(x["scales"], "x scales", K * T // 32, dev))
+    start = _starts(group_start, E, dev)
+    if out is not None:
+        out_dtype = torch.float32 if out.dtype is torch.float32 else torch.bfloat16
+    f32 = out_dtype is torch.float32
+    out, to = _result(out, (E, N, K), _F32 if f32 else _BF16, gc.device, dev)
+    workspace, ws, ws_bytes = _ws(workspace, gc.device, dev)
+    code = _lib().nvfp4_mx_grouped_wgrad(
+        *ins, T, E, N, K, start, to, f32, ws, ws_bytes,
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+    if code:
+        _check("nvfp4_mx_grouped_wgrad", code)
+    return out
