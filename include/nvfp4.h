@@ -620,6 +620,51 @@ NVFP4_API nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint
                                               void* out, int32_t out_fp32, void* workspace,
                                               size_t ws_bytes, int32_t* status, void* stream);
 
+/* The residual's addition, a token's RMS norm and its encoding in one pass:
+ *   h = bf16(x + residual)                   (h = x without a residual)
+ *   y = h * r * weight, r = rsqrt(mean(h^2) + eps)                  (fp32)
+ * x, residual, h: bf16 [rows][cols]; weight: bf16 [cols]; cols up to 16384. h is
+ * written iff a residual is given, and may be x or residual. y, if not NULL,
+ * receives bf16(y).
+ * target NVFP4_TARGET_MXFP8 (cols % 32 == 0): out receives y's MXFP8 row encoding
+ * as nvfp4_mx_quantize's (of the fp32 y, RNE).
+ * target NVFP4_TARGET_NVFP4 (cols % 16 == 0): y's NVFP4 row encoding with E4M3
+ * scales, RNE, four_over_six 0 or 1 (MSE rule). With global_amax (fp32 [1],
+ * current or stale) its steps are nvfp4_quantize's on the fp32 y. Without,
+ * each row has its own outer scale and row_amax (fp32 [rows]) receives r *
+ * max|h * weight|; codes and block scales are those of nvfp4_quantize_per_token's
+ * steps on h * weight, to which r is a common factor: they do not depend on how
+ * the sum of squares rounds. out->choice (may be NULL) receives ceil(cols/512)
+ * words a row; out->dequant (may be NULL) the values that the codes stand for.
+ * cfg: blocks NVFP4_BLOCKS_ROW, rounding NVFP4_ROUND_RNE.
+ * Data errors: NVFP4_DEV_NONFINITE_INPUT (also for a sum of squares or a product
+ * h * weight past fp32), NVFP4_DEV_BAD_AMAX. A row whose mean square and eps are 0
+ * gives zeros.
+ * Errors: NULL required pointers, target, eps negative or not finite, and config
+ * fields out of range, dequant with MXFP8 (NVFP4_ERR_ENUM), sizes, misaligned
+ * buffers. */
+NVFP4_API nvfp4_status nvfp4_add_rms_norm(const nvfp4_config* cfg, int32_t target, const void* x,
+                                          const void* residual, const void* weight, int64_t rows,
+                                          int64_t cols, float eps, void* h, void* y,
+                                          const float* global_amax, float* row_amax,
+                                          const nvfp4_out* out, int32_t* status, void* stream);
+
+/* Its gradient, the encoding's derivative taken as 1: gy (bf16 [rows][cols]) is
+ * the loss's gradient of y, gh (bf16, may be NULL) that of h by its other way,
+ * the residual stream; h is the forward's. With u = gy * weight:
+ *   gx = r * (u - h * r^2 * mean(u * h)) + gh      (of x and of the residual)
+ *   gw = sum over the rows of gy * h * r           (fp32 [cols], overwritten)
+ * cols % 16 == 0, up to 16384. gx may be gy, h or gh. gw is summed in a fixed
+ * order: the same inputs give the same bits on the same device.
+ * workspace: device memory, >= nvfp4_add_rms_norm_ws_bytes() bytes, 16-byte
+ * aligned, of any content; it serves one call at a time.
+ * Errors: as nvfp4_add_rms_norm; NVFP4_ERR_SHAPE for a workspace too small. */
+NVFP4_API size_t nvfp4_add_rms_norm_ws_bytes(void);
+NVFP4_API nvfp4_status nvfp4_add_rms_norm_bwd(const void* gy, const void* h, const void* weight,
+                                              const void* gh, int64_t rows, int64_t cols,
+                                              float eps, void* gx, float* gw, void* workspace,
+                                              size_t ws_bytes, int32_t* status, void* stream);
+
 /* ---- diagnostics: the device codecs element by element -------------------
  * For exhaustive checks of the conversions the kernels use. op:
  *   0: out[i] = E2M1 RNE code of in[i]

@@ -34,7 +34,8 @@ __all__ = [
     "alloc_kv_cache", "kv_attention_workspace", "nvfp4_kv_append", "nvfp4_kv_attention",
     "nvfp4_kv_plan", "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_bwd", "qk_norm_rope_workspace",
     "grouped_matmul_workspace", "nvfp4_grouped_matmul", "nvfp4_mx_grouped_matmul",
-    "nvfp4_mx_grouped_wgrad",
+    "nvfp4_mx_grouped_wgrad", "nvfp4_add_rms_norm", "nvfp4_add_rms_norm_bwd",
+    "add_rms_norm_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -651,5 +652,6 @@ from .kv import (alloc_kv_cache, kv_attention_workspace, nvfp4_kv_append,  # noq
                  nvfp4_kv_attention, nvfp4_kv_plan, nvfp4_qk_norm_rope, nvfp4_qk_norm_rope_bwd,
                  qk_norm_rope_workspace)
 from . import linear  # noqa: E402  (the linear layer's operators use kv's checks)
-from .linear import (grouped_matmul_workspace, nvfp4_grouped_matmul,  # noqa: E402
+from .linear import (add_rms_norm_workspace, grouped_matmul_workspace,  # noqa: E402
+                     nvfp4_add_rms_norm, nvfp4_add_rms_norm_bwd, nvfp4_grouped_matmul,
                      nvfp4_mx_grouped_matmul, nvfp4_mx_grouped_wgrad)

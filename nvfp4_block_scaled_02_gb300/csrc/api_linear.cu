@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "matmul.h"
+#include "norm.h"
 
 namespace {
 
@@ -161,6 +162,91 @@ nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint8_t* g_sca
   fill_ws(p, workspace);
   return cuda_status(nvfp4::launch_matmul(nvfp4::kMatmulMxWgrad, p, x_codes, g_codes,
                                           static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_add_rms_norm(const nvfp4_config* cfg, int32_t target, const void* x,
+                                const void* residual, const void* weight, int64_t rows,
+                                int64_t cols, float eps, void* h, void* y,
+                                const float* global_amax, float* row_amax, const nvfp4_out* out,
+                                int32_t* status, void* stream) {
+  if (!cfg) return NVFP4_ERR_NULL;
+  const bool fp4 = target == NVFP4_TARGET_NVFP4;
+  if ((!fp4 && target != NVFP4_TARGET_MXFP8) || !(eps >= 0.0f) || !std::isfinite(eps) ||
+      cfg->blocks != NVFP4_BLOCKS_ROW || cfg->rounding != NVFP4_ROUND_RNE)
+    return NVFP4_ERR_ENUM;
+  if (fp4 && (cfg->scale_fmt != NVFP4_SCALE_E4M3 || !(cfg->scale_max >= 0.0f) ||
+              !std::isfinite(cfg->scale_max) ||
+              (cfg->four_over_six != 0 && cfg->four_over_six != 1) ||
+              (cfg->four_over_six && cfg->four_over_six_rule != NVFP4_FOS_MSE)))
+    return NVFP4_ERR_ENUM;
+  if (rows < 0 || cols < 0 || rows > kMaxI32 || cols > nvfp4::kNormMaxCols ||
+      cols % (fp4 ? 16 : 32) != 0)
+    return NVFP4_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return NVFP4_OK;
+  if (!x || !weight || !out || !out->codes || !out->scales || (residual && !h) ||
+      (fp4 && !global_amax && !row_amax))
+    return NVFP4_ERR_NULL;
+  if (!fp4 && out->dequant) return NVFP4_ERR_ENUM;
+  for (const void* q : {x, residual, weight, (const void*)h, (const void*)y,
+                        (const void*)out->codes, (const void*)out->scales,
+                        (const void*)out->choice, (const void*)out->dequant})
+    if (!aligned(q, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(global_amax, 4) || !aligned(row_amax, 4) || !aligned(status, 4))
+    return NVFP4_ERR_ALIGN;
+  nvfp4::NormParams p{};
+  p.x = static_cast<const uint4*>(x);
+  p.res = static_cast<const uint4*>(residual);
+  p.w = static_cast<const uint4*>(weight);
+  p.R = rows;
+  p.C = (int32_t)cols;
+  p.eps = eps;
+  p.h = static_cast<uint4*>(h);
+  p.y = static_cast<uint4*>(y);
+  p.gamax = fp4 ? global_amax : nullptr;
+  p.M = cfg->scale_max > 0.0f ? cfg->scale_max : cfg->four_over_six ? 256.0f : 448.0f;
+  p.row_amax = row_amax;
+  p.codes = out->codes;
+  p.scales = out->scales;
+  p.choice = cfg->four_over_six ? out->choice : nullptr;
+  p.dq = static_cast<uint4*>(out->dequant);
+  p.status = status;
+  return cuda_status(nvfp4::launch_norm(p, fp4 ? 1 : 0, fp4 && cfg->four_over_six != 0,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_add_rms_norm_ws_bytes(void) { return nvfp4::kNormWsBytes; }
+
+nvfp4_status nvfp4_add_rms_norm_bwd(const void* gy, const void* h, const void* weight,
+                                    const void* gh, int64_t rows, int64_t cols, float eps,
+                                    void* gx, float* gw, void* workspace, size_t ws_bytes,
+                                    int32_t* status, void* stream) {
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return NVFP4_ERR_ENUM;
+  if (rows < 0 || cols < 0 || rows > kMaxI32 || cols > nvfp4::kNormMaxCols || cols % 16 != 0)
+    return NVFP4_ERR_SHAPE;
+  if (cols == 0) return NVFP4_OK;
+  if (!gw) return NVFP4_ERR_NULL;
+  if (!aligned(gw, 16)) return NVFP4_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0)  // a sum over nothing
+    return cuda_status(nvfp4::launch_zero_words(reinterpret_cast<uint32_t*>(gw), cols, st));
+  if (!gy || !h || !weight || !gx || !workspace) return NVFP4_ERR_NULL;
+  if (ws_bytes < nvfp4::kNormWsBytes) return NVFP4_ERR_SHAPE;
+  for (const void* q : {gy, h, weight, gh, (const void*)gx, (const void*)workspace})
+    if (!aligned(q, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(status, 4)) return NVFP4_ERR_ALIGN;
+  nvfp4::NormBwdParams p{};
+  p.gy = static_cast<const uint4*>(gy);
+  p.h = static_cast<const uint4*>(h);
+  p.w = static_cast<const uint4*>(weight);
+  p.gh = static_cast<const uint4*>(gh);
+  p.R = rows;
+  p.C = (int32_t)cols;
+  p.eps = eps;
+  p.gx = static_cast<uint4*>(gx);
+  p.gw = gw;
+  p.part = static_cast<float*>(workspace);
+  p.status = status;
+  return cuda_status(nvfp4::launch_norm_bwd(p, st));
 }
 
 }  // extern "C"

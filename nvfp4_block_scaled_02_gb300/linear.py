@@ -1,8 +1,9 @@
-"""Binding of the quantised linear layer's operators: products of NVFP4 and MXFP8
-encodings grouped by expert. Like the package's other entry points these only
+"""Binding of the quantised linear layer's operators: the residual norm that encodes
+its input (and its gradient), products of NVFP4 and MXFP8 encodings grouped by
+expert. Like the package's other entry points these only
 check and marshal arguments; ``include/nvfp4.h`` states what each computes.
 
-    a = nvfp4_quantize_per_token(x, Config(), dequant=False)
+    a = nvfp4_add_rms_norm(x, weight, residual)
     y = nvfp4_grouped_matmul(a, a["row_amax"], w, w_amax, group_start, workspace=ws)
 """
 from __future__ import annotations
@@ -12,7 +13,7 @@ import struct
 
 import torch
 
-from . import Config, SCALE_E4M3, _check, _i32, _i64, _vp
+from . import (Config, SCALE_E4M3, TARGET_MXFP8, TARGET_NVFP4, _check, _i32, _i64, _Out, _vp)
 from .kv import _BF16, _I32, _elsewhere, _lib, _optional, _refuse, _stream, _typed, _workspace
 
 _F32 = (torch.float32,)
@@ -36,10 +37,16 @@ def declare(L: C.CDLL) -> None:
     L.nvfp4_mx_grouped_matmul.argtypes = [_vp] * 4 + [_i64] * 4 + [_vp, _vp, _vp, size, _vp, _vp]
     L.nvfp4_mx_grouped_wgrad.argtypes = [_vp] * 4 + [_i64] * 4 + [_vp, _vp, _i32, _vp, size, _vp,
                                                                   _vp]
-    for name in ("nvfp4_grouped_matmul", "nvfp4_mx_grouped_matmul", "nvfp4_mx_grouped_wgrad"):
+    L.nvfp4_add_rms_norm.argtypes = [_vp, _i32, _vp, _vp, _vp, _i64, _i64, C.c_float, _vp, _vp,
+                                     _vp, _vp, _vp, _vp, _vp]
+    L.nvfp4_add_rms_norm_bwd.argtypes = [_vp] * 4 + [_i64, _i64, C.c_float, _vp, _vp, _vp, size,
+                                                     _vp, _vp]
+    for name in ("nvfp4_grouped_matmul", "nvfp4_mx_grouped_matmul", "nvfp4_mx_grouped_wgrad",
+                 "nvfp4_add_rms_norm", "nvfp4_add_rms_norm_bwd"):
         getattr(L, name).restype = C.c_int
-    L.nvfp4_grouped_matmul_ws_bytes.argtypes = []
-    L.nvfp4_grouped_matmul_ws_bytes.restype = size
+    for name in ("nvfp4_grouped_matmul_ws_bytes", "nvfp4_add_rms_norm_ws_bytes"):
+        getattr(L, name).argtypes = []
+        getattr(L, name).restype = size
 
 
 def grouped_matmul_workspace(device) -> torch.Tensor:
@@ -219,3 +226,122 @@ def nvfp4_mx_grouped_wgrad(g: dict, x: dict, group_start: torch.Tensor | None = 
     if code:
         _check("nvfp4_mx_grouped_wgrad", code)
     return out
+
+
+def _matrix(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    if (t.dtype in _BF16 and t.shape == shape and t.get_device() == dev >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _refuse(t, name, shape, _BF16, dev)
+
+
+def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor,
+                       residual: torch.Tensor | None = None, eps: float = 1e-6,
+                       target: int = TARGET_NVFP4, cfg: Config | None = None,
+                       global_amax: torch.Tensor | None = None, dequant: bool = False,
+                       h: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                       out: dict | None = None, row_amax: torch.Tensor | None = None,
+                       status: torch.Tensor | None = None) -> dict:
+    """h = x + residual, its RMS norm times weight, and the row encoding of that: NVFP4
+    with an outer scale for each row ("row_amax") or from global_amax (fp32 [1]), or
+    MXFP8 (target). x, residual: bf16 [rows, cols]; weight: bf16 [cols]. Returns {"h",
+    "y", "codes", "scales", "choice", "dequant", "row_amax"}: h is x itself without a
+    residual, y (bf16) is written where a buffer is passed, dequant (NVFP4) where asked
+    for. `out`: an encoding of an earlier call. Nothing is recorded for autograd:
+    nvfp4_add_rms_norm_bwd gives the gradient."""
+    dev = x.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_add_rms_norm(x, weight, residual, eps, target, cfg, global_amax, dequant,
+                                      h, y, out, row_amax, status)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    if target not in (TARGET_MXFP8, TARGET_NVFP4):
+        raise ValueError("target must be TARGET_MXFP8 or TARGET_NVFP4")
+    R, Cc = shape = x.shape
+    device, u8, fp4 = x.device, torch.uint8, target == TARGET_NVFP4
+    cfg = cfg or Config()
+    ins = (_matrix(x, "x", shape, dev),
+           0 if residual is None else _matrix(residual, "residual", shape, dev),
+           _matrix(weight, "weight", (Cc,), dev))
+    empty = torch.empty
+    if residual is None:
+        if h is not None and h is not x:
+            raise ValueError("h is x itself without a residual")
+        h, h_at = x, 0
+    else:
+        h = empty(shape, dtype=x.dtype, device=device) if h is None else h
+        h_at = _matrix(h, "h", shape, dev)
+    fos = fp4 and bool(cfg.four_over_six)
+    per, block = (2, 16) if fp4 else (1, 32)
+    words = R * ((Cc + 511) // 512)
+    if out is None:
+        out = {"codes": empty((R, Cc // per), dtype=u8, device=device),
+               "scales": empty((R, Cc // block), dtype=u8, device=device),
+               "choice": empty((R, (Cc + 511) // 512), dtype=torch.int32, device=device)
+               if fos else None,
+               "dequant": empty(shape, dtype=torch.bfloat16, device=device)
+               if dequant and fp4 else None}
+        o = _Out(out["codes"].data_ptr(), out["scales"].data_ptr(),
+                 out["choice"].data_ptr() if fos else None,
+                 None if out["dequant"] is None else out["dequant"].data_ptr())
+    else:
+        o = _Out(_bytes(out["codes"], "out codes", R * Cc // per, dev),
+                 _bytes(out["scales"], "out scales", R * Cc // block, dev),
+                 _optional(out.get("choice"), "out choice", words, _I32, dev) if fos else None,
+                 _optional(out.get("dequant"), "out dequant", R * Cc, _BF16, dev) if fp4 else None)
+    tensor = fp4 and global_amax is not None
+    if fp4 and not tensor and row_amax is None:
+        row_amax = empty(R, dtype=torch.float32, device=device)
+    c = cfg.c()
+    code = _lib().nvfp4_add_rms_norm(
+        C.addressof(c), target, *ins, R, Cc, eps, h_at,
+        0 if y is None else _matrix(y, "y", shape, dev),
+        _optional(global_amax, "global_amax", 1, _F32, dev) if tensor else 0,
+        _optional(row_amax, "row_amax", R, _F32, dev) if fp4 and not tensor else 0,
+        C.addressof(o), 0 if status is None else _optional(status, "status", 1, _I32, dev),
+        _stream(dev))
+    if code:
+        _check("nvfp4_add_rms_norm", code)
+    return {"h": h, "y": y, "codes": out["codes"], "scales": out["scales"],
+            "choice": out.get("choice"), "dequant": out.get("dequant"),
+            "row_amax": row_amax if fp4 and not tensor else None}
+
+
+def add_rms_norm_workspace(device) -> torch.Tensor:
+    """A workspace for nvfp4_add_rms_norm_bwd, for calls of any size: it serves one
+    call at a time and needs no clearing."""
+    return torch.empty((_lib().nvfp4_add_rms_norm_ws_bytes() + 3) // 4, dtype=torch.int32,
+                       device=device)
+
+
+def nvfp4_add_rms_norm_bwd(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                           gh: torch.Tensor | None = None, eps: float = 1e-6,
+                           workspace: torch.Tensor | None = None, gx: torch.Tensor | None = None,
+                           status: torch.Tensor | None = None) -> dict:
+    """Gradient of nvfp4_add_rms_norm from the gradient of its normed output (the
+    encoding passed straight through), its h and, where the residual stream goes on, the
+    gradient gh of h: {"gx" (bf16, of x and of the residual), "gw" (fp32 [cols])}.
+    workspace: from add_rms_norm_workspace; a fresh one is taken when none is given."""
+    dev = h.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_add_rms_norm_bwd(gy, h, weight, gh, eps, workspace, gx, status)
+    if h.dim() != 2:
+        raise ValueError("h must be [rows, cols]")
+    R, Cc = shape = h.shape
+    ins = (_matrix(gy, "gy", shape, dev), _matrix(h, "h", shape, dev),
+           _matrix(weight, "weight", (Cc,), dev),
+           0 if gh is None else _matrix(gh, "gh", shape, dev))
+    if gx is None:
+        gx = torch.empty(shape, dtype=h.dtype, device=h.device)
+    gw = torch.empty(Cc, dtype=torch.float32, device=h.device)
+    if workspace is None:
+        workspace = add_rms_norm_workspace(h.device)
+    code = _lib().nvfp4_add_rms_norm_bwd(
+        *ins, R, Cc, eps, _matrix(gx, "gx", shape, dev), gw.data_ptr(),
+        _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel(),
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+    if code:
+        _check("nvfp4_add_rms_norm_bwd", code)
+    return {"gx": gx, "gw": gw}
