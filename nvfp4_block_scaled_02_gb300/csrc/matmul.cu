@@ -2,6 +2,8 @@
 #include "matmul.h"
 #include "tcgen05.cuh"
 
+#include <type_traits>
+
 namespace nvfp4 {
 
 namespace {
@@ -35,22 +37,42 @@ __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile
   return true;
 }
 
-// `valid` bytes (0 to 4) from p on, the others 0; [base, end) is the array, base 16-byte aligned.
-__device__ __forceinline__ uint32_t bytes4(const uint8_t* p, int valid, const uint8_t* end) {
-  if (valid <= 0) return 0;
-  valid = min(valid, 4);
-  const uint32_t off = (uint32_t)((uintptr_t)p & 3);
-  const uint8_t* a = p - off;
-  auto word = [&](const uint8_t* q) {
-    if (q + 4 <= end) return __ldg(reinterpret_cast<const uint32_t*>(q));
-    uint32_t w = 0;
-    for (int i = 0; i < 3; ++i)
-      if (q + i < end) w |= (uint32_t)q[i] << (8 * i);
-    return w;
-  };
-  const uint32_t lo = word(a), hi = off + valid > 4 ? word(a + 4) : 0;
-  const uint32_t v = __funnelshift_r(lo, hi, 8 * off);
-  return valid >= 4 ? v : v & ((1u << (8 * valid)) - 1);
+// 16 bytes at q (16-byte aligned); those at `end` and after it are 0 and not read.
+__device__ __forceinline__ uint4 bytes16(const uint8_t* q, const uint8_t* end) {
+  if (q + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(q));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)
+      if (q + 4 * j + i < end) w[j] |= (uint32_t)q[4 * j + i] << (8 * i);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Bytes off .. off + 15 of the 32 in lo and hi (off < 16).
+__device__ __forceinline__ uint4 window16(uint4 lo, uint4 hi, uint32_t off) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const uint32_t s = 8 * (off & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
+                    __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+}
+// x without the bytes from `n` on.
+__device__ __forceinline__ uint4 first_bytes(uint4 x, int n) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int m = n - 4 * j;
+    w[j] = m >= 4 ? w[j] : m <= 0 ? 0 : w[j] & ((1u << (8 * m)) - 1);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int KIND>
@@ -61,6 +83,7 @@ struct Kind {
   static constexpr int kStepK = kFp4 ? 64 : 32;     // values of a product
   static constexpr int kStageSf = kFp4 ? 16 : 4;    // scale bytes of a row in a stage
   static constexpr int kSfBlock = 128 * kStageSf;   // scale bytes of 128 rows in a stage
+  static constexpr int kFetch = 16 / kStageSf;      // stages whose scales are fetched together
 };
 
 // What one CTA does at a time: features f0 .. of a group times some of its
@@ -73,6 +96,30 @@ struct Work {
   int k0, k1;
   int tile, part, parts;
 };
+
+// Fills N slots, then empties and refills them in turn until emptying one fails.
+template <int N, int I = 0, class Fetch>
+__device__ __forceinline__ void fill_ring(Fetch& fetch) {
+  if constexpr (I < N) {
+    fetch(std::integral_constant<int, I>{});
+    fill_ring<N, I + 1>(fetch);
+  }
+}
+template <int N, int I = 0, class Fetch, class Store>
+__device__ __forceinline__ bool turn_ring(Fetch& fetch, Store& store) {
+  if constexpr (I < N) {
+    if (!store(std::integral_constant<int, I>{})) return false;
+    fetch(std::integral_constant<int, I>{});
+    return turn_ring<N, I + 1>(fetch, store);
+  }
+  return true;
+}
+template <int N, class Fetch, class Store>
+__device__ __forceinline__ void ring_of(Fetch& fetch, Store& store) {
+  fill_ring<N>(fetch);
+  while (turn_ring<N>(fetch, store)) {
+  }
+}
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -103,10 +150,15 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
   const int share = (p.E + kThreads - 1) / kThreads;
   const int e0 = min(tid * share, p.E), e1 = min(e0 + share, p.E);
   int mine = 0, most = 0;
+  // whether the 16 scale bytes of a row that are fetched together are aligned
+  bool sf_aligned = p.sf_stride % 16 == 0;
   for (int e = e0; e < e1; ++e) {
     int64_t a = p.start ? p.start[e] : 0, b = p.start ? p.start[e + 1] : rows_all;
     bool bad = a < 0 || b < a || b > rows_all;
-    if (T::kWgrad) bad = bad || (a | b) % 32 != 0;
+    if (T::kWgrad) {
+      bad = bad || (a | b) % 32 != 0;
+      sf_aligned = sf_aligned && a % 512 == 0;
+    }
     if (bad) {
       if (blockIdx.x == 0) flag(p.status, NVFP4_DEV_BAD_INDEX);
       a = b = 0;
@@ -136,7 +188,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     mbar_init(&s.end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncthreads();
+  sf_aligned = __syncthreads_and(sf_aligned);
   int before = incl - mine, total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s.scan[w];
@@ -186,9 +238,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     w.c_row = (T::kWgrad ? 0 : row) + w.c0;
     w.steps = (int)((sum + T::kStepK - 1) / T::kStepK);
     const int n = (int)((sum + T::kStageK - 1) / T::kStageK);
-    w.parts = min(split, max(1, n / 2));
-    w.k0 = (int)((int64_t)n * w.part / w.parts);
-    w.k1 = (int)((int64_t)n * (w.part + 1) / w.parts);
+    // a part is of whole fetches of scales, and of two stages at least
+    const int units = (n + T::kFetch - 1) / T::kFetch;
+    w.parts = min(split, max(1, min(n / 2, units)));
+    w.k0 = (int)((int64_t)units * w.part / w.parts) * T::kFetch;
+    w.k1 = min(n, (int)((int64_t)units * (w.part + 1) / w.parts) * T::kFetch);
     return w.part < w.parts && w.cols > 0;
   };
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
@@ -406,81 +460,94 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     const int block = warp - kScaleWarp;  // 0 features, 1 and 2 columns
     const uint8_t* base = block == 0 ? p.f_sf : p.c_sf;
     const int64_t rows = block == 0 ? p.f_rows : p.c_rows;
-    const uint8_t* end = base + rows * p.sf_stride;
-    const bool wide = T::kFp4 && p.sf_stride % 16 == 0;
-    constexpr int kWords = T::kStageSf / 4, kAhead = T::kFp4 ? 3 : 4;
-    // the stage to fetch next
-    int item = blockIdx.x, k = 0;
-    Work w{};
-    bool have = false;
-    auto advance = [&]() {
-      while (!have || k >= w.k1) {
-        if (have) item += gridDim.x;
-        have = false;
-        if (item >= items) return false;
-        if (!work_of(item, w)) {
-          item += gridDim.x;
-          continue;
-        }
-        have = true;
-        k = w.k0;
-      }
-      return true;
-    };
-    uint32_t v[kAhead][4][kWords];
-    bool there[kAhead];
-    auto fetch = [&](uint32_t (&d)[4][kWords]) -> bool {
-      if (!advance()) return false;
-      const int64_t row0 = block == 0 ? w.f_row : w.c_row + 128 * (block - 1);
-      const int64_t at = w.k_at / 32 + (int64_t)k * T::kStageSf;
-      const int valid = (int)min(p.sf_stride - at, (int64_t)T::kStageSf);
-      const bool any = block == 0 || 128 * (block - 1) < w.cols;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + 32 * i + lane;
-        const uint8_t* q = base + row * p.sf_stride + at;
-        const bool in = any && row < rows;
-        if constexpr (T::kFp4) {
-          if (wide) {
-            const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
-            d[i][0] = x.x, d[i][1] = x.y, d[i][2] = x.z, d[i][3] = x.w;
+    // 16 bytes of every row at a time, several fetches ahead of their use. Where they are
+    // aligned they stay as they came; else two aligned pieces are kept and cut at their use.
+    auto feed = [&](auto aligned_c, auto ahead_c) {
+      constexpr bool kAligned = decltype(aligned_c)::value;
+      constexpr int kAhead = decltype(ahead_c)::value;
+      const uint8_t* end = base + rows * p.sf_stride;
+      int item = blockIdx.x, k = 0;  // the fetch that comes next
+      Work w{};
+      bool have = false;
+      uint4 lo[kAhead][4], hi[kAligned ? 1 : kAhead][4];
+      uint32_t off[kAligned ? 1 : kAhead][4];
+      int count[kAhead], valid[kAhead];  // stages, and bytes of a row, of a fetch; 0: the end
+      auto fetch = [&](auto slot_c) {
+        constexpr int kSlot = decltype(slot_c)::value;
+        count[kSlot] = 0;
+        while (!have || k >= w.k1) {
+          if (have) item += gridDim.x;
+          have = false;
+          if (item >= items) return;
+          if (!work_of(item, w)) {
+            item += gridDim.x;
             continue;
           }
+          have = true;
+          k = w.k0;
         }
+        const int64_t row0 = block == 0 ? w.f_row : w.c_row + 128 * (block - 1);
+        const int64_t at = w.k_at / 32 + (int64_t)k * T::kStageSf;
+        const bool any = block == 0 || 128 * (block - 1) < w.cols;
+        count[kSlot] = min(T::kFetch, w.k1 - k);
+        valid[kSlot] = (int)min(p.sf_stride - at, (int64_t)16);
+        k += T::kFetch;
 #pragma unroll
-        for (int j = 0; j < kWords; ++j)
-          d[i][j] = in ? bytes4(q + 4 * j, valid - 4 * j, end) : 0;
-      }
-      ++k;
-      return true;
+        for (int i = 0; i < 4; ++i) {
+          const int64_t row = row0 + 32 * i + lane;
+          const uint8_t* q = base + row * p.sf_stride + at;
+          const bool in = any && row < rows;
+          if constexpr (kAligned) {
+            lo[kSlot][i] = in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
+          } else {
+            off[kSlot][i] = (uint32_t)((uintptr_t)q & 15);
+            q -= off[kSlot][i];
+            lo[kSlot][i] = in ? bytes16(q, end) : make_uint4(0, 0, 0, 0);
+            hi[kSlot][i] = in && off[kSlot][i] + valid[kSlot] > 16 ? bytes16(q + 16, end)
+                                                                   : make_uint4(0, 0, 0, 0);
+          }
+        }
+      };
+      uint32_t n = 0;
+      // the stages of a fetch, to shared memory; false at the end
+      auto store = [&](auto slot_c) -> bool {
+        constexpr int kSlot = decltype(slot_c)::value;
+        if (count[kSlot] == 0) return false;
+        uint32_t x[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 v = lo[kSlot][i];
+          if constexpr (!kAligned)
+            v = first_bytes(window16(v, hi[kSlot][i], off[kSlot][i]), valid[kSlot]);
+          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+        }
+        constexpr int kWords = T::kStageSf / 4;
+#pragma unroll
+        for (int c = 0; c < T::kFetch; ++c) {
+          if (c >= count[kSlot]) break;
+          const uint32_t st = n % stages;
+          if (!wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1)) return false;
+          if (block <= c_blocks) {
+            uint4* dst = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
+                                                  block * T::kSfBlock) + lane;
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+              dst[32 * j] = make_uint4(x[0][c * kWords + j], x[1][c * kWords + j],
+                                       x[2][c * kWords + j], x[3][c * kWords + j]);
+            fence_smem_async();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.full[st]);
+          ++n;
+        }
+        return true;
+      };
+      ring_of<kAhead>(fetch, store);
     };
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) there[a] = fetch(v[a]);
-    bool go = true;
-    for (uint32_t n = 0; go;) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        if (!go) break;
-        if (!there[a]) {
-          go = false;
-          break;
-        }
-        const uint32_t st = n % stages;
-        if (!(go = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
-        if (block <= c_blocks) {
-          uint4* dst = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
-                                                block * T::kSfBlock) + lane;
-#pragma unroll
-          for (int j = 0; j < kWords; ++j)
-            dst[32 * j] = make_uint4(v[a][0][j], v[a][1][j], v[a][2][j], v[a][3][j]);
-          fence_smem_async();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.full[st]);
-        ++n;
-        there[a] = fetch(v[a]);
-      }
-    }
+    if (sf_aligned)
+      feed(std::true_type{}, std::integral_constant<int, T::kFp4 ? 5 : 3>{});
+    else
+      feed(std::false_type{}, std::integral_constant<int, T::kFp4 ? 3 : 2>{});
   }
   __syncwarp();
   fence_before();
