@@ -10,7 +10,7 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kEpilogueWarps = 8;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleWarps = 3;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleWarps = 6;
 constexpr int kThreads = (kEpilogueWarps + 2 + kScaleWarps) * 32;
 constexpr int kTileF = 128, kTileC = 256;
 constexpr int kStageRow = 128;                 // code bytes of a row in a stage: one swizzle line
@@ -21,6 +21,7 @@ constexpr int kRing = 216 * 1024;              // bytes of the ring of stages
 constexpr int kSmem = kRing + 1024;            // and its alignment
 // Tensor memory: two accumulators of 256 columns that share 96, scales twice.
 constexpr int kAcc1 = 160, kScales = 416, kScalesEach = 48;
+constexpr int kPairCols = 96;                  // columns of a group from which pairs of CTAs pay
 constexpr long long kWaitCycles = 2000000000;  // about a second
 
 __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* dead,
@@ -132,7 +133,7 @@ struct Shared {
   float scale[2][kTileC];          // outer scales of a tile's columns
 };
 
-template <int KIND>
+template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__ CUtensorMap c_map,
               const MatmulParams p) {
@@ -142,7 +143,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
   __shared__ Shared s;
   uint8_t* ring = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
-  const int f_tiles = (p.N + kTileF - 1) / kTileF;
+  // this CTA of the pair, and the pair (CG = 1: a CTA by itself)
+  const int rank = CG == 2 ? (int)cluster_rank() : 0;
+  const int pair = (int)blockIdx.x / CG, pairs = (int)gridDim.x / CG;
+  const int f_tiles = (p.N + kTileF * CG - 1) / (kTileF * CG);
   const int64_t rows_all = T::kWgrad ? p.K : p.c_rows;
 
   // ---- the groups' tiles -----------------------------------------------------
@@ -180,11 +184,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
   if (tid == 0) {
     s.dead = 0;
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&s.full[i], 1 + kScaleWarps);
+      mbar_init(&s.full[i], 1 + CG * kScaleWarps);
       mbar_init(&s.empty[i], 1);
     }
     mbar_init(&s.acc_full, 1);
-    mbar_init(&s.acc_free, kEpilogueWarps);
+    mbar_init(&s.acc_free, CG * kEpilogueWarps);
     mbar_init(&s.end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -198,17 +202,22 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
   for (int e = e0; e < e1; ++e) s.tile[e] += before;
   if (tid == 0) s.tile[p.E] = total;
   // parts of a tile's sum, for more CTAs than tiles
-  const int split = max(1, min((int)gridDim.x / max(total, 1), 16));
+  const int split = max(1, min(pairs / max(total, 1), 16));
   const int items = total * split;
-  if ((int)blockIdx.x >= items) return;
-  if (warp == kMmaWarp) tmem_alloc(&s.tmem, 512);
+  if (pair >= items) return;
+  if (warp == kMmaWarp) {
+    if constexpr (CG == 2) tmem_alloc_pair(&s.tmem, 512);
+    else tmem_alloc(&s.tmem, 512);
+  }
   fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers are there
+  else __syncthreads();
   fence_after();
   const uint32_t tmem = s.tmem;
 
   // a stage: features' codes, columns' codes, features' scales, columns' scales
-  const int c_boxes = (most + kBoxC - 1) / kBoxC;
+  // (a pair's CTA holds half of the columns' codes and all of their scales)
+  const int c_boxes = (((most + 15) & ~15) / CG + kBoxC - 1) / kBoxC;
   const int c_blocks = (most + 127) / 128;
   const int sf_at = kFBytes + c_boxes * kBoxC * kStageRow;
   const int stage_bytes = (sf_at + (1 + c_blocks) * T::kSfBlock + 1023) & ~1023;
@@ -225,7 +234,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     }
     w.g = lo;
     const int r = w.tile - s.tile[lo], ct = r / f_tiles;
-    w.f0 = (r - ct * f_tiles) * kTileF;
+    w.f0 = ((r - ct * f_tiles) * CG + rank) * kTileF;
     const int row = p.start ? __ldg(p.start + lo) : 0;
     const int rows = p.start ? __ldg(p.start + lo + 1) - row : (int)rows_all;
     const int cols = T::kWgrad ? p.C : rows;
@@ -252,12 +261,18 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     return __all_sync(kAll, wait(b, parity));
   };
 
+  // an arrival at the barrier of the pair's first CTA, which issues the products
+  auto arrive_first = [&](uint64_t* b) {
+    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(b, 0));
+    else mbar_arrive(b);
+  };
+
   if (warp < kEpilogueWarps) {
     // ==== results ==============================================================
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t acc_lane = tmem + ((uint32_t)quarter << 21);
     int done = 0, tiles = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    for (int item = pair; item < items; item += pairs) {
       Work w;
       if (!work_of(item, w)) continue;
       float* sc = s.scale[tiles++ & 1];
@@ -283,7 +298,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
       }
       const uint32_t acc = acc_lane + (buf ? kAcc1 : 0);
       const int f = w.f0 + quarter * 32 + lane;
-      float* part = p.part + (int64_t)item * kMatmulPart + quarter * 32 + lane;
+      float* part = p.part + ((int64_t)item * CG + rank) * kMatmulPart + quarter * 32 + lane;
       // the result of column c and the next ones, for the lane's feature
       auto put = [&](int c, float (&v)[32]) {
         if constexpr (T::kFp4) {
@@ -321,7 +336,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
         if (i == 3 && sum) {
           fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.acc_free);
+          if (lane == 0) arrive_first(&s.acc_free);
         }
         const int chunk = buf ? i : 7 - i;
         if ((chunk & 1) != half || chunk * 32 >= w.cols) continue;
@@ -349,11 +364,12 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
         // the CTA that takes the tile's last ticket adds the parts in order
         __threadfence();
         asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
-        if (tid == 0) s.last = atomicAdd(&p.tickets[w.tile], 1u) == (uint32_t)w.parts - 1;
+        if (tid == 0) s.last = atomicAdd(&p.tickets[w.tile * CG + rank], 1u) == (uint32_t)w.parts - 1;
         asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
         if (s.last) {
           __threadfence();
-          const float* all = p.part + (int64_t)w.tile * split * kMatmulPart + quarter * 32 + lane;
+          const float* all =
+              p.part + ((int64_t)w.tile * split * CG + rank) * kMatmulPart + quarter * 32 + lane;
 #pragma unroll 1
           for (int chunk = half; chunk * 32 < w.cols; chunk += 2) {
             float v[32];
@@ -364,11 +380,12 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (chunk * 32 + j < w.cols)
-                  v[j] = __fadd_rn(v[j], __ldcg(all + (int64_t)q * kMatmulPart + (chunk * 32 + j) * 128));
+                  v[j] = __fadd_rn(v[j], __ldcg(all + (int64_t)q * CG * kMatmulPart +
+                                                  (chunk * 32 + j) * 128));
             }
             put(chunk * 32, v);
           }
-          if (tid == 0) p.tickets[w.tile] = 0;
+          if (tid == 0) p.tickets[w.tile * CG + rank] = 0;
         }
       }
     }
@@ -376,23 +393,37 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     // ==== codes: one lane to a box ==============================================
     uint32_t n = 0;
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+    for (int item = pair; ok && item < items; item += pairs) {
       Work w;
       if (!work_of(item, w)) continue;
-      const int boxes = (w.cols + kBoxC - 1) / kBoxC;
-      const int x0 = (int)(T::kFp4 ? 0 : w.k_at);
+      const int held = ((w.cols + 15) & ~15) / CG;  // columns of this CTA
+      const int boxes = (held + kBoxC - 1) / kBoxC;
+      const int x0 = (int)(T::kFp4 ? 0 : w.k_at), c_row = (int)w.c_row + rank * held;
       for (int k = w.k0; k < w.k1; ++k, ++n) {
         const uint32_t st = n % stages;
         if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
         const uint32_t dst = smem_addr(ring + st * stage_bytes);
-        if (lane == 0) {
-          mbar_expect(&s.full[st], kFBytes + boxes * kBoxC * kStageRow);
-          tma_load(dst, &f_map, x0 + k * kStageRow, (int)w.f_row, &s.full[st]);
+        const int x = x0 + k * kStageRow;
+        if constexpr (CG == 2) {
+          const uint32_t bar = cluster_addr(&s.full[st], 0);
+          if (lane == 0) {
+            if (rank == 0) mbar_expect(&s.full[st], 2 * (kFBytes + boxes * kBoxC * kStageRow));
+            tma_load_pair(dst, &f_map, x, (int)w.f_row, bar);
+          }
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_pair(dst + kFBytes + lane * kBoxC * kStageRow, &c_map, x,
+                          c_row + lane * kBoxC, bar);
+        } else {
+          if (lane == 0) {
+            mbar_expect(&s.full[st], kFBytes + boxes * kBoxC * kStageRow);
+            tma_load(dst, &f_map, x, (int)w.f_row, &s.full[st]);
+          }
+          __syncwarp();
+          if (lane < boxes)
+            tma_load(dst + kFBytes + lane * kBoxC * kStageRow, &c_map, x, c_row + lane * kBoxC,
+                     &s.full[st]);
         }
-        __syncwarp();
-        if (lane < boxes)
-          tma_load(dst + kFBytes + lane * kBoxC * kStageRow, &c_map, x0 + k * kStageRow,
-                   (int)w.c_row + lane * kBoxC, &s.full[st]);
       }
     }
     if (!ok) {
@@ -405,7 +436,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     // ==== products ==============================================================
     uint32_t n = 0, tiles = 0;
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+    for (int item = pair; rank == 0 && ok && item < items; item += pairs) {
       Work w;
       if (!work_of(item, w)) continue;
       if (w.k1 <= w.k0) continue;
@@ -424,10 +455,10 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
           constexpr int kPer = T::kFp4 ? 4 : 1;  // scale columns groups per stage
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
-            copy_scales(sf + 4 * j, scale_desc(sf16 + j * 32));
-            copy_scales(sf + 16 + 8 * j, scale_desc(sf16 + T::kSfBlock / 16 + j * 32));
+            copy_scales<CG>(sf + 4 * j, scale_desc(sf16 + j * 32));
+            copy_scales<CG>(sf + 16 + 8 * j, scale_desc(sf16 + T::kSfBlock / 16 + j * 32));
             if (blocks > 1)
-              copy_scales(sf + 16 + 8 * j + 4, scale_desc(sf16 + 2 * T::kSfBlock / 16 + j * 32));
+              copy_scales<CG>(sf + 16 + 8 * j + 4, scale_desc(sf16 + 2 * T::kSfBlock / 16 + j * 32));
           }
           const uint64_t df = smem_desc(at >> 4, 16), dc = smem_desc((at + kFBytes) >> 4, 16);
 #pragma unroll
@@ -435,76 +466,100 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
             if (k * 4 + j >= w.steps) break;
             const bool add = k > w.k0 || j > 0;
             if constexpr (T::kFp4)
-              mma_nvfp4(acc, df + 2 * j, dc + 2 * j, nvfp4_mma_desc(n16), sf + 4 * j,
+              mma_nvfp4<CG>(acc, df + 2 * j, dc + 2 * j, nvfp4_mma_desc(CG, n16), sf + 4 * j,
                         sf + 16 + 8 * j, add);
             else
-              mma_mxfp8(acc, df + 2 * j, dc + 2 * j, mxfp8_mma_desc(n16, j), sf, sf + 16, add);
+              mma_mxfp8<CG>(acc, df + 2 * j, dc + 2 * j, mxfp8_mma_desc(CG, n16, j), sf, sf + 16, add);
           }
-          mma_commit(&s.empty[st]);
-          if (k + 1 == w.k1) mma_commit(&s.acc_full);
+          if constexpr (CG == 2) {
+            mma_commit_pair(&s.empty[st]);
+            if (k + 1 == w.k1) mma_commit_pair(&s.acc_full);
+          } else {
+            mma_commit(&s.empty[st]);
+            if (k + 1 == w.k1) mma_commit(&s.acc_full);
+          }
         }
         __syncwarp();
       }
       ++tiles;
     }
-    // nothing is in flight when the tensor memory is freed
+    // nothing is in flight when the tensor memory is freed and the CTAs end
     if (elect_one()) {
-      mma_commit(&s.end);
+      if constexpr (CG == 2) {
+        if (rank == 0) mma_commit_pair(&s.end);
+      } else {
+        mma_commit(&s.end);
+      }
       const long long t0 = clock64();
       while (!mbar_try(&s.end, 0) && clock64() - t0 < kWaitCycles) {
       }
     }
     __syncwarp();
   } else {
-    // ==== scales: a warp to 128 rows, lane l to rows l, l + 32, l + 64, l + 96 ====
-    const int block = warp - kScaleWarp;  // 0 features, 1 and 2 columns
+    // ==== scales: two warps to 128 rows ==========================================
+    // A line of the layout that tensor memory takes holds rows l, l + 32, l + 64 and
+    // l + 96; a warp has 16 of the 32 lines. A lane fetches 16 bytes of its line's four
+    // rows, kQ lanes side by side pieces that follow one another, several fetches ahead.
+    const int block = (warp - kScaleWarp) >> 1;  // 0 features, 1 and 2 columns
+    const int line0 = ((warp - kScaleWarp) & 1) * 16;
     const uint8_t* base = block == 0 ? p.f_sf : p.c_sf;
     const int64_t rows = block == 0 ? p.f_rows : p.c_rows;
-    // 16 bytes of every row at a time, several fetches ahead of their use. Where they are
-    // aligned they stay as they came; else two aligned pieces are kept and cut at their use.
-    auto feed = [&](auto aligned_c, auto ahead_c) {
+    // Where the 16 bytes are aligned they stay as they came; else two aligned pieces are
+    // kept and cut at their use.
+    auto feed = [&](auto aligned_c, auto ahead_c, auto q_c) {
       constexpr bool kAligned = decltype(aligned_c)::value;
-      constexpr int kAhead = decltype(ahead_c)::value;
+      constexpr int kAhead = decltype(ahead_c)::value, kQ = decltype(q_c)::value;
+      constexpr int kB = kQ / 2, kLines = 32 / kQ;       // line groups of a warp, their lines
+      constexpr int kStages = kQ * T::kFetch;            // stages of a fetch
+      constexpr int kWords = T::kStageSf / 4;            // scale words of a row in a stage
+      const int piece = lane % kQ, line = line0 + lane / kQ;
       const uint8_t* end = base + rows * p.sf_stride;
-      int item = blockIdx.x, k = 0;  // the fetch that comes next
+      int item = pair, k = 0;  // the fetch that comes next
       Work w{};
       bool have = false;
-      uint4 lo[kAhead][4], hi[kAligned ? 1 : kAhead][4];
-      uint32_t off[kAligned ? 1 : kAhead][4];
-      int count[kAhead], valid[kAhead];  // stages, and bytes of a row, of a fetch; 0: the end
+      uint4 lo[kAhead][kB][4], hi[kAligned ? 1 : kAhead][kB][4];
+      uint32_t off[kAhead];            // low bits of the lane's first address
+      int count[kAhead], valid[kAhead];  // stages of a fetch (0: the end), bytes of the lane's piece
+      const uint32_t row_step = (uint32_t)(32 * p.sf_stride), line_step = (uint32_t)(kLines * p.sf_stride);
       auto fetch = [&](auto slot_c) {
         constexpr int kSlot = decltype(slot_c)::value;
         count[kSlot] = 0;
         while (!have || k >= w.k1) {
-          if (have) item += gridDim.x;
+          if (have) item += pairs;
           have = false;
           if (item >= items) return;
           if (!work_of(item, w)) {
-            item += gridDim.x;
+            item += pairs;
             continue;
           }
           have = true;
           k = w.k0;
         }
-        const int64_t row0 = block == 0 ? w.f_row : w.c_row + 128 * (block - 1);
-        const int64_t at = w.k_at / 32 + (int64_t)k * T::kStageSf;
-        const bool any = block == 0 || 128 * (block - 1) < w.cols;
-        count[kSlot] = min(T::kFetch, w.k1 - k);
-        valid[kSlot] = (int)min(p.sf_stride - at, (int64_t)16);
-        k += T::kFetch;
+        const int64_t row0 = (block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + line;
+        const int64_t at = w.k_at / 32 + (int64_t)k * T::kStageSf + 16 * piece;
+        const bool any = (block == 0 || 128 * (block - 1) < w.cols) &&
+                         piece * T::kFetch < w.k1 - k;
+        count[kSlot] = min(kStages, w.k1 - k);
+        valid[kSlot] = (int)max((int64_t)0, min(p.sf_stride - at, (int64_t)16));
+        k += kStages;
+        const uint8_t* first = base + row0 * p.sf_stride + at;
+        off[kSlot] = (uint32_t)(uintptr_t)first;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t row = row0 + 32 * i + lane;
-          const uint8_t* q = base + row * p.sf_stride + at;
-          const bool in = any && row < rows;
-          if constexpr (kAligned) {
-            lo[kSlot][i] = in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
-          } else {
-            off[kSlot][i] = (uint32_t)((uintptr_t)q & 15);
-            q -= off[kSlot][i];
-            lo[kSlot][i] = in ? bytes16(q, end) : make_uint4(0, 0, 0, 0);
-            hi[kSlot][i] = in && off[kSlot][i] + valid[kSlot] > 16 ? bytes16(q + 16, end)
-                                                                   : make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < kB; ++b) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = any && row0 + 32 * i + kLines * b < rows;
+            const uint8_t* q = first + i * 32 * p.sf_stride + b * kLines * p.sf_stride;
+            if constexpr (kAligned) {
+              lo[kSlot][b][i] =
+                  in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
+            } else {
+              const uint32_t o = (uint32_t)(uintptr_t)q & 15;
+              q -= o;
+              lo[kSlot][b][i] = in ? bytes16(q, end) : make_uint4(0, 0, 0, 0);
+              hi[kSlot][b][i] =
+                  in && o + valid[kSlot] > 16 ? bytes16(q + 16, end) : make_uint4(0, 0, 0, 0);
+            }
           }
         }
       };
@@ -513,47 +568,61 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
       auto store = [&](auto slot_c) -> bool {
         constexpr int kSlot = decltype(slot_c)::value;
         if (count[kSlot] == 0) return false;
-        uint32_t x[4][4];
+        uint32_t x[kB][4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 v = lo[kSlot][i];
-          if constexpr (!kAligned)
-            v = first_bytes(window16(v, hi[kSlot][i], off[kSlot][i]), valid[kSlot]);
-          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+        for (int b = 0; b < kB; ++b) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 v = lo[kSlot][b][i];
+            if constexpr (!kAligned)
+              v = first_bytes(window16(v, hi[kSlot][b][i],
+                                       (off[kSlot] + i * row_step + b * line_step) & 15),
+                              valid[kSlot]);
+            x[b][i][0] = v.x, x[b][i][1] = v.y, x[b][i][2] = v.z, x[b][i][3] = v.w;
+          }
         }
-        constexpr int kWords = T::kStageSf / 4;
 #pragma unroll
-        for (int c = 0; c < T::kFetch; ++c) {
+        for (int c = 0; c < kStages; ++c) {
           if (c >= count[kSlot]) break;
           const uint32_t st = n % stages;
           if (!wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1)) return false;
-          if (block <= c_blocks) {
+          if (block <= c_blocks && piece == c / T::kFetch) {
             uint4* dst = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
-                                                  block * T::kSfBlock) + lane;
+                                                  block * T::kSfBlock) + line;
+            const int word = c % T::kFetch * kWords;
 #pragma unroll
-            for (int j = 0; j < kWords; ++j)
-              dst[32 * j] = make_uint4(x[0][c * kWords + j], x[1][c * kWords + j],
-                                       x[2][c * kWords + j], x[3][c * kWords + j]);
+            for (int b = 0; b < kB; ++b) {
+#pragma unroll
+              for (int j = 0; j < kWords; ++j)
+                dst[32 * j + kLines * b] = make_uint4(x[b][0][word + j], x[b][1][word + j],
+                                                      x[b][2][word + j], x[b][3][word + j]);
+            }
             fence_smem_async();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s.full[st]);
+          if (lane == 0) arrive_first(&s.full[st]);
           ++n;
         }
         return true;
       };
       ring_of<kAhead>(fetch, store);
     };
+    constexpr std::integral_constant<int, 2> two{};
     if (sf_aligned)
-      feed(std::true_type{}, std::integral_constant<int, T::kFp4 ? 5 : 3>{});
+      feed(std::true_type{}, std::integral_constant<int, T::kFp4 ? 2 : 3>{},
+           std::integral_constant<int, T::kFp4 ? 4 : 2>{});
     else
-      feed(std::false_type{}, std::integral_constant<int, T::kFp4 ? 3 : 2>{});
+      feed(std::false_type{}, two, two);
   }
   __syncwarp();
   fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // nothing of the other CTA's reads or signals here
+  else __syncthreads();
   fence_after();
-  if (warp == kMmaWarp) tmem_free(tmem, 512);
+  if (warp == kMmaWarp) {
+    if constexpr (CG == 2) tmem_free_pair(tmem, 512);
+    else tmem_free(tmem, 512);
+  }
 }
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
@@ -583,14 +652,33 @@ bool make_map(CUtensorMap* m, const uint8_t* at, int64_t bytes, int64_t rows, in
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND>
+template <int KIND, int CG>
 cudaError_t launch_t(const MatmulParams& p, const CUtensorMap& f, const CUtensorMap& c,
                      cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(matmul_kernel<KIND>, kSmem, ready);
+  const cudaError_t e = allow_smem(matmul_kernel<KIND, CG>, kSmem, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl_smem(matmul_kernel<KIND>, dim3(std::min(sm_count(), kMatmulMaxCtas)),
-                         dim3(kThreads), kSmem, st, f, c, p);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(std::min(sm_count(), kMatmulMaxCtas) & ~(CG - 1)));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = kSmem;
+  lc.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CG;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = CG;
+  return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, f, c, p);
+}
+template <int KIND>
+cudaError_t launch_k(const MatmulParams& p, const CUtensorMap& f, const CUtensorMap& c,
+                     cudaStream_t st) {
+  const int64_t cols = KIND == kMatmulMxWgrad ? p.C : p.c_rows / p.E;
+  return p.N > kTileF && cols >= kPairCols ? launch_t<KIND, 2>(p, f, c, st)
+                                           : launch_t<KIND, 1>(p, f, c, st);
 }
 
 }  // namespace
@@ -604,9 +692,9 @@ cudaError_t launch_matmul(int kind, const MatmulParams& p, const uint8_t* f_code
                     !make_map(&c, c_codes, bytes, p.c_rows, kBoxC)))
     return cudaErrorInvalidValue;
   switch (kind) {
-    case kMatmulNvfp4: return launch_t<kMatmulNvfp4>(p, f, c, st);
-    case kMatmulMx: return launch_t<kMatmulMx>(p, f, c, st);
-    default: return launch_t<kMatmulMxWgrad>(p, f, c, st);
+    case kMatmulNvfp4: return launch_k<kMatmulNvfp4>(p, f, c, st);
+    case kMatmulMx: return launch_k<kMatmulMx>(p, f, c, st);
+    default: return launch_k<kMatmulMxWgrad>(p, f, c, st);
   }
 }
 

@@ -153,35 +153,87 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr16) {
   return (uint64_t)addr16 | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
 }
 // Those 512 bytes into four columns of tensor memory (the same in each quarter
-// of its lanes). Products issued after it by the same thread read them.
+// of its lanes). Products issued after it by the same thread read them. With
+// CG = 2 here and below, one thread acts for a pair of CTAs: each copies from
+// its own shared memory to its own tensor memory.
+template <int CG>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-               : "memory");
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
 }
 // E2M1 x E2M1, a UE4M3 scale per 16 (K = 64), and E4M3 x E4M3, a UE8M0 scale per
-// 32 (K = 32); M = 128, fp32 accumulators. byte: which of a column's four scale
-// bytes the MXFP8 product takes.
-__host__ __device__ constexpr uint32_t nvfp4_mma_desc(int n) {
-  return 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+// 32 (K = 32); M = 128 m, fp32 accumulators. byte: which of a column's four scale
+// bytes the MXFP8 product takes. A pair of CTAs holds 128 rows of A and half of
+// B's columns each, B's scales both, and gets its rows' results.
+__host__ __device__ constexpr uint32_t nvfp4_mma_desc(int m, int n) {
+  return 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m * 128 >> 4) << 24;
 }
-__host__ __device__ constexpr uint32_t mxfp8_mma_desc(int n, int byte) {
-  return (uint32_t)byte << 4 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(128 >> 4) << 24 |
-         (uint32_t)byte << 29;
+__host__ __device__ constexpr uint32_t mxfp8_mma_desc(int m, int n, int byte) {
+  return (uint32_t)byte << 4 | (uint32_t)(n >> 3) << 17 | 1u << 23 |
+         (uint32_t)(m * 128 >> 4) << 24 | (uint32_t)byte << 29;
 }
+#define NVFP4_SCALED_MMA(CG, KIND)                                            \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"              \
+               "tcgen05.mma.cta_group::" CG ".kind::" KIND                   \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a),    \
+               "l"(b), "r"(desc), "r"(sa), "r"(sb), "r"((uint32_t)add)       \
+               : "memory")
+template <int CG>
 __device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                           uint32_t sa, uint32_t sb, bool add) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
-               "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a),
-               "l"(b), "r"(desc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-               : "memory");
+  if constexpr (CG == 2) NVFP4_SCALED_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  else NVFP4_SCALED_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
 }
+template <int CG>
 __device__ __forceinline__ void mma_mxfp8(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                           uint32_t sa, uint32_t sb, bool add) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
-               "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a),
-               "l"(b), "r"(desc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+  if constexpr (CG == 2) NVFP4_SCALED_MMA("2", "mxf8f6f4.block_scale.scale_vec::1X");
+  else NVFP4_SCALED_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
+}
+#undef NVFP4_SCALED_MMA
+
+// ---------------------------------------------------------- pairs of CTAs ---
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a shared object of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+// An arrival at a barrier of another CTA of the cluster. What the caller wrote to
+// its own shared memory is ordered before it by fence_smem_async, for the copies
+// and products that its own SM then makes on the other CTA's behalf; a release of
+// cluster scope would wait for everything that the thread has in flight (a stage
+// of 128-value rows then took 2000 clocks where it takes 750).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mma_commit to the barrier at that place in both CTAs of the pair.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+               ".multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(b)), "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
                : "memory");
 }
 
@@ -198,6 +250,14 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const void* map, int x, i
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
                "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y),
                "r"(smem_addr(b))
+               : "memory");
+}
+// The same whose bytes are counted by a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int x, int y,
+                                              uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+               ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map),
+               "r"(x), "r"(y), "r"(bar)
                : "memory");
 }
 
