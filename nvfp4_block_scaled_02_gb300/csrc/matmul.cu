@@ -15,12 +15,13 @@ constexpr int kThreads = (kEpilogueWarps + 2 + kScaleWarps) * 32;
 constexpr int kTileF = 128, kTileC = 256;
 constexpr int kStageRow = 128;                 // code bytes of a row in a stage: one swizzle line
 constexpr int kFBytes = kTileF * kStageRow;
-constexpr int kBoxC = 32;                      // columns of one copy
+constexpr int kBox = 128, kBoxSmall = 32;      // rows of one copy
 constexpr int kMaxStages = 12;
 constexpr int kRing = 216 * 1024;              // bytes of the ring of stages
 constexpr int kSmem = kRing + 1024;            // and its alignment
 // Tensor memory: two accumulators of 256 columns that share 96, scales twice.
 constexpr int kAcc1 = 160, kScales = 416, kScalesEach = 48;
+constexpr int kBand = 8;                       // column tiles of a band
 constexpr int kPairCols = 96;                  // columns of a group from which pairs of CTAs pay
 constexpr long long kWaitCycles = 2000000000;  // about a second
 
@@ -76,6 +77,21 @@ __device__ __forceinline__ uint4 first_bytes(uint4 x, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Copies of n columns: large boxes as far as they fill, then one more or, for up to half
+// of it, small ones.
+struct Boxes {
+  int large, count;
+  __device__ __forceinline__ explicit Boxes(int n) {
+    const int rest = n % kBox;
+    large = n / kBox + (rest > kBox / 2);
+    count = large + (rest > kBox / 2 ? 0 : (rest + kBoxSmall - 1) / kBoxSmall);
+  }
+  __device__ __forceinline__ int row(int i) const {  // of box i
+    return i < large ? i * kBox : large * kBox + (i - large) * kBoxSmall;
+  }
+  __device__ __forceinline__ int rows() const { return row(count); }
+};
+
 template <int KIND>
 struct Kind {
   static constexpr bool kFp4 = KIND == kMatmulNvfp4;
@@ -122,8 +138,14 @@ __device__ __forceinline__ void ring_of(Fetch& fetch, Store& store) {
   }
 }
 
+struct Maps {
+  CUtensorMap f, c, c_small;     // codes of the features' and the columns' rows
+  CUtensorMap fs, cs, cs_small;  // their scales
+};
+
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t raw[3][kMaxStages];     // scales of 128 rows as they lie in memory
   uint64_t acc_full, acc_free, end;
   uint32_t tmem;
   volatile int dead;
@@ -135,8 +157,7 @@ struct Shared {
 
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
-matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__ CUtensorMap c_map,
-              const MatmulParams p) {
+matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   using T = Kind<KIND>;
   pdl_begin();
   extern __shared__ uint8_t smem_raw[];
@@ -181,11 +202,15 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
   most = __reduce_max_sync(kAll, most);
   if (lane == 31) s.scan[warp] = incl;
   if (lane == 0) s.most[warp] = most;
+  // NVFP4 rows whose scales are aligned: a stage's 16 bytes of a row are copied to their stage
+  // and turned there into the layout of tensor memory
+  const bool in_place = T::kFp4 && p.sf_stride % 16 == 0;
   if (tid == 0) {
     s.dead = 0;
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&s.full[i], 1 + CG * kScaleWarps);
+      mbar_init(&s.full[i], 1 + CG * (in_place ? kScaleWarps / 2 : kScaleWarps));
       mbar_init(&s.empty[i], 1);
+      for (int b = 0; b < 3; ++b) mbar_init(&s.raw[b][i], 1);
     }
     mbar_init(&s.acc_full, 1);
     mbar_init(&s.acc_free, CG * kEpilogueWarps);
@@ -217,9 +242,8 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
 
   // a stage: features' codes, columns' codes, features' scales, columns' scales
   // (a pair's CTA holds half of the columns' codes and all of their scales)
-  const int c_boxes = (((most + 15) & ~15) / CG + kBoxC - 1) / kBoxC;
   const int c_blocks = (most + 127) / 128;
-  const int sf_at = kFBytes + c_boxes * kBoxC * kStageRow;
+  const int sf_at = kFBytes + Boxes(((most + 15) & ~15) / CG).rows() * kStageRow;
   const int stage_bytes = (sf_at + (1 + c_blocks) * T::kSfBlock + 1023) & ~1023;
   const int stages = min(kRing / stage_bytes, kMaxStages);
 
@@ -233,12 +257,15 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
       else hi = mid;
     }
     w.g = lo;
-    const int r = w.tile - s.tile[lo], ct = r / f_tiles;
-    w.f0 = ((r - ct * f_tiles) * CG + rank) * kTileF;
     const int row = p.start ? __ldg(p.start + lo) : 0;
     const int rows = p.start ? __ldg(p.start + lo + 1) - row : (int)rows_all;
     const int cols = T::kWgrad ? p.C : rows;
     const int c_tiles = (cols + kTileC - 1) / kTileC, size = (cols + c_tiles - 1) / c_tiles;
+    // bands of column tiles, a band's columns first
+    const int r = w.tile - s.tile[lo], band = r / (kBand * f_tiles);
+    const int wide = min(kBand, c_tiles - band * kBand), in = r - band * kBand * f_tiles;
+    const int ft = in / wide, ct = band * kBand + in - ft * wide;
+    w.f0 = (ft * CG + rank) * kTileF;
     w.c0 = ct * size;
     w.cols = min(size, cols - w.c0);
     const int64_t sum = T::kWgrad ? rows : p.K;
@@ -261,6 +288,12 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
     return __all_sync(kAll, wait(b, parity));
   };
 
+  // Given up: copies in flight land before the CTA ends (milliseconds are many times enough).
+  auto land = [&]() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 20000000) {
+    }
+  };
   // an arrival at the barrier of the pair's first CTA, which issues the products
   auto arrive_first = [&](uint64_t* b) {
     if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(b, 0));
@@ -397,41 +430,36 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
       Work w;
       if (!work_of(item, w)) continue;
       const int held = ((w.cols + 15) & ~15) / CG;  // columns of this CTA
-      const int boxes = (held + kBoxC - 1) / kBoxC;
-      const int x0 = (int)(T::kFp4 ? 0 : w.k_at), c_row = (int)w.c_row + rank * held;
+      const Boxes boxes(held);
+      const uint32_t bytes = kFBytes + boxes.rows() * kStageRow;
+      const int x0 = (int)(T::kFp4 ? 0 : w.k_at);
+      const int c_row = (int)w.c_row + rank * held + boxes.row(lane);
+      const CUtensorMap* c_box = lane < boxes.large ? &maps.c : &maps.c_small;
       for (int k = w.k0; k < w.k1; ++k, ++n) {
         const uint32_t st = n % stages;
         if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
         const uint32_t dst = smem_addr(ring + st * stage_bytes);
+        const uint32_t c_dst = dst + kFBytes + boxes.row(lane) * kStageRow;
         const int x = x0 + k * kStageRow;
         if constexpr (CG == 2) {
           const uint32_t bar = cluster_addr(&s.full[st], 0);
           if (lane == 0) {
-            if (rank == 0) mbar_expect(&s.full[st], 2 * (kFBytes + boxes * kBoxC * kStageRow));
-            tma_load_pair(dst, &f_map, x, (int)w.f_row, bar);
+            if (rank == 0) mbar_expect(&s.full[st], 2 * bytes);
+            tma_load_pair(dst, &maps.f, x, (int)w.f_row, bar);
           }
           __syncwarp();
-          if (lane < boxes)
-            tma_load_pair(dst + kFBytes + lane * kBoxC * kStageRow, &c_map, x,
-                          c_row + lane * kBoxC, bar);
+          if (lane < boxes.count) tma_load_pair(c_dst, c_box, x, c_row, bar);
         } else {
           if (lane == 0) {
-            mbar_expect(&s.full[st], kFBytes + boxes * kBoxC * kStageRow);
-            tma_load(dst, &f_map, x, (int)w.f_row, &s.full[st]);
+            mbar_expect(&s.full[st], bytes);
+            tma_load(dst, &maps.f, x, (int)w.f_row, &s.full[st]);
           }
           __syncwarp();
-          if (lane < boxes)
-            tma_load(dst + kFBytes + lane * kBoxC * kStageRow, &c_map, x, c_row + lane * kBoxC,
-                     &s.full[st]);
+          if (lane < boxes.count) tma_load(c_dst, c_box, x, c_row, &s.full[st]);
         }
       }
     }
-    if (!ok) {
-      // given up: copies in flight land before the CTA ends (milliseconds are many times enough)
-      const long long t0 = clock64();
-      while (clock64() - t0 < 20000000) {
-      }
-    }
+    if (!ok) land();
   } else if (warp == kMmaWarp) {
     // ==== products ==============================================================
     uint32_t n = 0, tiles = 0;
@@ -495,6 +523,60 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
       }
     }
     __syncwarp();
+  } else if (in_place && warp == kScaleWarp) {
+    // ==== scales: copies, a lane to 128 rows ======================================
+    uint32_t n = 0;
+    bool ok = true;
+    for (int item = pair; ok && item < items; item += pairs) {
+      Work w;
+      if (!work_of(item, w)) continue;
+      const Boxes boxes(w.cols);
+      const int row = boxes.row(lane - 1), in = lane == 0 ? 0 : 1 + row / 128;  // its 128 rows
+      const CUtensorMap* map =
+          lane == 0 ? &maps.fs : lane <= boxes.large ? &maps.cs : &maps.cs_small;
+      const int y = lane == 0 ? (int)w.f_row : (int)w.c_row + row;
+      const uint32_t at = sf_at + (lane == 0 ? 0 : T::kSfBlock + row * T::kStageSf);
+      const int held = lane == 0 ? 128 : max(0, min(boxes.rows() - (lane - 1) * 128, 128));
+      for (int k = w.k0; k < w.k1; ++k, ++n) {
+        const uint32_t st = n % stages;
+        if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
+        if (lane <= c_blocks) mbar_expect(&s.raw[lane][st], held * T::kStageSf);
+        __syncwarp();
+        if (lane <= boxes.count)
+          tma_load(smem_addr(ring + st * stage_bytes + at), map, k * T::kStageSf, y,
+                   &s.raw[in][st]);
+      }
+    }
+    if (!ok) land();
+  } else if (in_place && warp < kScaleWarp + 3) {
+    // (two warps without work)
+  } else if (in_place) {
+    // ==== scales: lane l turns rows l, l + 32, l + 64, l + 96 ======================
+    const int block = warp - kScaleWarp - 3;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int item = pair; ok && item < items; item += pairs) {
+      Work w;
+      if (!work_of(item, w)) continue;
+      for (int k = w.k0; k < w.k1; ++k, ++n) {
+        const uint32_t st = n % stages;
+        if (block <= c_blocks) {
+          if (!(ok = wait_warp(&s.raw[block][st], (n / stages) & 1))) break;
+          uint4* at = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
+                                               block * T::kSfBlock) + lane;
+          const uint4 a = at[0], b = at[32], c = at[64], d = at[96];
+          at[0] = make_uint4(a.x, b.x, c.x, d.x);
+          at[32] = make_uint4(a.y, b.y, c.y, d.y);
+          at[64] = make_uint4(a.z, b.z, c.z, d.z);
+          at[96] = make_uint4(a.w, b.w, c.w, d.w);
+          fence_smem_async();
+        } else if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) {
+          break;
+        }
+        __syncwarp();
+        if (lane == 0) arrive_first(&s.full[st]);
+      }
+    }
   } else {
     // ==== scales: two warps to 128 rows ==========================================
     // A line of the layout that tensor memory takes holds rows l, l + 32, l + 64 and
@@ -608,11 +690,15 @@ matmul_kernel(const __grid_constant__ CUtensorMap f_map, const __grid_constant__
       ring_of<kAhead>(fetch, store);
     };
     constexpr std::integral_constant<int, 2> two{};
-    if (sf_aligned)
-      feed(std::true_type{}, std::integral_constant<int, T::kFp4 ? 2 : 3>{},
-           std::integral_constant<int, T::kFp4 ? 4 : 2>{});
-    else
+    if constexpr (!T::kFp4) {
+      if (sf_aligned) {
+        feed(std::true_type{}, std::integral_constant<int, 3>{}, two);
+      } else {
+        feed(std::false_type{}, two, two);
+      }
+    } else {
       feed(std::false_type{}, two, two);
+    }
   }
   __syncwarp();
   fence_before();
@@ -641,20 +727,21 @@ EncodeTiled encode_tiled() {
   return f;
 }
 
-// rows x bytes, boxes of `box` rows of one swizzle line; false if it cannot be made
-bool make_map(CUtensorMap* m, const uint8_t* at, int64_t bytes, int64_t rows, int box) {
+// rows x bytes, boxes of box_rows x box_bytes; false if it cannot be made
+bool make_map(CUtensorMap* m, const uint8_t* at, int64_t bytes, int64_t rows, int box_bytes,
+              int box_rows) {
   const EncodeTiled f = encode_tiled();
   if (!f) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bytes};
-  const cuuint32_t sizes[2] = {kStageRow, (cuuint32_t)box}, steps[2] = {1, 1};
+  const cuuint32_t sizes[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows}, steps[2] = {1, 1};
   return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(at), dims, strides, sizes,
-           steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           box_bytes == kStageRow ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KIND, int CG>
-cudaError_t launch_t(const MatmulParams& p, const CUtensorMap& f, const CUtensorMap& c,
-                     cudaStream_t st) {
+cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(matmul_kernel<KIND, CG>, kSmem, ready);
   if (e != cudaSuccess) return e;
@@ -671,30 +758,35 @@ cudaError_t launch_t(const MatmulParams& p, const CUtensorMap& f, const CUtensor
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   lc.attrs = at;
   lc.numAttrs = CG;
-  return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, f, c, p);
+  return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, m, p);
 }
 template <int KIND>
-cudaError_t launch_k(const MatmulParams& p, const CUtensorMap& f, const CUtensorMap& c,
-                     cudaStream_t st) {
+cudaError_t launch_k(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   const int64_t cols = KIND == kMatmulMxWgrad ? p.C : p.c_rows / p.E;
-  return p.N > kTileF && cols >= kPairCols ? launch_t<KIND, 2>(p, f, c, st)
-                                           : launch_t<KIND, 1>(p, f, c, st);
+  return p.N > kTileF && cols >= kPairCols ? launch_t<KIND, 2>(p, m, st)
+                                           : launch_t<KIND, 1>(p, m, st);
 }
 
 }  // namespace
 
 cudaError_t launch_matmul(int kind, const MatmulParams& p, const uint8_t* f_codes,
                           const uint8_t* c_codes, cudaStream_t st) {
-  CUtensorMap f{}, c{};
+  Maps m{};
   const int64_t bytes = kind == kMatmulNvfp4 ? p.K / 2 : p.K;
   // without rows to sum over no copy is made: a weights' gradient of zeros
-  if (bytes > 0 && (!make_map(&f, f_codes, bytes, p.f_rows, kTileF) ||
-                    !make_map(&c, c_codes, bytes, p.c_rows, kBoxC)))
+  if (bytes > 0 && (!make_map(&m.f, f_codes, bytes, p.f_rows, kStageRow, kTileF) ||
+                    !make_map(&m.c, c_codes, bytes, p.c_rows, kStageRow, kBox) ||
+                    !make_map(&m.c_small, c_codes, bytes, p.c_rows, kStageRow, kBoxSmall)))
+    return cudaErrorInvalidValue;
+  if (kind == kMatmulNvfp4 && p.sf_stride % 16 == 0 &&
+      (!make_map(&m.fs, p.f_sf, p.sf_stride, p.f_rows, 16, kTileF) ||
+       !make_map(&m.cs, p.c_sf, p.sf_stride, p.c_rows, 16, kBox) ||
+       !make_map(&m.cs_small, p.c_sf, p.sf_stride, p.c_rows, 16, kBoxSmall)))
     return cudaErrorInvalidValue;
   switch (kind) {
-    case kMatmulNvfp4: return launch_k<kMatmulNvfp4>(p, f, c, st);
-    case kMatmulMx: return launch_k<kMatmulMx>(p, f, c, st);
-    default: return launch_k<kMatmulMxWgrad>(p, f, c, st);
+    case kMatmulNvfp4: return launch_k<kMatmulNvfp4>(p, m, st);
+    case kMatmulMx: return launch_k<kMatmulMx>(p, m, st);
+    default: return launch_k<kMatmulMxWgrad>(p, m, st);
   }
 }
 
