@@ -19,8 +19,8 @@ constexpr int kBox = 128, kBoxSmall = 32;      // rows of one copy
 constexpr int kMaxStages = 12;
 constexpr int kRing = 216 * 1024;              // bytes of the ring of stages
 constexpr int kSmem = kRing + 1024;            // and its alignment
-// Tensor memory: two accumulators of 256 columns that share 96, scales twice.
-constexpr int kAcc1 = 160, kScales = 416, kScalesEach = 48;
+// Tensor memory: two accumulators of 256 columns that share 64, then the scales of a stage.
+constexpr int kAcc1 = 192, kScales = 448;
 constexpr int kBand = 8;                       // column tiles of a band
 constexpr int kPairCols = 96;                  // columns of a group from which pairs of CTAs pay
 constexpr long long kWaitCycles = 2000000000;  // about a second
@@ -109,7 +109,7 @@ struct Work {
   int g, f0, c0, cols;      // group, first feature, first column, columns
   int64_t f_row, c_row;     // rows of the two matrices
   int64_t k_at;             // first value of the sum
-  int steps;                // products of the whole sum
+  int first, steps;         // the sum's first product and the end of its products
   int k0, k1;
   int tile, part, parts;
 };
@@ -137,6 +137,15 @@ __device__ __forceinline__ void ring_of(Fetch& fetch, Store& store) {
   while (turn_ring<N>(fetch, store)) {
   }
 }
+
+// A place in the ring of stages and the parity of its present turn.
+struct Place {
+  int st = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) st = 0, turn ^= 1;
+  }
+};
 
 struct Maps {
   CUtensorMap f, c, c_small;     // codes of the features' and the columns' rows
@@ -176,13 +185,12 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   const int e0 = min(tid * share, p.E), e1 = min(e0 + share, p.E);
   int mine = 0, most = 0;
   // whether the 16 scale bytes of a row that are fetched together are aligned
-  bool sf_aligned = p.sf_stride % 16 == 0;
+  const bool sf_aligned = p.sf_stride % 16 == 0;
   for (int e = e0; e < e1; ++e) {
     int64_t a = p.start ? p.start[e] : 0, b = p.start ? p.start[e + 1] : rows_all;
     bool bad = a < 0 || b < a || b > rows_all;
     if (T::kWgrad) {
       bad = bad || (a | b) % 32 != 0;
-      sf_aligned = sf_aligned && a % 512 == 0;
     }
     if (bad) {
       if (blockIdx.x == 0) flag(p.status, NVFP4_DEV_BAD_INDEX);
@@ -217,7 +225,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
     mbar_init(&s.end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  sf_aligned = __syncthreads_and(sf_aligned);
+  __syncthreads();
   int before = incl - mine, total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s.scan[w];
@@ -268,8 +276,12 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
     w.f0 = (ft * CG + rank) * kTileF;
     w.c0 = ct * size;
     w.cols = min(size, cols - w.c0);
-    const int64_t sum = T::kWgrad ? rows : p.K;
-    w.k_at = T::kWgrad ? row : 0;
+    // A weights' gradient sums over values `row` on, in stages that begin at multiples of 128
+    // (whole words of scales): the first stage's products in front of it are left out.
+    const int skip = T::kWgrad ? row % T::kStageK : 0;
+    const int64_t sum = T::kWgrad ? (rows > 0 ? rows + skip : 0) : p.K;
+    w.k_at = T::kWgrad ? row - skip : 0;
+    w.first = skip / T::kStepK;
     w.f_row = (T::kWgrad ? 0 : (int64_t)lo * p.N) + w.f0;
     w.c_row = (T::kWgrad ? 0 : row) + w.c0;
     w.steps = (int)((sum + T::kStepK - 1) / T::kStepK);
@@ -280,6 +292,13 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
     w.k0 = (int)((int64_t)units * w.part / w.parts) * T::kFetch;
     w.k1 = min(n, (int)((int64_t)units * (w.part + 1) / w.parts) * T::kFetch);
     return w.part < w.parts && w.cols > 0;
+  };
+  // The pair's next piece of work from `item` on; false at the end. Finding one takes some
+  // hundred clocks: where a warp feeds the ring it looks ahead while the ring is full.
+  auto seek = [&](int& item, Work& w) -> bool {
+    for (; item < items; item += pairs)
+      if (work_of(item, w)) return true;
+    return false;
   };
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
     return mbar_try(b, parity) || wait_long(b, parity, &s.dead, p.status);
@@ -339,48 +358,51 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], sc[c + i < w.cols ? c + i : 0]), gf);
         }
         const int64_t row0 = T::kWgrad ? (int64_t)w.g * p.C + w.c0 : w.c_row;
+        // every lane has a feature, every column is there: no checks
+        const bool whole = c + 32 <= w.cols && f - lane + 32 <= p.N;
         if (p.out_f32) {
           float* o = static_cast<float*>(p.out) + (row0 + c) * p.N + f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < w.cols && f < p.N) o[(int64_t)i * p.N] = v[i];
+          for (int i = 0; i < 32; ++i, o += p.N)
+            if (whole || (c + i < w.cols && f < p.N)) *o = v[i];
         } else if (p.N % 2 == 0) {
           // neighbouring lanes swap, so that each stores two features of one column
           const int odd = lane & 1;
           uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
                                                     (row0 + c + odd) * p.N + (f & ~1));
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < 32; i += 2, o += p.N) {
             const uint32_t a = pack_bf16x2(v[i], v[i + 1]), b = __shfl_xor_sync(kAll, a, 1);
             const uint32_t x = __byte_perm(a, b, odd ? 0x3276u : 0x5410u);
-            if (c + i + odd < w.cols && f < p.N) o[(int64_t)i * p.N / 2] = x;
+            if (whole || (c + i + odd < w.cols && f < p.N)) *o = x;
           }
         } else {
           uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + c) * p.N + f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < w.cols && f < p.N)
-              o[(int64_t)i * p.N] = (uint16_t)pack_bf16x2(v[i], 0.0f);
+          for (int i = 0; i < 32; ++i, o += p.N)
+            if (whole || (c + i < w.cols && f < p.N)) *o = (uint16_t)pack_bf16x2(v[i], 0.0f);
         }
       };
-      // the columns that the two accumulators share leave first
+      // A warpgroup has every other 32 columns. Those that the two accumulators share come
+      // first, and once they are in registers the next tile's products may begin.
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        if (i == 3 && sum) {
-          fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_first(&s.acc_free);
-        }
-        const int chunk = buf ? i : 7 - i;
-        if ((chunk & 1) != half || chunk * 32 >= w.cols) continue;
+      for (int i = 0; i < 4; ++i) {
+        const int chunk = 2 * (buf ? i : 3 - i) + half;
+        const bool some = chunk * 32 < w.cols;
         uint32_t r[32];
-        if (sum) {
+        if (sum && some) {
           tmem_ld32(acc + chunk * 32, r);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
+        if (i == 0 && sum) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first(&s.acc_free);
+        }
+        if (!some) continue;
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
@@ -424,20 +446,23 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
     }
   } else if (warp == kCopyWarp) {
     // ==== codes: one lane to a box ==============================================
-    uint32_t n = 0;
+    Place pl;
     bool ok = true;
-    for (int item = pair; ok && item < items; item += pairs) {
-      Work w;
-      if (!work_of(item, w)) continue;
+    int item = pair;
+    Work ahead;
+    bool more = seek(item, ahead);
+    while (ok && more) {
+      const Work w = ahead;
+      more = false;
       const int held = ((w.cols + 15) & ~15) / CG;  // columns of this CTA
       const Boxes boxes(held);
       const uint32_t bytes = kFBytes + boxes.rows() * kStageRow;
       const int x0 = (int)(T::kFp4 ? 0 : w.k_at);
       const int c_row = (int)w.c_row + rank * held + boxes.row(lane);
       const CUtensorMap* c_box = lane < boxes.large ? &maps.c : &maps.c_small;
-      for (int k = w.k0; k < w.k1; ++k, ++n) {
-        const uint32_t st = n % stages;
-        if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
+      for (int k = w.k0; k < w.k1; ++k, pl.next(stages)) {
+        const int st = pl.st;
+        if (!(ok = wait_warp(&s.empty[st], pl.turn ^ 1))) break;
         const uint32_t dst = smem_addr(ring + st * stage_bytes);
         const uint32_t c_dst = dst + kFBytes + boxes.row(lane) * kStageRow;
         const int x = x0 + k * kStageRow;
@@ -457,28 +482,37 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           __syncwarp();
           if (lane < boxes.count) tma_load(c_dst, c_box, x, c_row, &s.full[st]);
         }
+        if (k == w.k0) more = seek(item += pairs, ahead);
       }
+      if (w.k1 <= w.k0) more = seek(item += pairs, ahead);
     }
     if (!ok) land();
   } else if (warp == kMmaWarp) {
     // ==== products ==============================================================
-    uint32_t n = 0, tiles = 0;
+    uint32_t tiles = 0;
+    Place pl;
     bool ok = true;
-    for (int item = pair; rank == 0 && ok && item < items; item += pairs) {
-      Work w;
-      if (!work_of(item, w)) continue;
-      if (w.k1 <= w.k0) continue;
+    int item = pair;
+    Work ahead;
+    bool more = rank == 0 && seek(item, ahead);
+    while (ok && more) {
+      const Work w = ahead;
+      if (w.k1 <= w.k0) {
+        item += pairs;
+        more = seek(item, ahead);
+        continue;
+      }
       const int n16 = (w.cols + 15) & ~15, blocks = (w.cols + 127) >> 7;
       const uint32_t acc = tmem + (tiles & 1 ? kAcc1 : 0);
       if (tiles > 0 && !(ok = wait_warp(&s.acc_free, (tiles - 1) & 1))) break;
       fence_after();
-      for (int k = w.k0; k < w.k1; ++k, ++n) {
-        const uint32_t st = n % stages;
-        if (!(ok = wait_warp(&s.full[st], (n / stages) & 1))) break;
+      for (int k = w.k0; k < w.k1; ++k, pl.next(stages)) {
+        const int st = pl.st;
+        if (!(ok = wait_warp(&s.full[st], pl.turn))) break;
         fence_after();
         if (elect_one()) {
           const uint32_t at = smem_addr(ring + st * stage_bytes);
-          const uint32_t sf = tmem + kScales + (n & 1) * kScalesEach;
+          const uint32_t sf = tmem + kScales;
           const uint32_t sf16 = (at + sf_at) >> 4;
           constexpr int kPer = T::kFp4 ? 4 : 1;  // scale columns groups per stage
 #pragma unroll
@@ -492,7 +526,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (k * 4 + j >= w.steps) break;
-            const bool add = k > w.k0 || j > 0;
+            if (T::kWgrad && k * 4 + j < w.first) continue;
+            const bool add = k > w.k0 || j > (T::kWgrad && k == 0 ? w.first : 0);
             if constexpr (T::kFp4)
               mma_nvfp4<CG>(acc, df + 2 * j, dc + 2 * j, nvfp4_mma_desc(CG, n16), sf + 4 * j,
                         sf + 16 + 8 * j, add);
@@ -508,6 +543,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           }
         }
         __syncwarp();
+        if (k == w.k0) more = seek(item += pairs, ahead);
       }
       ++tiles;
     }
@@ -525,11 +561,14 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
     __syncwarp();
   } else if (in_place && warp == kScaleWarp) {
     // ==== scales: copies, a lane to 128 rows ======================================
-    uint32_t n = 0;
+    Place pl;
     bool ok = true;
-    for (int item = pair; ok && item < items; item += pairs) {
-      Work w;
-      if (!work_of(item, w)) continue;
+    int item = pair;
+    Work ahead;
+    bool more = seek(item, ahead);
+    while (ok && more) {
+      const Work w = ahead;
+      more = false;
       const Boxes boxes(w.cols);
       const int row = boxes.row(lane - 1), in = lane == 0 ? 0 : 1 + row / 128;  // its 128 rows
       const CUtensorMap* map =
@@ -537,14 +576,15 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
       const int y = lane == 0 ? (int)w.f_row : (int)w.c_row + row;
       const uint32_t at = sf_at + (lane == 0 ? 0 : T::kSfBlock + row * T::kStageSf);
       const int held = lane == 0 ? 128 : max(0, min(boxes.rows() - (lane - 1) * 128, 128));
-      for (int k = w.k0; k < w.k1; ++k, ++n) {
-        const uint32_t st = n % stages;
-        if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) break;
+      for (int k = w.k0; k < w.k1; ++k, pl.next(stages)) {
+        const int st = pl.st;
+        if (!(ok = wait_warp(&s.empty[st], pl.turn ^ 1))) break;
         if (lane <= c_blocks) mbar_expect(&s.raw[lane][st], held * T::kStageSf);
         __syncwarp();
         if (lane <= boxes.count)
           tma_load(smem_addr(ring + st * stage_bytes + at), map, k * T::kStageSf, y,
                    &s.raw[in][st]);
+        if (k == w.k0) more = seek(item += pairs, ahead);
       }
     }
     if (!ok) land();
@@ -553,15 +593,18 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   } else if (in_place) {
     // ==== scales: lane l turns rows l, l + 32, l + 64, l + 96 ======================
     const int block = warp - kScaleWarp - 3;
-    uint32_t n = 0;
+    Place pl;
     bool ok = true;
-    for (int item = pair; ok && item < items; item += pairs) {
-      Work w;
-      if (!work_of(item, w)) continue;
-      for (int k = w.k0; k < w.k1; ++k, ++n) {
-        const uint32_t st = n % stages;
+    int item = pair;
+    Work ahead;
+    bool more = seek(item, ahead);
+    while (ok && more) {
+      const Work w = ahead;
+      more = false;
+      for (int k = w.k0; k < w.k1; ++k, pl.next(stages)) {
+        const int st = pl.st;
         if (block <= c_blocks) {
-          if (!(ok = wait_warp(&s.raw[block][st], (n / stages) & 1))) break;
+          if (!(ok = wait_warp(&s.raw[block][st], pl.turn))) break;
           uint4* at = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
                                                block * T::kSfBlock) + lane;
           const uint4 a = at[0], b = at[32], c = at[64], d = at[96];
@@ -570,11 +613,12 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           at[64] = make_uint4(a.z, b.z, c.z, d.z);
           at[96] = make_uint4(a.w, b.w, c.w, d.w);
           fence_smem_async();
-        } else if (!(ok = wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1))) {
+        } else if (!(ok = wait_warp(&s.empty[st], pl.turn ^ 1))) {
           break;
         }
         __syncwarp();
         if (lane == 0) arrive_first(&s.full[st]);
+        if (k == w.k0) more = seek(item += pairs, ahead);
       }
     }
   } else {
@@ -601,27 +645,26 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
       bool have = false;
       uint4 lo[kAhead][kB][4], hi[kAligned ? 1 : kAhead][kB][4];
       uint32_t off[kAhead];            // low bits of the lane's first address
-      int count[kAhead], valid[kAhead];  // stages of a fetch (0: the end), bytes of the lane's piece
+      // the end of a fetch's stages (0: no more), their begin, bytes of the lane's piece
+      int count[kAhead], lead[kAhead], valid[kAhead];
       const uint32_t row_step = (uint32_t)(32 * p.sf_stride), line_step = (uint32_t)(kLines * p.sf_stride);
       auto fetch = [&](auto slot_c) {
         constexpr int kSlot = decltype(slot_c)::value;
         count[kSlot] = 0;
         while (!have || k >= w.k1) {
           if (have) item += pairs;
-          have = false;
-          if (item >= items) return;
-          if (!work_of(item, w)) {
-            item += pairs;
-            continue;
-          }
-          have = true;
+          have = seek(item, w);
+          if (!have) return;
           k = w.k0;
+          // (a weights' gradient may begin inside 16 aligned bytes)
+          if (kAligned && T::kWgrad) k -= (int)(w.k_at / T::kStageK + k) % T::kFetch;
         }
         const int64_t row0 = (block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + line;
         const int64_t at = w.k_at / 32 + (int64_t)k * T::kStageSf + 16 * piece;
         const bool any = (block == 0 || 128 * (block - 1) < w.cols) &&
                          piece * T::kFetch < w.k1 - k;
         count[kSlot] = min(kStages, w.k1 - k);
+        lead[kSlot] = max(w.k0 - k, 0);
         valid[kSlot] = (int)max((int64_t)0, min(p.sf_stride - at, (int64_t)16));
         k += kStages;
         const uint8_t* first = base + row0 * p.sf_stride + at;
@@ -645,7 +688,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           }
         }
       };
-      uint32_t n = 0;
+      Place pl;
       // the stages of a fetch, to shared memory; false at the end
       auto store = [&](auto slot_c) -> bool {
         constexpr int kSlot = decltype(slot_c)::value;
@@ -666,8 +709,9 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
 #pragma unroll
         for (int c = 0; c < kStages; ++c) {
           if (c >= count[kSlot]) break;
-          const uint32_t st = n % stages;
-          if (!wait_warp(&s.empty[st], ((n / stages) & 1) ^ 1)) return false;
+          if (kAligned && T::kWgrad && c < lead[kSlot]) continue;
+          const int st = pl.st;
+          if (!wait_warp(&s.empty[st], pl.turn ^ 1)) return false;
           if (block <= c_blocks && piece == c / T::kFetch) {
             uint4* dst = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
                                                   block * T::kSfBlock) + line;
@@ -683,7 +727,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           }
           __syncwarp();
           if (lane == 0) arrive_first(&s.full[st]);
-          ++n;
+          pl.next(stages);
         }
         return true;
       };
