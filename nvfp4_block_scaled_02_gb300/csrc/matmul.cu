@@ -107,8 +107,8 @@ struct Kind {
 // columns, over stages k0 .. k1 - 1 of the sum.
 struct Work {
   int g, f0, c0, cols;      // group, first feature, first column, columns
-  int64_t f_row, c_row;     // rows of the two matrices
-  int64_t k_at;             // first value of the sum
+  int f_row, c_row;         // rows of the two matrices
+  int k_at;                 // first value of the sum
   int first, steps;         // the sum's first product and the end of its products
   int k0, k1;
   int tile, part, parts;
@@ -168,7 +168,6 @@ template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   using T = Kind<KIND>;
-  pdl_begin();
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
   uint8_t* ring = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -178,6 +177,28 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   const int pair = (int)blockIdx.x / CG, pairs = (int)gridDim.x / CG;
   const int f_tiles = (p.N + kTileF * CG - 1) / (kTileF * CG);
   const int64_t rows_all = T::kWgrad ? p.K : p.c_rows;
+
+  // NVFP4 rows whose scales are aligned: a stage's 16 bytes of a row are copied to their stage
+  // and turned there into the layout of tensor memory
+  const bool in_place = T::kFp4 && p.sf_stride % 16 == 0;
+  // What does not depend on earlier kernels, while they end.
+  if (warp == 0) {
+    if (lane < kMaxStages) {
+      mbar_init(&s.full[lane], 1 + CG * (in_place ? kScaleWarps / 2 : kScaleWarps));
+      mbar_init(&s.empty[lane], 1);
+      for (int b = 0; b < 3; ++b) mbar_init(&s.raw[b][lane], 1);
+    } else if (lane == kMaxStages) {
+      s.dead = 0;
+      mbar_init(&s.acc_full, 1);
+      mbar_init(&s.acc_free, CG * kEpilogueWarps);
+      mbar_init(&s.end, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == kCopyWarp && lane < (in_place ? 6 : 3)) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const CUtensorMap*>(&maps) + lane)
+                 : "memory");
+  }
+  pdl_begin();
 
   // ---- the groups' tiles -----------------------------------------------------
   // a thread to `share` groups, then a scan over the threads
@@ -210,21 +231,6 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   most = __reduce_max_sync(kAll, most);
   if (lane == 31) s.scan[warp] = incl;
   if (lane == 0) s.most[warp] = most;
-  // NVFP4 rows whose scales are aligned: a stage's 16 bytes of a row are copied to their stage
-  // and turned there into the layout of tensor memory
-  const bool in_place = T::kFp4 && p.sf_stride % 16 == 0;
-  if (tid == 0) {
-    s.dead = 0;
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&s.full[i], 1 + CG * (in_place ? kScaleWarps / 2 : kScaleWarps));
-      mbar_init(&s.empty[i], 1);
-      for (int b = 0; b < 3; ++b) mbar_init(&s.raw[b][i], 1);
-    }
-    mbar_init(&s.acc_full, 1);
-    mbar_init(&s.acc_free, CG * kEpilogueWarps);
-    mbar_init(&s.end, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   __syncthreads();
   int before = incl - mine, total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
@@ -255,9 +261,15 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   const int stage_bytes = (sf_at + (1 + c_blocks) * T::kSfBlock + 1023) & ~1023;
   const int stages = min(kRing / stage_bytes, kMaxStages);
 
+  // 32-bit unsigned divisions only, and none where there is one of a kind: what a call
+  // that fits the SMs once pays before its first copy.
   auto work_of = [&](int item, Work& w) -> bool {
-    w.tile = item / split;
-    w.part = item - w.tile * split;
+    w.tile = item;
+    w.part = 0;
+    if (split > 1) {
+      w.tile = (int)((uint32_t)item / (uint32_t)split);
+      w.part = item - w.tile * split;
+    }
     int lo = 0, hi = p.E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -268,29 +280,44 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
     const int row = p.start ? __ldg(p.start + lo) : 0;
     const int rows = p.start ? __ldg(p.start + lo + 1) - row : (int)rows_all;
     const int cols = T::kWgrad ? p.C : rows;
-    const int c_tiles = (cols + kTileC - 1) / kTileC, size = (cols + c_tiles - 1) / c_tiles;
-    // bands of column tiles, a band's columns first
-    const int r = w.tile - s.tile[lo], band = r / (kBand * f_tiles);
-    const int wide = min(kBand, c_tiles - band * kBand), in = r - band * kBand * f_tiles;
-    const int ft = in / wide, ct = band * kBand + in - ft * wide;
+    int ft = w.tile - s.tile[lo];
+    w.c0 = 0;
+    w.cols = cols;
+    if (cols > kTileC) {
+      const uint32_t c_tiles = (uint32_t)(cols + kTileC - 1) / kTileC;
+      const uint32_t size = ((uint32_t)cols + c_tiles - 1) / c_tiles;
+      // bands of column tiles, a band's columns first
+      uint32_t band = 0, in = (uint32_t)ft, wide = c_tiles;
+      if (c_tiles > kBand) {
+        band = in / (uint32_t)(kBand * f_tiles);
+        in -= band * (uint32_t)(kBand * f_tiles);
+        wide = min((uint32_t)kBand, c_tiles - band * kBand);
+      }
+      ft = (int)(in / wide);
+      w.c0 = (int)((band * kBand + in - (uint32_t)ft * wide) * size);
+      w.cols = min((int)size, cols - w.c0);
+    }
     w.f0 = (ft * CG + rank) * kTileF;
-    w.c0 = ct * size;
-    w.cols = min(size, cols - w.c0);
     // A weights' gradient sums over values `row` on, in stages that begin at multiples of 128
     // (whole words of scales): the first stage's products in front of it are left out.
-    const int skip = T::kWgrad ? row % T::kStageK : 0;
-    const int64_t sum = T::kWgrad ? (rows > 0 ? rows + skip : 0) : p.K;
+    const int skip = T::kWgrad ? row & (T::kStageK - 1) : 0;
+    const int sum = T::kWgrad ? (rows > 0 ? rows + skip : 0) : (int)p.K;
     w.k_at = T::kWgrad ? row - skip : 0;
     w.first = skip / T::kStepK;
-    w.f_row = (T::kWgrad ? 0 : (int64_t)lo * p.N) + w.f0;
+    w.f_row = (T::kWgrad ? 0 : lo * p.N) + w.f0;
     w.c_row = (T::kWgrad ? 0 : row) + w.c0;
-    w.steps = (int)((sum + T::kStepK - 1) / T::kStepK);
-    const int n = (int)((sum + T::kStageK - 1) / T::kStageK);
-    // a part is of whole fetches of scales, and of two stages at least
-    const int units = (n + T::kFetch - 1) / T::kFetch;
-    w.parts = min(split, max(1, min(n / 2, units)));
-    w.k0 = (int)((int64_t)units * w.part / w.parts) * T::kFetch;
-    w.k1 = min(n, (int)((int64_t)units * (w.part + 1) / w.parts) * T::kFetch);
+    w.steps = (int)((uint32_t)(sum + T::kStepK - 1) / T::kStepK);
+    const int n = (int)((uint32_t)(sum + T::kStageK - 1) / T::kStageK);
+    w.parts = 1;
+    w.k0 = 0;
+    w.k1 = n;
+    if (split > 1) {
+      // a part is of whole fetches of scales, and of two stages at least
+      const int units = (n + T::kFetch - 1) / T::kFetch;
+      w.parts = min(split, max(1, min(n / 2, units)));
+      w.k0 = (int)((uint32_t)(units * w.part) / (uint32_t)w.parts) * T::kFetch;
+      w.k1 = min(n, (int)((uint32_t)(units * (w.part + 1)) / (uint32_t)w.parts) * T::kFetch);
+    }
     return w.part < w.parts && w.cols > 0;
   };
   // The pair's next piece of work from `item` on; false at the end. Finding one takes some
@@ -351,19 +378,21 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
       const uint32_t acc = acc_lane + (buf ? kAcc1 : 0);
       const int f = w.f0 + quarter * 32 + lane;
       float* part = p.part + ((int64_t)item * CG + rank) * kMatmulPart + quarter * 32 + lane;
-      // the result of column c and the next ones, for the lane's feature
-      auto put = [&](int c, float (&v)[32]) {
+      // the results of columns c .. c + n - 1, for the lane's feature
+      auto put = [&](int c, auto& v) {
+        constexpr int kN = sizeof(v) / sizeof(float);
         if constexpr (T::kFp4) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], sc[c + i < w.cols ? c + i : 0]), gf);
+          for (int i = 0; i < kN; ++i)
+            v[i] = __fmul_rn(__fmul_rn(v[i], sc[c + i < w.cols ? c + i : 0]), gf);
         }
-        const int64_t row0 = T::kWgrad ? (int64_t)w.g * p.C + w.c0 : w.c_row;
+        const int64_t row0 = T::kWgrad ? (int64_t)w.g * p.C + w.c0 : (int64_t)w.c_row;
         // every lane has a feature, every column is there: no checks
-        const bool whole = c + 32 <= w.cols && f - lane + 32 <= p.N;
+        const bool whole = c + kN <= w.cols && f - lane + 32 <= p.N;
         if (p.out_f32) {
           float* o = static_cast<float*>(p.out) + (row0 + c) * p.N + f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i, o += p.N)
+          for (int i = 0; i < kN; ++i, o += p.N)
             if (whole || (c + i < w.cols && f < p.N)) *o = v[i];
         } else if (p.N % 2 == 0) {
           // neighbouring lanes swap, so that each stores two features of one column
@@ -371,7 +400,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
                                                     (row0 + c + odd) * p.N + (f & ~1));
 #pragma unroll
-          for (int i = 0; i < 32; i += 2, o += p.N) {
+          for (int i = 0; i < kN; i += 2, o += p.N) {
             const uint32_t a = pack_bf16x2(v[i], v[i + 1]), b = __shfl_xor_sync(kAll, a, 1);
             const uint32_t x = __byte_perm(a, b, odd ? 0x3276u : 0x5410u);
             if (whole || (c + i + odd < w.cols && f < p.N)) *o = x;
@@ -379,7 +408,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
         } else {
           uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + c) * p.N + f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i, o += p.N)
+          for (int i = 0; i < kN; ++i, o += p.N)
             if (whole || (c + i < w.cols && f < p.N)) *o = (uint16_t)pack_bf16x2(v[i], 0.0f);
         }
       };
@@ -417,28 +446,37 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
       if (sum) ++done;
       if (w.parts > 1) {
         // the CTA that takes the tile's last ticket adds the parts in order
-        __threadfence();
         asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
-        if (tid == 0) s.last = atomicAdd(&p.tickets[w.tile * CG + rank], 1u) == (uint32_t)w.parts - 1;
+        if (tid == 0) {
+          __threadfence();
+          s.last = atomicAdd(&p.tickets[w.tile * CG + rank], 1u) == (uint32_t)w.parts - 1;
+          __threadfence();
+        }
         asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
         if (s.last) {
-          __threadfence();
           const float* all =
               p.part + ((int64_t)w.tile * split * CG + rank) * kMatmulPart + quarter * 32 + lane;
 #pragma unroll 1
-          for (int chunk = half; chunk * 32 < w.cols; chunk += 2) {
-            float v[32];
+          for (int c = half * 16; c < w.cols; c += 32) {
+            float v[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
 #pragma unroll 1
-            for (int q = 0; q < w.parts; ++q) {
+            for (int q = 0; q < w.parts; q += 4) {  // loads of four parts in flight
+              float r[4][16];
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (chunk * 32 + j < w.cols)
-                  v[j] = __fadd_rn(v[j], __ldcg(all + (int64_t)q * CG * kMatmulPart +
-                                                  (chunk * 32 + j) * 128));
+              for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  r[u][j] = q + u < w.parts && c + j < w.cols
+                                ? __ldcg(all + (int64_t)(q + u) * CG * kMatmulPart + (c + j) * 128)
+                                : 0.0f;
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], r[u][j]);
             }
-            put(chunk * 32, v);
+            put(c, v);
           }
           if (tid == 0) p.tickets[w.tile * CG + rank] = 0;
         }
@@ -457,8 +495,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
       const int held = ((w.cols + 15) & ~15) / CG;  // columns of this CTA
       const Boxes boxes(held);
       const uint32_t bytes = kFBytes + boxes.rows() * kStageRow;
-      const int x0 = (int)(T::kFp4 ? 0 : w.k_at);
-      const int c_row = (int)w.c_row + rank * held + boxes.row(lane);
+      const int x0 = w.k_at;
+      const int c_row = w.c_row + rank * held + boxes.row(lane);
       const CUtensorMap* c_box = lane < boxes.large ? &maps.c : &maps.c_small;
       for (int k = w.k0; k < w.k1; ++k, pl.next(stages)) {
         const int st = pl.st;
@@ -470,14 +508,14 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           const uint32_t bar = cluster_addr(&s.full[st], 0);
           if (lane == 0) {
             if (rank == 0) mbar_expect(&s.full[st], 2 * bytes);
-            tma_load_pair(dst, &maps.f, x, (int)w.f_row, bar);
+            tma_load_pair(dst, &maps.f, x, w.f_row, bar);
           }
           __syncwarp();
           if (lane < boxes.count) tma_load_pair(c_dst, c_box, x, c_row, bar);
         } else {
           if (lane == 0) {
             mbar_expect(&s.full[st], bytes);
-            tma_load(dst, &maps.f, x, (int)w.f_row, &s.full[st]);
+            tma_load(dst, &maps.f, x, w.f_row, &s.full[st]);
           }
           __syncwarp();
           if (lane < boxes.count) tma_load(c_dst, c_box, x, c_row, &s.full[st]);
@@ -573,7 +611,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
       const int row = boxes.row(lane - 1), in = lane == 0 ? 0 : 1 + row / 128;  // its 128 rows
       const CUtensorMap* map =
           lane == 0 ? &maps.fs : lane <= boxes.large ? &maps.cs : &maps.cs_small;
-      const int y = lane == 0 ? (int)w.f_row : (int)w.c_row + row;
+      const int y = lane == 0 ? w.f_row : w.c_row + row;
       const uint32_t at = sf_at + (lane == 0 ? 0 : T::kSfBlock + row * T::kStageSf);
       const int held = lane == 0 ? 128 : max(0, min(boxes.rows() - (lane - 1) * 128, 128));
       for (int k = w.k0; k < w.k1; ++k, pl.next(stages)) {
@@ -659,13 +697,13 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
           // (a weights' gradient may begin inside 16 aligned bytes)
           if (kAligned && T::kWgrad) k -= (int)(w.k_at / T::kStageK + k) % T::kFetch;
         }
-        const int64_t row0 = (block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + line;
-        const int64_t at = w.k_at / 32 + (int64_t)k * T::kStageSf + 16 * piece;
+        const int64_t row0 = (int64_t)(block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + line;
+        const int at = w.k_at / 32 + k * T::kStageSf + 16 * piece;
         const bool any = (block == 0 || 128 * (block - 1) < w.cols) &&
                          piece * T::kFetch < w.k1 - k;
         count[kSlot] = min(kStages, w.k1 - k);
         lead[kSlot] = max(w.k0 - k, 0);
-        valid[kSlot] = (int)max((int64_t)0, min(p.sf_stride - at, (int64_t)16));
+        valid[kSlot] = max(0, min((int)p.sf_stride - at, 16));
         k += kStages;
         const uint8_t* first = base + row0 * p.sf_stride + at;
         off[kSlot] = (uint32_t)(uintptr_t)first;
