@@ -197,7 +197,12 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   } else if (warp == kCopyWarp && lane < (in_place ? 6 : 3)) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const CUtensorMap*>(&maps) + lane)
                  : "memory");
+  } else if (warp == kMmaWarp) {
+    if constexpr (CG == 2) tmem_alloc_pair(&s.tmem, 512);
+    else tmem_alloc(&s.tmem, 512);
   }
+  __syncwarp();
+  if constexpr (CG == 2) cluster_arrive();
   pdl_begin();
 
   // ---- the groups' tiles -----------------------------------------------------
@@ -231,7 +236,10 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   most = __reduce_max_sync(kAll, most);
   if (lane == 31) s.scan[warp] = incl;
   if (lane == 0) s.most[warp] = most;
+  fence_before();
   __syncthreads();
+  fence_after();
+  if constexpr (CG == 2) cluster_wait();  // the other CTA's barriers are there
   int before = incl - mine, total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s.scan[w];
@@ -240,18 +248,10 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   }
   for (int e = e0; e < e1; ++e) s.tile[e] += before;
   if (tid == 0) s.tile[p.E] = total;
+  __syncthreads();
   // parts of a tile's sum, for more CTAs than tiles
   const int split = max(1, min(pairs / max(total, 1), 16));
   const int items = total * split;
-  if (pair >= items) return;
-  if (warp == kMmaWarp) {
-    if constexpr (CG == 2) tmem_alloc_pair(&s.tmem, 512);
-    else tmem_alloc(&s.tmem, 512);
-  }
-  fence_before();
-  if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers are there
-  else __syncthreads();
-  fence_after();
   const uint32_t tmem = s.tmem;
 
   // a stage: features' codes, columns' codes, features' scales, columns' scales
@@ -784,8 +784,11 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   }
   __syncwarp();
   fence_before();
-  if constexpr (CG == 2) cluster_sync();  // nothing of the other CTA's reads or signals here
-  else __syncthreads();
+  if constexpr (CG == 2) {  // nothing of the other CTA's reads or signals here
+    cluster_arrive();
+    cluster_wait();
+  }
+  if constexpr (CG == 1) __syncthreads();
   fence_after();
   if (warp == kMmaWarp) {
     if constexpr (CG == 2) tmem_free_pair(tmem, 512);
