@@ -81,15 +81,15 @@ __device__ __forceinline__ uint4 first_bytes(uint4 x, int n) {
 // of it, small ones.
 struct Boxes {
   int large, count;
-  __device__ __forceinline__ explicit Boxes(int n) {
+  __host__ __device__ __forceinline__ explicit Boxes(int n) {
     const int rest = n % kBox;
     large = n / kBox + (rest > kBox / 2);
     count = large + (rest > kBox / 2 ? 0 : (rest + kBoxSmall - 1) / kBoxSmall);
   }
-  __device__ __forceinline__ int row(int i) const {  // of box i
+  __host__ __device__ __forceinline__ int row(int i) const {  // of box i
     return i < large ? i * kBox : large * kBox + (i - large) * kBoxSmall;
   }
-  __device__ __forceinline__ int rows() const { return row(count); }
+  __host__ __device__ __forceinline__ int rows() const { return row(count); }
 };
 
 template <int KIND>
@@ -102,6 +102,31 @@ struct Kind {
   static constexpr int kSfBlock = 128 * kStageSf;   // scale bytes of 128 rows in a stage
   static constexpr int kFetch = 16 / kStageSf;      // stages whose scales are fetched together
 };
+
+// How a call is cut: tiles, parts of a tile's sum (where there are more CTAs than tiles), and
+// a stage of the ring: features' codes, columns' codes, features' scales, columns' scales (a
+// pair's CTA holds half of the columns' codes and all of their scales).
+struct Geometry {
+  int split, items;
+  int c_blocks, sf_at, stage_bytes, stages;
+};
+// total tiles of at most `most` columns, for so many CTAs or pairs of CTAs
+template <int KIND, int CG>
+__host__ __device__ __forceinline__ Geometry geometry(int total, int most, int pairs) {
+  Geometry g;
+  g.split = 1;
+  if (total > 0 && 2 * total <= pairs) {
+    g.split = (int)((uint32_t)pairs / (uint32_t)total);
+    if (g.split > 16) g.split = 16;
+  }
+  g.items = total * g.split;
+  g.c_blocks = (most + 127) / 128;
+  g.sf_at = kFBytes + Boxes(((most + 15) & ~15) / CG).rows() * kStageRow;
+  g.stage_bytes = (g.sf_at + (1 + g.c_blocks) * Kind<KIND>::kSfBlock + 1023) & ~1023;
+  g.stages = (int)((uint32_t)kRing / (uint32_t)g.stage_bytes);
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
+  return g;
+}
 
 // What one CTA does at a time: features f0 .. of a group times some of its
 // columns, over stages k0 .. k1 - 1 of the sum.
@@ -160,13 +185,14 @@ struct Shared {
   volatile int dead;
   int last;
   int scan[kThreads / 32], most[kThreads / 32];
+  Geometry geo;
   int tile[kMatmulMaxGroups + 1];  // a group's first tile
   float scale[2][kTileC];          // outer scales of a tile's columns
 };
 
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
-matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
+matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geometry geo_known) {
   using T = Kind<KIND>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
@@ -177,6 +203,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   const int pair = (int)blockIdx.x / CG, pairs = (int)gridDim.x / CG;
   const int f_tiles = (p.N + kTileF * CG - 1) / (kTileF * CG);
   const int64_t rows_all = T::kWgrad ? p.K : p.c_rows;
+  const bool scan = !T::kWgrad && p.start;  // the tiles are known on the device only
 
   // NVFP4 rows whose scales are aligned: a stage's 16 bytes of a row are copied to their stage
   // and turned there into the layout of tensor memory
@@ -206,60 +233,59 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
   pdl_begin();
 
   // ---- the groups' tiles -----------------------------------------------------
-  // a thread to `share` groups, then a scan over the threads
+  // Ragged rows: a thread to `share` groups, then a scan over the threads. Otherwise the
+  // host knows the tiles.
+  const bool sf_aligned = p.sf_stride % 16 == 0;
+  int before = 0, mine = 0;
   const int share = (p.E + kThreads - 1) / kThreads;
   const int e0 = min(tid * share, p.E), e1 = min(e0 + share, p.E);
-  int mine = 0, most = 0;
-  // whether the 16 scale bytes of a row that are fetched together are aligned
-  const bool sf_aligned = p.sf_stride % 16 == 0;
-  for (int e = e0; e < e1; ++e) {
-    int64_t a = p.start ? p.start[e] : 0, b = p.start ? p.start[e + 1] : rows_all;
-    bool bad = a < 0 || b < a || b > rows_all;
-    if (T::kWgrad) {
-      bad = bad || (a | b) % 32 != 0;
+  if (scan) {
+    int most = 0;
+    for (int e = e0; e < e1; ++e) {
+      int64_t a = p.start[e], b = p.start[e + 1];
+      if (a < 0 || b < a || b > rows_all) {
+        if (blockIdx.x == 0) flag(p.status, NVFP4_DEV_BAD_INDEX);
+        a = b = 0;
+      }
+      const int cols = (int)(b - a), c_tiles = (cols + kTileC - 1) / kTileC;
+      if (c_tiles > 0)
+        most = max(most, c_tiles == 1 ? cols
+                                      : (int)((uint32_t)(cols + c_tiles - 1) / (uint32_t)c_tiles));
+      s.tile[e] = mine;
+      mine += c_tiles * f_tiles;
     }
-    if (bad) {
-      if (blockIdx.x == 0) flag(p.status, NVFP4_DEV_BAD_INDEX);
-      a = b = 0;
+    int incl = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kAll, incl, d);
+      if (lane >= d) incl += o;
     }
-    const int cols = T::kWgrad ? p.C : (int)(b - a);
-    const int c_tiles = (cols + kTileC - 1) / kTileC;
-    if (c_tiles > 0) most = max(most, (cols + c_tiles - 1) / c_tiles);
-    s.tile[e] = mine;
-    if (!bad) mine += c_tiles * f_tiles;
+    most = __reduce_max_sync(kAll, most);
+    if (lane == 31) s.scan[warp] = incl;
+    if (lane == 0) s.most[warp] = most;
+    before = incl - mine;
   }
-  int incl = mine;
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(kAll, incl, d);
-    if (lane >= d) incl += o;
-  }
-  most = __reduce_max_sync(kAll, most);
-  if (lane == 31) s.scan[warp] = incl;
-  if (lane == 0) s.most[warp] = most;
   fence_before();
   __syncthreads();
   fence_after();
   if constexpr (CG == 2) cluster_wait();  // the other CTA's barriers are there
-  int before = incl - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s.scan[w];
-    total += s.scan[w];
-    most = max(most, s.most[w]);
+  if (scan) {
+    int total = 0, most = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s.scan[w];
+      total += s.scan[w];
+      most = max(most, s.most[w]);
+    }
+    for (int e = e0; e < e1; ++e) s.tile[e] += before;
+    if (tid == 0) {
+      s.tile[p.E] = total;
+      s.geo = geometry<KIND, CG>(total, most, pairs);
+    }
+    __syncthreads();
   }
-  for (int e = e0; e < e1; ++e) s.tile[e] += before;
-  if (tid == 0) s.tile[p.E] = total;
-  __syncthreads();
-  // parts of a tile's sum, for more CTAs than tiles
-  const int split = max(1, min(pairs / max(total, 1), 16));
-  const int items = total * split;
+  const Geometry geo = scan ? s.geo : geo_known;
+  const int split = geo.split, items = geo.items, c_blocks = geo.c_blocks, sf_at = geo.sf_at;
+  const int stage_bytes = geo.stage_bytes, stages = geo.stages;
   const uint32_t tmem = s.tmem;
-
-  // a stage: features' codes, columns' codes, features' scales, columns' scales
-  // (a pair's CTA holds half of the columns' codes and all of their scales)
-  const int c_blocks = (most + 127) / 128;
-  const int sf_at = kFBytes + Boxes(((most + 15) & ~15) / CG).rows() * kStageRow;
-  const int stage_bytes = (sf_at + (1 + c_blocks) * T::kSfBlock + 1023) & ~1023;
-  const int stages = min(kRing / stage_bytes, kMaxStages);
 
   // 32-bit unsigned divisions only, and none where there is one of a kind: what a call
   // that fits the SMs once pays before its first copy.
@@ -270,17 +296,30 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p) {
       w.tile = (int)((uint32_t)item / (uint32_t)split);
       w.part = item - w.tile * split;
     }
-    int lo = 0, hi = p.E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.tile[mid] <= w.tile) lo = mid;
-      else hi = mid;
+    int lo = 0, ft = w.tile;
+    if (scan) {
+      int hi = p.E;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.tile[mid] <= w.tile) lo = mid;
+        else hi = mid;
+      }
+      ft -= s.tile[lo];
+    } else if (T::kWgrad) {
+      lo = (int)fastdiv((uint32_t)w.tile, p.by_tiles);
+      ft -= lo * p.tiles;
     }
     w.g = lo;
-    const int row = p.start ? __ldg(p.start + lo) : 0;
-    const int rows = p.start ? __ldg(p.start + lo + 1) - row : (int)rows_all;
+    int row = 0, rows = (int)rows_all;
+    if (p.start) {
+      row = __ldg(p.start + lo);
+      rows = __ldg(p.start + lo + 1) - row;
+    }
+    if (T::kWgrad && (row < 0 || rows < 0 || rows > rows_all - row || (row | rows) % 32 != 0)) {
+      flag(p.status, NVFP4_DEV_BAD_INDEX);
+      return false;
+    }
     const int cols = T::kWgrad ? p.C : rows;
-    int ft = w.tile - s.tile[lo];
     w.c0 = 0;
     w.cols = cols;
     if (cols > kTileC) {
@@ -843,7 +882,15 @@ cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   lc.attrs = at;
   lc.numAttrs = CG;
-  return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, m, p);
+  const int cols = KIND == kMatmulMxWgrad ? p.C : (int)p.c_rows;
+  const int c_tiles = (cols + kTileC - 1) / kTileC;
+  MatmulParams q = p;
+  q.tiles = c_tiles * ((p.N + kTileF * CG - 1) / (kTileF * CG));
+  q.by_tiles = make_fastdiv((uint32_t)std::max(q.tiles, 1));
+  const Geometry geo = geometry<KIND, CG>(q.tiles * (KIND == kMatmulMxWgrad ? p.E : 1),
+                                          (cols + c_tiles - 1) / std::max(c_tiles, 1),
+                                          (int)lc.gridDim.x / CG);
+  return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, m, q, geo);
 }
 template <int KIND>
 cudaError_t launch_k(const MatmulParams& p, const Maps& m, cudaStream_t st) {

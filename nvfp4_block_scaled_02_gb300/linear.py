@@ -14,7 +14,7 @@ import struct
 import torch
 
 from . import (Config, SCALE_E4M3, TARGET_MXFP8, TARGET_NVFP4, _check, _i32, _i64, _Out, _vp)
-from .kv import _BF16, _I32, _elsewhere, _lib, _optional, _refuse, _stream, _typed, _workspace
+from .kv import _BF16, _I32, _lib, _optional, _refuse, _typed, _workspace
 
 _F32 = (torch.float32,)
 _U8 = (torch.uint8, torch.int8)
@@ -25,8 +25,11 @@ class _Operand(C.Structure):
                 ("scale_max", C.c_float)]
 
 
-_OPERAND = struct.Struct("@3Pqf4x")
-assert _OPERAND.size == C.sizeof(_Operand)
+# structs packed into bytes, as in kv; the default config is packed once
+_OPERAND, _OUT = struct.Struct("@3Pqf4x"), struct.Struct("@4P")
+assert _OPERAND.size == C.sizeof(_Operand) and _OUT.size == C.sizeof(_Out)
+_DEFAULT = bytes(Config().c())
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def declare(L: C.CDLL) -> None:
@@ -57,11 +60,11 @@ def grouped_matmul_workspace(device) -> torch.Tensor:
 
 def _bytes(t: torch.Tensor, name: str, n: int, dev: int) -> int:
     """An encoding's array of exactly n bytes."""
+    if t.dtype in _U8 and t.numel() == n and t.get_device() == dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in _U8 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
         _refuse(t, name, None, _U8, dev)
-    if t.numel() != n:
-        raise ValueError(f"{name} holds {t.numel()} bytes; the call needs {n}")
-    return t.data_ptr()
+    raise ValueError(f"{name} holds {t.numel()} bytes; the call needs {n}")
 
 
 def _rows_of(t: torch.Tensor, name: str) -> tuple[int, int]:
@@ -100,6 +103,7 @@ def _result(out, shape, dtypes, device, dev: int):
 
 
 def _ws(workspace, device, dev: int):
+    """The workspace (which has to outlive the call's enqueuing), its address and bytes."""
     if workspace is None:
         workspace = grouped_matmul_workspace(device)
     return workspace, _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel()
@@ -128,7 +132,7 @@ def nvfp4_grouped_matmul(a: dict, a_amax: torch.Tensor, b: dict, b_amax: torch.T
     for the call when none is given."""
     ac, bc = a["codes"], b["codes"]
     dev = ac.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _device():
         with torch.cuda.device(dev):
             return nvfp4_grouped_matmul(a, a_amax, b, b_amax, group_start, a_cfg, b_cfg, out,
                                         workspace, status)
@@ -152,7 +156,7 @@ def nvfp4_grouped_matmul(a: dict, a_amax: torch.Tensor, b: dict, b_amax: torch.T
     workspace, ws, ws_bytes = _ws(workspace, ac.device, dev)
     code = _lib().nvfp4_grouped_matmul(
         pa, pb, T, E, N, 2 * half, start, to, ws, ws_bytes,
-        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
     if code:
         _check("nvfp4_grouped_matmul", code)
     return out
@@ -167,7 +171,7 @@ def nvfp4_mx_grouped_matmul(a: dict, b: dict, group_start: torch.Tensor | None =
     out_cols, cols]."""
     ac, bc = a["codes"], b["codes"]
     dev = ac.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _device():
         with torch.cuda.device(dev):
             return nvfp4_mx_grouped_matmul(a, b, group_start, out, workspace, status)
     T, K = _rows_of(ac, "a codes")
@@ -182,7 +186,7 @@ def nvfp4_mx_grouped_matmul(a: dict, b: dict, group_start: torch.Tensor | None =
     workspace, ws, ws_bytes = _ws(workspace, ac.device, dev)
     code = _lib().nvfp4_mx_grouped_matmul(
         *ins, T, E, N, K, start, to, ws, ws_bytes,
-        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
     if code:
         _check("nvfp4_mx_grouped_matmul", code)
     return out
@@ -199,7 +203,7 @@ def nvfp4_mx_grouped_wgrad(g: dict, x: dict, group_start: torch.Tensor | None = 
     Every entry of group_start is a multiple of 32."""
     gc, xc = g["codes"], x["codes"]
     dev = gc.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _device():
         with torch.cuda.device(dev):
             return nvfp4_mx_grouped_wgrad(g, x, group_start, out, out_dtype, workspace, status)
     if out_dtype not in (torch.bfloat16, torch.float32):
@@ -222,7 +226,7 @@ def nvfp4_mx_grouped_wgrad(g: dict, x: dict, group_start: torch.Tensor | None = 
     workspace, ws, ws_bytes = _ws(workspace, gc.device, dev)
     code = _lib().nvfp4_mx_grouped_wgrad(
         *ins, T, E, N, K, start, to, f32, ws, ws_bytes,
-        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
     if code:
         _check("nvfp4_mx_grouped_wgrad", code)
     return out
@@ -250,62 +254,75 @@ def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor,
     for. `out`: an encoding of an earlier call. Nothing is recorded for autograd:
     nvfp4_add_rms_norm_bwd gives the gradient."""
     dev = x.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _device():
         with torch.cuda.device(dev):
             return nvfp4_add_rms_norm(x, weight, residual, eps, target, cfg, global_amax, dequant,
                                       h, y, out, row_amax, status)
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [rows, cols]")
-    if target not in (TARGET_MXFP8, TARGET_NVFP4):
+    R, Cc = shape
+    # one expression for what is usual; what is wrong is looked up only if it fails
+    if not (x.dtype in _BF16 and x.is_contiguous() and dev >= 0 and weight.dtype in _BF16
+            and weight.shape == (Cc,) and weight.get_device() == dev and weight.is_contiguous()
+            and (residual is None or (residual.dtype in _BF16 and residual.shape == shape
+                                      and residual.get_device() == dev
+                                      and residual.is_contiguous()))):
+        _matrix(x, "x", shape, dev)
+        _matrix(weight, "weight", (Cc,), dev)
+        _matrix(residual, "residual", shape, dev)
+    fp4 = target == TARGET_NVFP4
+    if not fp4 and target != TARGET_MXFP8:
         raise ValueError("target must be TARGET_MXFP8 or TARGET_NVFP4")
-    R, Cc = shape = x.shape
-    device, u8, fp4 = x.device, torch.uint8, target == TARGET_NVFP4
-    cfg = cfg or Config()
-    ins = (_matrix(x, "x", shape, dev),
-           0 if residual is None else _matrix(residual, "residual", shape, dev),
-           _matrix(weight, "weight", (Cc,), dev))
-    empty = torch.empty
+    empty, device = torch.empty, x.device
     if residual is None:
         if h is not None and h is not x:
             raise ValueError("h is x itself without a residual")
         h, h_at = x, 0
+    elif h is None:
+        h = torch.empty_like(x)
+        h_at = h.data_ptr()
     else:
-        h = empty(shape, dtype=x.dtype, device=device) if h is None else h
         h_at = _matrix(h, "h", shape, dev)
-    fos = fp4 and bool(cfg.four_over_six)
+    fos = fp4 and cfg is not None and bool(cfg.four_over_six)
     per, block = (2, 16) if fp4 else (1, 32)
-    words = R * ((Cc + 511) // 512)
     if out is None:
-        out = {"codes": empty((R, Cc // per), dtype=u8, device=device),
-               "scales": empty((R, Cc // block), dtype=u8, device=device),
-               "choice": empty((R, (Cc + 511) // 512), dtype=torch.int32, device=device)
-               if fos else None,
-               "dequant": empty(shape, dtype=torch.bfloat16, device=device)
-               if dequant and fp4 else None}
-        o = _Out(out["codes"].data_ptr(), out["scales"].data_ptr(),
-                 out["choice"].data_ptr() if fos else None,
-                 None if out["dequant"] is None else out["dequant"].data_ptr())
+        codes = empty((R, Cc // per), dtype=torch.uint8, device=device)
+        scales = empty((R, Cc // block), dtype=torch.uint8, device=device)
+        choice = dq = None
+        if fos:
+            choice = empty((R, (Cc + 511) // 512), dtype=torch.int32, device=device)
+        if dequant and fp4:
+            dq = empty(shape, dtype=torch.bfloat16, device=device)
+        o = _OUT.pack(codes.data_ptr(), scales.data_ptr(), choice.data_ptr() if fos else 0,
+                      0 if dq is None else dq.data_ptr())
     else:
-        o = _Out(_bytes(out["codes"], "out codes", R * Cc // per, dev),
-                 _bytes(out["scales"], "out scales", R * Cc // block, dev),
-                 _optional(out.get("choice"), "out choice", words, _I32, dev) if fos else None,
-                 _optional(out.get("dequant"), "out dequant", R * Cc, _BF16, dev) if fp4 else None)
-    tensor = fp4 and global_amax is not None
-    if fp4 and not tensor and row_amax is None:
+        codes, scales, choice, dq = (out["codes"], out["scales"], out.get("choice"),
+                                     out.get("dequant"))
+        o = _OUT.pack(
+            _bytes(codes, "out codes", R * Cc // per, dev),
+            _bytes(scales, "out scales", R * Cc // block, dev),
+            _optional(choice, "out choice", R * ((Cc + 511) // 512), _I32, dev) if fos else 0,
+            _optional(dq, "out dequant", R * Cc, _BF16, dev) if fp4 else 0)
+    amax_at = row_at = 0
+    if not fp4:
+        row_amax = None
+    elif global_amax is not None:
+        amax_at, row_amax = _optional(global_amax, "global_amax", 1, _F32, dev), None
+    elif row_amax is None:
         row_amax = empty(R, dtype=torch.float32, device=device)
-    c = cfg.c()
+        row_at = row_amax.data_ptr()
+    else:
+        row_at = _optional(row_amax, "row_amax", R, _F32, dev)
     code = _lib().nvfp4_add_rms_norm(
-        C.addressof(c), target, *ins, R, Cc, eps, h_at,
-        0 if y is None else _matrix(y, "y", shape, dev),
-        _optional(global_amax, "global_amax", 1, _F32, dev) if tensor else 0,
-        _optional(row_amax, "row_amax", R, _F32, dev) if fp4 and not tensor else 0,
-        C.addressof(o), 0 if status is None else _optional(status, "status", 1, _I32, dev),
-        _stream(dev))
+        _DEFAULT if cfg is None else bytes(cfg.c()), target, x.data_ptr(),
+        0 if residual is None else residual.data_ptr(), weight.data_ptr(), R, Cc, eps, h_at,
+        0 if y is None else _matrix(y, "y", shape, dev), amax_at, row_at, o,
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
     if code:
         _check("nvfp4_add_rms_norm", code)
-    return {"h": h, "y": y, "codes": out["codes"], "scales": out["scales"],
-            "choice": out.get("choice"), "dequant": out.get("dequant"),
-            "row_amax": row_amax if fp4 and not tensor else None}
+    return {"h": h, "y": y, "codes": codes, "scales": scales, "choice": choice, "dequant": dq,
+            "row_amax": row_amax}
 
 
 def add_rms_norm_workspace(device) -> torch.Tensor:
@@ -324,24 +341,25 @@ def nvfp4_add_rms_norm_bwd(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     gradient gh of h: {"gx" (bf16, of x and of the residual), "gw" (fp32 [cols])}.
     workspace: from add_rms_norm_workspace; a fresh one is taken when none is given."""
     dev = h.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _device():
         with torch.cuda.device(dev):
             return nvfp4_add_rms_norm_bwd(gy, h, weight, gh, eps, workspace, gx, status)
-    if h.dim() != 2:
+    shape = h.shape
+    if len(shape) != 2:
         raise ValueError("h must be [rows, cols]")
-    R, Cc = shape = h.shape
+    R, Cc = shape
     ins = (_matrix(gy, "gy", shape, dev), _matrix(h, "h", shape, dev),
            _matrix(weight, "weight", (Cc,), dev),
            0 if gh is None else _matrix(gh, "gh", shape, dev))
     if gx is None:
-        gx = torch.empty(shape, dtype=h.dtype, device=h.device)
+        gx = torch.empty_like(h)
     gw = torch.empty(Cc, dtype=torch.float32, device=h.device)
     if workspace is None:
         workspace = add_rms_norm_workspace(h.device)
     code = _lib().nvfp4_add_rms_norm_bwd(
         *ins, R, Cc, eps, _matrix(gx, "gx", shape, dev), gw.data_ptr(),
         _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel(),
-        0 if status is None else _optional(status, "status", 1, _I32, dev), _stream(dev))
+        0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
     if code:
         _check("nvfp4_add_rms_norm_bwd", code)
     return {"gx": gx, "gw": gw}
