@@ -11,6 +11,7 @@
 // the order of the sum of squares.
 #include "encode.cuh"
 #include "norm.h"
+#include "tcgen05.cuh"
 
 namespace nvfp4 {
 
@@ -214,25 +215,39 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
 }
 
 // Gradient. u = gy w: gx = r (u - h r^2 mean(u h)) + gh, and the weight's gradient is the
-// sum over rows of gy h r. A thread keeps the weight gradients of its values over the
-// CTA's rows; a second kernel adds the CTAs' sums in order.
+// sum over rows of gy h r. Rows come by bulk copies into a ring in shared memory, so that
+// several are on their way whatever the registers hold; a thread keeps the weight gradients
+// of its values over the CTA's rows, and a second kernel adds the CTAs' sums in order.
+constexpr long long kWaitCycles = 2000000000;  // about a second
+constexpr int kMaxDepth = 8;
+constexpr int kRingBwd = 200 * 1024;  // bytes of shared memory for rows on an SM
+
 template <int K>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormBwdParams p) {
-  pdl_begin();
+__global__ void __launch_bounds__(kMaxThreads, K == 1 ? 2 : 1)
+norm_bwd_kernel(const NormBwdParams p, const int depth) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kMaxDepth];
   __shared__ float2 s_sum[2][kMaxThreads / 32];
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int chunks = p.C / 8;
-  auto load_row = [&](int64_t row, uint4 (&gy)[K], uint4 (&h)[K], uint4 (&gh)[K]) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = k * nt + tid;
-      const bool ok = row < p.R && c < chunks;
-      const int64_t at = row * chunks + c;
-      gy[k] = ok ? __ldcs(p.gy + at) : make_uint4(0, 0, 0, 0);
-      h[k] = ok ? __ldcs(p.h + at) : make_uint4(0, 0, 0, 0);
-      if (p.gh) gh[k] = ok ? __ldcs(p.gh + at) : make_uint4(0, 0, 0, 0);
-    }
+  const uint32_t bytes = (uint32_t)p.C * 2;  // of a row of one tensor
+  if (tid == 0) {
+    for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_begin();
+  __syncthreads();
+  auto copy_row = [&](int64_t row, int slot) {  // one thread
+    if (row >= p.R) return;
+    uint8_t* to = ring + (size_t)slot * 3 * bytes;
+    mbar_expect(&full[slot], p.gh ? 3 * bytes : 2 * bytes);
+    const int64_t at = row * chunks;
+    bulk_load(to, p.gy + at, bytes, &full[slot]);
+    bulk_load(to + bytes, p.h + at, bytes, &full[slot]);
+    if (p.gh) bulk_load(to + 2 * bytes, p.gh + at, bytes, &full[slot]);
   };
+  if (tid == 0)
+    for (int i = 0; i < depth; ++i) copy_row(blockIdx.x + (int64_t)i * gridDim.x, i);
   uint4 wt[K];
   f2 gw[K][4];
 #pragma unroll
@@ -242,24 +257,32 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormBwdPara
 #pragma unroll
     for (int j = 0; j < 4; ++j) gw[k][j] = make_float2(0.0f, 0.0f);
   }
-  // Up to two chunks a thread the next row is in flight while this one is worked on; four
-  // (rows of more than 8192 values) would spill.
-  constexpr bool kAhead = K <= 2;
-  uint4 gy[K], h[K], gh[K];
-  if (kAhead) load_row(blockIdx.x, gy, h, gh);
-  int par = 0;
+  int slot = 0, par = 0;
+  uint32_t turn = 0;
+  bool alive = true;
   for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x, par ^= 1) {
-    uint4 cg[K], ch[K], cr[K];
-    if (!kAhead) load_row(row, gy, h, gh);
+    if (alive && !mbar_try(&full[slot], turn)) {
+      const long long t0 = clock64();
+      while (!mbar_try(&full[slot], turn))
+        if (clock64() - t0 > kWaitCycles) {
+          flag(p.status, NVFP4_DEV_TIMEOUT);
+          alive = false;  // nothing is waited for any more; the barriers are still met
+          break;
+        }
+    }
+    const uint4* from = reinterpret_cast<const uint4*>(ring + (size_t)slot * 3 * bytes);
+    uint4 gy[K], h[K], gh[K];
     f2 a2 = make_float2(0.0f, 0.0f), ad = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      cg[k] = gy[k];
-      ch[k] = h[k];
-      cr[k] = gh[k];
+      const int c = k * nt + tid;
+      const bool ok = c < chunks;
+      gy[k] = ok ? from[c] : make_uint4(0, 0, 0, 0);
+      h[k] = ok ? from[chunks + c] : make_uint4(0, 0, 0, 0);
+      gh[k] = ok && p.gh ? from[2 * chunks + c] : make_uint4(0, 0, 0, 0);
       f2 g[4], v[4], w[4];
-      unpack8(cg[k], g);
-      unpack8(ch[k], v);
+      unpack8(gy[k], g);
+      unpack8(h[k], v);
       unpack8(wt[k], w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -267,7 +290,6 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormBwdPara
         ad = f2_fma(f2_mul(g[j], w[j]), v[j], ad);
       }
     }
-    if (kAhead) load_row(row + gridDim.x, gy, h, gh);
     float2 sum = make_float2(__fadd_rn(a2.x, a2.y), __fadd_rn(ad.x, ad.y));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
@@ -275,7 +297,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormBwdPara
       sum.y = __fadd_rn(sum.y, __shfl_xor_sync(kAll, sum.y, d));
     }
     if (lane == 0) s_sum[par][warp] = sum;
-    __syncthreads();
+    __syncthreads();  // sums in; the row is in registers
+    if (tid == 0) copy_row(row + (int64_t)depth * gridDim.x, slot);
+    if (++slot == depth) slot = 0, turn ^= 1;
     sum = s_sum[par][0];
     for (int i = 1; i < warps; ++i) {
       sum.x = __fadd_rn(sum.x, s_sum[par][i].x);
@@ -289,25 +313,25 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormBwdPara
     const f2 r2 = make_float2(r, r), t2 = make_float2(t, t);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      f2 g[4], v[4], w[4], o[4];
-      unpack8(cg[k], g);
-      unpack8(ch[k], v);
+      f2 g[4], v[4], w[4], q[4], o[4];
+      unpack8(gy[k], g);
+      unpack8(h[k], v);
       unpack8(wt[k], w);
+      unpack8(gh[k], q);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f2 n = f2_mul(v[j], r2);
-        gw[k][j] = f2_fma(g[j], n, gw[k][j]);
-        o[j] = f2_fma(n, t2, f2_mul(f2_mul(g[j], w[j]), r2));
-      }
-      if (p.gh) {
-        f2 q[4];
-        unpack8(cr[k], q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = make_float2(__fadd_rn(o[j].x, q[j].x), __fadd_rn(o[j].y, q[j].y));
+        const f2 x = f2_mul(v[j], r2);
+        gw[k][j] = f2_fma(g[j], x, gw[k][j]);
+        o[j] = f2_fma(x, t2, f2_mul(f2_mul(g[j], w[j]), r2));
+        if (p.gh) o[j] = make_float2(__fadd_rn(o[j].x, q[j].x), __fadd_rn(o[j].y, q[j].y));
       }
       const int c = k * nt + tid;
       if (c < chunks) __stcs(p.gx + row * chunks + c, pack8(o));
+    }
+  }
+  if (!alive) {  // copies in flight land before the CTA ends
+    const long long t0 = clock64();
+    while (clock64() - t0 < 20000000) {
     }
   }
 #pragma unroll
@@ -342,10 +366,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) column_sum_kernel(const float*
 
 // CTAs of `kernel` with so many threads on an SM; `fit` keeps the answers by warps.
 template <class Kernel>
-int ctas_per_sm(Kernel kernel, int threads, std::atomic<int>* fit) {
+int ctas_per_sm(Kernel kernel, int threads, std::atomic<int>* fit, size_t smem = 0) {
   int n = fit[threads / 32].load(std::memory_order_relaxed);
   if (n == 0) {
-    n = resident_ctas(kernel, threads);
+    n = resident_ctas(kernel, threads, smem);
     fit[threads / 32].store(n, std::memory_order_relaxed);
   }
   return n;
@@ -369,11 +393,19 @@ cudaError_t sized(const NormParams& p, cudaStream_t st) {
 template <int K>
 cudaError_t run_bwd(const NormBwdParams& p, cudaStream_t st) {
   const int chunks = p.C / 8, threads = ((chunks + K - 1) / K + 31) / 32 * 32;
+  // rows on their way: at least two, and up to 4096 values so many that a thread's share of
+  // shared memory is that of 1024 threads on an SM
+  const int row = 3 * 2 * p.C, room = K == 1 ? kRingBwd / 1024 * threads : kRingBwd;
+  const int depth = std::max(2, std::min(kMaxDepth, room / row));
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(norm_bwd_kernel<K>, kRingBwd, ready);
+  if (e != cudaSuccess) return e;
   static std::atomic<int> fit[kMaxThreads / 32 + 1];
-  const int per_sm = ctas_per_sm(norm_bwd_kernel<K>, threads, fit);
+  const int per_sm = ctas_per_sm(norm_bwd_kernel<K>, threads, fit, (size_t)depth * row);
   const int64_t grid = std::min<int64_t>(
       std::min<int64_t>(p.R, (int64_t)sm_count() * per_sm), std::max<int64_t>(1, kNormPart / p.C));
-  const cudaError_t e = launch_pdl(norm_bwd_kernel<K>, dim3((unsigned)grid), dim3(threads), st, p);
+  e = launch_pdl_smem(norm_bwd_kernel<K>, dim3((unsigned)grid), dim3(threads),
+                      (size_t)depth * row, st, p, depth);
   if (e != cudaSuccess) return e;
   return launch_pdl(column_sum_kernel, dim3((unsigned)((p.C + 31) / 32)), dim3(kSumWarps * 32), st,
                     (const float*)p.part, (int)grid, (int)p.C, p.gw);

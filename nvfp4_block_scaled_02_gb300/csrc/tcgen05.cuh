@@ -247,6 +247,12 @@ __device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
+// So many bytes that follow one another (a multiple of 16, both addresses too).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(b))
+               : "memory");
+}
 // A box of a two-dimensional map, its first value at (x, y), to shared memory.
 __device__ __forceinline__ void tma_load(uint32_t dst, const void* map, int x, int y, uint64_t* b) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
