@@ -348,17 +348,28 @@ def nvfp4_add_rms_norm_bwd(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     if len(shape) != 2:
         raise ValueError("h must be [rows, cols]")
     R, Cc = shape
-    ins = (_matrix(gy, "gy", shape, dev), _matrix(h, "h", shape, dev),
-           _matrix(weight, "weight", (Cc,), dev),
-           0 if gh is None else _matrix(gh, "gh", shape, dev))
+    if not (h.dtype in _BF16 and h.is_contiguous() and dev >= 0 and gy.dtype in _BF16
+            and gy.shape == shape and gy.get_device() == dev and gy.is_contiguous()
+            and weight.dtype in _BF16 and weight.shape == (Cc,) and weight.get_device() == dev
+            and weight.is_contiguous()
+            and (gh is None or (gh.dtype in _BF16 and gh.shape == shape and gh.get_device() == dev
+                                and gh.is_contiguous()))):
+        _matrix(gy, "gy", shape, dev)
+        _matrix(h, "h", shape, dev)
+        _matrix(weight, "weight", (Cc,), dev)
+        _matrix(gh, "gh", shape, dev)
     if gx is None:
         gx = torch.empty_like(h)
+        gx_at = gx.data_ptr()
+    else:
+        gx_at = _matrix(gx, "gx", shape, dev)
     gw = torch.empty(Cc, dtype=torch.float32, device=h.device)
     if workspace is None:
         workspace = add_rms_norm_workspace(h.device)
     code = _lib().nvfp4_add_rms_norm_bwd(
-        *ins, R, Cc, eps, _matrix(gx, "gx", shape, dev), gw.data_ptr(),
-        _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel(),
+        gy.data_ptr(), h.data_ptr(), weight.data_ptr(), 0 if gh is None else gh.data_ptr(), R, Cc,
+        eps, gx_at, gw.data_ptr(), _optional(workspace, "workspace", 1, _I32, dev),
+        4 * workspace.numel(),
         0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
     if code:
         _check("nvfp4_add_rms_norm_bwd", code)
