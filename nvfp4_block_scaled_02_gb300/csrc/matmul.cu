@@ -39,6 +39,12 @@ __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile
   return true;
 }
 
+// The barrier's phase counts one arrival when this thread's copies so far are done.
+__device__ __forceinline__ void copies_arrive(uint64_t* b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(b))
+               : "memory");
+}
+
 // 16 bytes at q (16-byte aligned); those at `end` and after it are 0 and not read.
 __device__ __forceinline__ uint4 bytes16(const uint8_t* q, const uint8_t* end) {
   if (q + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(q));
@@ -112,7 +118,8 @@ struct Geometry {
 };
 // total tiles of at most `most` columns, for so many CTAs or pairs of CTAs
 template <int KIND, int CG>
-__host__ __device__ __forceinline__ Geometry geometry(int total, int most, int pairs) {
+__host__ __device__ __forceinline__ Geometry geometry(int total, int most, int pairs,
+                                                      bool aligned) {
   Geometry g;
   g.split = 1;
   if (total > 0 && 2 * total <= pairs) {
@@ -122,7 +129,9 @@ __host__ __device__ __forceinline__ Geometry geometry(int total, int most, int p
   g.items = total * g.split;
   g.c_blocks = (most + 127) / 128;
   g.sf_at = kFBytes + Boxes(((most + 15) & ~15) / CG).rows() * kStageRow;
-  g.stage_bytes = (g.sf_at + (1 + g.c_blocks) * Kind<KIND>::kSfBlock + 1023) & ~1023;
+  // (NVFP4 scales that are not aligned come as two aligned pieces)
+  const int sf = (1 + g.c_blocks) * Kind<KIND>::kSfBlock * (Kind<KIND>::kFp4 && !aligned ? 2 : 1);
+  g.stage_bytes = (g.sf_at + sf + 1023) & ~1023;
   g.stages = (int)((uint32_t)kRing / (uint32_t)g.stage_bytes);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   return g;
@@ -205,15 +214,14 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
   const int64_t rows_all = T::kWgrad ? p.K : p.c_rows;
   const bool scan = !T::kWgrad && p.start;  // the tiles are known on the device only
 
-  // NVFP4 rows whose scales are aligned: a stage's 16 bytes of a row are copied to their stage
-  // and turned there into the layout of tensor memory
-  const bool in_place = T::kFp4 && p.sf_stride % 16 == 0;
+  // Whether 16 scale bytes of a row are aligned in memory.
+  const bool sf_aligned = p.sf_stride % 16 == 0;
   // What does not depend on earlier kernels, while they end.
   if (warp == 0) {
     if (lane < kMaxStages) {
-      mbar_init(&s.full[lane], 1 + CG * (in_place ? kScaleWarps / 2 : kScaleWarps));
+      mbar_init(&s.full[lane], 1 + CG * (T::kFp4 ? kScaleWarps / 2 : kScaleWarps));
       mbar_init(&s.empty[lane], 1);
-      for (int b = 0; b < 3; ++b) mbar_init(&s.raw[b][lane], 1);
+      for (int b = 0; b < 3; ++b) mbar_init(&s.raw[b][lane], sf_aligned ? 1 : 32);
     } else if (lane == kMaxStages) {
       s.dead = 0;
       mbar_init(&s.acc_full, 1);
@@ -221,7 +229,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       mbar_init(&s.end, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  } else if (warp == kCopyWarp && lane < (in_place ? 6 : 3)) {
+  } else if (warp == kCopyWarp && lane < (T::kFp4 && sf_aligned ? 6 : 3)) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const CUtensorMap*>(&maps) + lane)
                  : "memory");
   } else if (warp == kMmaWarp) {
@@ -235,7 +243,6 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
   // ---- the groups' tiles -----------------------------------------------------
   // Ragged rows: a thread to `share` groups, then a scan over the threads. Otherwise the
   // host knows the tiles.
-  const bool sf_aligned = p.sf_stride % 16 == 0;
   int before = 0, mine = 0;
   const int share = (p.E + kThreads - 1) / kThreads;
   const int e0 = min(tid * share, p.E), e1 = min(e0 + share, p.E);
@@ -278,7 +285,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     for (int e = e0; e < e1; ++e) s.tile[e] += before;
     if (tid == 0) {
       s.tile[p.E] = total;
-      s.geo = geometry<KIND, CG>(total, most, pairs);
+      s.geo = geometry<KIND, CG>(total, most, pairs, sf_aligned);
     }
     __syncthreads();
   }
@@ -636,7 +643,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       }
     }
     __syncwarp();
-  } else if (in_place && warp == kScaleWarp) {
+  } else if (T::kFp4 && sf_aligned && warp == kScaleWarp) {
     // ==== scales: copies, a lane to 128 rows ======================================
     Place pl;
     bool ok = true;
@@ -665,11 +672,66 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       }
     }
     if (!ok) land();
-  } else if (in_place && warp < kScaleWarp + 3) {
-    // (two warps without work)
-  } else if (in_place) {
+  } else if (T::kFp4 && warp < kScaleWarp + 3) {
+    // ==== scales that are not aligned: copies, a warp to 128 rows ====================
+    // The two aligned pieces that hold a stage's 16 bytes of a row, two stages at a time (a
+    // warp's copy then finds 32 bytes of 16 rows side by side).
+    const int block = warp - kScaleWarp;  // 0 features, 1 and 2 columns
+    const uint8_t* base = block == 0 ? p.f_sf : p.c_sf;
+    const int64_t rows = block == 0 ? p.f_rows : p.c_rows;
+    const uint8_t* end = base + rows * p.sf_stride;
+    const int piece = lane & 1;
+    Place pl;
+    bool ok = true;
+    int item = pair;
+    Work ahead;
+    bool more = !sf_aligned && block <= c_blocks && seek(item, ahead);
+    while (ok && more) {
+      const Work w = ahead;
+      const int64_t row0 = (int64_t)(block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) +
+                           (lane >> 1);
+      const bool any = block == 0 || 128 * (block - 1) < w.cols;
+      more = false;
+      for (int k = w.k0; k < w.k1; k += 2) {
+        const bool both = k + 1 < w.k1;
+        Place next = pl;
+        next.next(stages);
+        ok = wait_warp(&s.empty[pl.st], pl.turn ^ 1) &&
+             (!both || wait_warp(&s.empty[next.st], next.turn ^ 1));
+        if (!ok) break;
+        if (piece == 0 || both) {
+          const int at = (k + piece) * T::kStageSf, valid = min(T::kStageSf, (int)p.sf_stride - at);
+          uint8_t* dst = ring + (piece ? next.st : pl.st) * stage_bytes + sf_at +
+                         block * T::kSfBlock + (lane >> 1) * 16;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool in = any && row0 + 16 * i < rows;
+            const uint8_t* q = in ? base + (row0 + 16 * i) * p.sf_stride + at : base;
+            const int off = (int)((uintptr_t)q & 15);
+            q -= off;
+            // (nothing is read at the array's end or after it)
+            const int lo = in ? (int)min((int64_t)16, (int64_t)(end - q)) : 0;
+            const int hi = in && off + valid > 16 ? (int)min((int64_t)16, (int64_t)(end - q) - 16) : 0;
+            cp_async16_zfill(dst + 256 * i, q, lo);
+            cp_async16_zfill(dst + (1 + c_blocks) * T::kSfBlock + 256 * i, hi > 0 ? q + 16 : base,
+                             hi);
+          }
+        }
+        copies_arrive(&s.raw[block][pl.st]);
+        if (both) {
+          copies_arrive(&s.raw[block][next.st]);
+          pl = next;
+        }
+        pl.next(stages);
+        if (k == w.k0) more = seek(item += pairs, ahead);
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (T::kFp4) {
     // ==== scales: lane l turns rows l, l + 32, l + 64, l + 96 ======================
     const int block = warp - kScaleWarp - 3;
+    const uint32_t base = (uint32_t)(uintptr_t)(block == 0 ? p.f_sf : p.c_sf);
     Place pl;
     bool ok = true;
     int item = pair;
@@ -678,17 +740,27 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     while (ok && more) {
       const Work w = ahead;
       more = false;
+      // where a row's bytes begin in its first piece
+      const uint32_t row = (uint32_t)(block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + lane;
+      const uint32_t stride = (uint32_t)p.sf_stride, off = base + row * stride;
       for (int k = w.k0; k < w.k1; ++k, pl.next(stages)) {
         const int st = pl.st;
         if (block <= c_blocks) {
           if (!(ok = wait_warp(&s.raw[block][st], pl.turn))) break;
           uint4* at = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
                                                block * T::kSfBlock) + lane;
-          const uint4 a = at[0], b = at[32], c = at[64], d = at[96];
-          at[0] = make_uint4(a.x, b.x, c.x, d.x);
-          at[32] = make_uint4(a.y, b.y, c.y, d.y);
-          at[64] = make_uint4(a.z, b.z, c.z, d.z);
-          at[96] = make_uint4(a.w, b.w, c.w, d.w);
+          uint4 v[4] = {at[0], at[32], at[64], at[96]};
+          if (!sf_aligned) {
+            const uint4* hi = at + (1 + c_blocks) * T::kSfBlock / 16;
+            const int valid = min(T::kStageSf, (int)p.sf_stride - k * T::kStageSf);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[i] = first_bytes(window16(v[i], hi[32 * i], (off + 32 * i * stride) & 15), valid);
+          }
+          at[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+          at[32] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+          at[64] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+          at[96] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
           fence_smem_async();
         } else if (!(ok = wait_warp(&s.empty[st], pl.turn ^ 1))) {
           break;
@@ -811,15 +883,10 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       ring_of<kAhead>(fetch, store);
     };
     constexpr std::integral_constant<int, 2> two{};
-    if constexpr (!T::kFp4) {
-      if (sf_aligned) {
-        feed(std::true_type{}, std::integral_constant<int, 3>{}, two);
-      } else {
-        feed(std::false_type{}, two, two);
-      }
-    } else {
+    if (sf_aligned)
+      feed(std::true_type{}, std::integral_constant<int, 3>{}, two);
+    else
       feed(std::false_type{}, two, two);
-    }
   }
   __syncwarp();
   fence_before();
@@ -889,7 +956,7 @@ cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   q.by_tiles = make_fastdiv((uint32_t)std::max(q.tiles, 1));
   const Geometry geo = geometry<KIND, CG>(q.tiles * (KIND == kMatmulMxWgrad ? p.E : 1),
                                           (cols + c_tiles - 1) / std::max(c_tiles, 1),
-                                          (int)lc.gridDim.x / CG);
+                                          (int)lc.gridDim.x / CG, p.sf_stride % 16 == 0);
   return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, m, q, geo);
 }
 template <int KIND>
