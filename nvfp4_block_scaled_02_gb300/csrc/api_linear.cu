@@ -27,9 +27,11 @@ nvfp4_status check_ws(const void* workspace, size_t ws_bytes) {
   return aligned(workspace, 16) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 void fill_ws(nvfp4::MatmulParams& p, void* workspace) {
-  p.tickets = static_cast<uint32_t*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                    (size_t)4 * 2 * nvfp4::kMatmulMaxCtas);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  p.tickets = reinterpret_cast<uint32_t*>(at);
+  at += nvfp4::kMatmulTicketBytes;
+  p.part = reinterpret_cast<float*>(at);
+  p.padded = at + (size_t)4 * nvfp4::kMatmulMaxCtas * nvfp4::kMatmulPart;
 }
 
 // What the two products over ragged rows have in common.

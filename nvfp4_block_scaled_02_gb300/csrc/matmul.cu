@@ -23,6 +23,7 @@ constexpr int kSmem = kRing + 1024;            // and its alignment
 constexpr int kAcc1 = 192, kScales = 448;
 constexpr int kBand = 8;                       // column tiles of a band
 constexpr int kPairCols = 96;                  // columns of a group from which pairs of CTAs pay
+constexpr double kPadGain = 0.3;               // see launch_matmul
 constexpr long long kWaitCycles = 2000000000;  // about a second
 
 __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* dead,
@@ -902,6 +903,30 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
   }
 }
 
+// Scales in rows of `stride` bytes, copied to rows of `wide` (a multiple of 16), zeros behind a
+// row's bytes. A thread to 16 bytes; two arrays, one after the other.
+constexpr int kPadThreads = 256;
+__global__ void __launch_bounds__(kPadThreads) pad_scales_kernel(
+    const uint8_t* a, int64_t a_rows, const uint8_t* b, int64_t b_rows, int stride, int units,
+    FastDiv by_units, uint8_t* out) {
+  pdl_begin();
+  const int64_t n = (a_rows + b_rows) * units;
+  for (int64_t i = (int64_t)blockIdx.x * kPadThreads + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * kPadThreads) {
+    const int64_t row = fastdiv((uint32_t)i, by_units);
+    const int at = 16 * (int)(i - row * units), valid = min(16, stride - at);
+    const bool first = row < a_rows;
+    const uint8_t* base = first ? a : b;
+    const uint8_t* end = base + (first ? a_rows : b_rows) * stride;
+    const uint8_t* q = base + (first ? row : row - a_rows) * stride + at;
+    const uint32_t off = (uint32_t)((uintptr_t)q & 15);
+    q -= off;
+    const uint4 lo = bytes16(q, end);
+    const uint4 hi = off + valid > 16 ? bytes16(q + 16, end) : make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(out)[i] = first_bytes(window16(lo, hi, off), valid);
+  }
+}
+
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
 
 // The driver's function that makes tensor maps (the library links the runtime alone).
@@ -968,8 +993,35 @@ cudaError_t launch_k(const MatmulParams& p, const Maps& m, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_matmul(int kind, const MatmulParams& p, const uint8_t* f_codes,
+cudaError_t launch_matmul(int kind, const MatmulParams& given, const uint8_t* f_codes,
                           const uint8_t* c_codes, cudaStream_t st) {
+  MatmulParams p = given;
+  // Rows of scales that are not whole 16 bytes take the kernel longer, a stage by about kPadGain
+  // microseconds; copying them first takes a launch and their bytes twice.
+  const int64_t units = (p.sf_stride + 15) / 16, padded = 16 * units;
+  if (p.sf_stride % 16 != 0 && (p.f_rows + p.c_rows) * padded <= (int64_t)kMatmulPadBytes) {
+    const bool wgrad = kind == kMatmulMxWgrad;
+    const int64_t c_tiles = wgrad ? p.E * (((int64_t)p.C + kTileC - 1) / kTileC)
+                                  : p.c_rows / kTileC + std::min<int64_t>(p.E, p.c_rows);
+    const int64_t stage = kind == kMatmulNvfp4 ? 256 : 128;
+    const int64_t stages = c_tiles * ((p.N + kTileF - 1) / kTileF) *
+                           (wgrad ? (p.K / p.E + stage - 1) / stage : (p.K + stage - 1) / stage);
+    const double here = (double)stages / sm_count() * kPadGain;
+    const double copy = 3.0 + 2e-6 * (double)((p.f_rows + p.c_rows) * padded) / 3.0;
+    if (here > copy) {
+      const int64_t n = (p.f_rows + p.c_rows) * units;
+      const int64_t ctas = std::min<int64_t>((n + kPadThreads - 1) / kPadThreads,
+                                             (int64_t)sm_count() * 8);
+      const cudaError_t e =
+          launch_pdl(pad_scales_kernel, dim3((unsigned)ctas), dim3(kPadThreads), st, p.f_sf,
+                     p.f_rows, p.c_sf, p.c_rows, (int)p.sf_stride, (int)units,
+                     make_fastdiv((uint32_t)units), p.padded);
+      if (e != cudaSuccess) return e;
+      p.f_sf = p.padded;
+      p.c_sf = p.padded + p.f_rows * padded;
+      p.sf_stride = padded;
+    }
+  }
   Maps m{};
   const int64_t bytes = kind == kMatmulNvfp4 ? p.K / 2 : p.K;
   // without rows to sum over no copy is made: a weights' gradient of zeros

@@ -27,6 +27,7 @@ struct MatmulParams {
   int32_t out_f32;
   uint32_t* tickets;
   float* part;
+  uint8_t* padded;              // kMatmulPadBytes
   int32_t* status;
 };
 
@@ -35,8 +36,10 @@ enum { kMatmulNvfp4 = 0, kMatmulMx = 1, kMatmulMxWgrad = 2 };
 constexpr int kMatmulMaxGroups = 1024;
 constexpr int kMatmulMaxCtas = 192;
 constexpr int kMatmulPart = 256 * 128;  // floats of a partial result
+constexpr size_t kMatmulPadBytes = (size_t)64 << 20;  // scales in rows of whole 16 bytes
+constexpr size_t kMatmulTicketBytes = (size_t)4 * 2 * kMatmulMaxCtas;
 constexpr size_t kMatmulWsBytes =
-    (size_t)4 * 2 * kMatmulMaxCtas + (size_t)4 * kMatmulMaxCtas * kMatmulPart;
+    kMatmulTicketBytes + (size_t)4 * kMatmulMaxCtas * kMatmulPart + kMatmulPadBytes;
 
 cudaError_t launch_matmul(int kind, const MatmulParams& p, const uint8_t* f_codes,
                           const uint8_t* c_codes, cudaStream_t st);

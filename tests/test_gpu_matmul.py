@@ -46,7 +46,9 @@ def check_rows(out, before, a, b, start):
 SIZES = [(1, 1, 1, 32), (1, 1, 128, 256), (1, 16, 128, 512), (1, 5, 130, 96), (1, 128, 256, 1024),
          (1, 256, 128, 256), (1, 257, 256, 288), (3, 300, 200, 544), (5, 700, 1000, 416),
          (7, 40, 77, 160), (1, 33, 64, 7168), (1, 300, 128, 4096), (64, 90, 2048, 1024),
-         (2, 3000, 1536, 320), (1, 2000, 4096, 512), (300, 900, 136, 64)]
+         (2, 3000, 1536, 320), (1, 2000, 4096, 512), (300, 900, 136, 64),
+         # rows of scales that are not whole 16 bytes, in sums long enough to be copied first
+         (4, 3000, 1536, 7136), (24, 200, 1500, 7136)]
 
 
 @pytest.mark.parametrize("E,T,N,K", SIZES)
@@ -91,7 +93,8 @@ def test_mx_product(ws, E, T, N, K):
 
 @pytest.mark.parametrize("E,T,N,K", [(1, 32, 1, 1), (1, 64, 130, 77), (1, 128, 256, 128),
                                      (3, 320, 200, 100), (4, 960, 1000, 544), (1, 4096, 128, 128),
-                                     (16, 4096, 512, 300), (40, 640, 33, 64), (2, 32, 300, 256)])
+                                     (16, 4096, 512, 300), (40, 640, 33, 64), (2, 32, 300, 256),
+                                     (2, 8160, 2048, 2000)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_mx_weight_gradient(ws, E, T, N, K, dtype):
     rng = np.random.default_rng(E + T + N + K)
