@@ -197,7 +197,7 @@ struct Shared {
   int scan[kThreads / 32], most[kThreads / 32];
   Geometry geo;
   int tile[kMatmulMaxGroups + 1];  // a group's first tile
-  float scale[2][kTileC];          // outer scales of a tile's columns
+  alignas(16) float scale[2][kTileC];  // outer scales of a tile's columns
 };
 
 template <int KIND, int CG>
@@ -407,11 +407,13 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         const SliceScale f = slice_scale(p.f_amax[w.g], p.f_M);
         gf = f.g;
         bool bad = f.bad;
+        float gc = 0.0f;
         if (tid < w.cols) {
           const SliceScale c = slice_scale(p.c_amax[p.c_amax_each ? w.c_row + tid : 0], p.c_M);
-          sc[tid] = c.g;
+          gc = c.g;
           bad = bad || c.bad;
         }
+        sc[tid] = gc;
         if (bad) flag(p.status, NVFP4_DEV_BAD_AMAX);
         asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
       }
@@ -430,8 +432,13 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         constexpr int kN = sizeof(v) / sizeof(float);
         if constexpr (T::kFp4) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i)
-            v[i] = __fmul_rn(__fmul_rn(v[i], sc[c + i < w.cols ? c + i : 0]), gf);
+          for (int i = 0; i < kN; i += 4) {
+            const float4 g = *reinterpret_cast<const float4*>(sc + c + i);
+            v[i] = __fmul_rn(__fmul_rn(v[i], g.x), gf);
+            v[i + 1] = __fmul_rn(__fmul_rn(v[i + 1], g.y), gf);
+            v[i + 2] = __fmul_rn(__fmul_rn(v[i + 2], g.z), gf);
+            v[i + 3] = __fmul_rn(__fmul_rn(v[i + 3], g.w), gf);
+          }
         }
         const int64_t row0 = T::kWgrad ? (int64_t)w.g * p.C + w.c0 : (int64_t)w.c_row;
         // every lane has a feature, every column is there: no checks

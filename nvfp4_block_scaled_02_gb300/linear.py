@@ -92,21 +92,18 @@ def _starts(start: torch.Tensor | None, groups: int, dev: int) -> int:
     return _typed(start, "group_start", (groups + 1,), torch.int32, dev)
 
 
-def _result(out, shape, dtypes, device, dev: int):
-    if out is None:
-        out = torch.empty(shape, dtype=dtypes[0], device=device)
-        return out, out.data_ptr()
-    if out.dtype not in dtypes or out.shape != shape or out.get_device() != dev or (
-            not out.is_contiguous()):
-        _refuse(out, "out", shape, dtypes, dev)
-    return out, out.data_ptr()
+def _result(out, shape, dtypes, dev: int) -> int:
+    if out.dtype in dtypes and out.shape == shape and out.get_device() == dev and (
+            out.is_contiguous()):
+        return out.data_ptr()
+    return _refuse(out, "out", shape, dtypes, dev)
 
 
-def _ws(workspace, device, dev: int):
-    """The workspace (which has to outlive the call's enqueuing), its address and bytes."""
-    if workspace is None:
-        workspace = grouped_matmul_workspace(device)
-    return workspace, _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel()
+def _encoded(codes, scales, n: int, m: int, dev: int) -> bool:
+    """Whether codes and scales are byte arrays of n and m elements on the device."""
+    return (codes.dtype in _U8 and scales.dtype in _U8 and codes.numel() == n
+            and scales.numel() == m and codes.get_device() == dev == scales.get_device()
+            and dev >= 0 and codes.is_contiguous() and scales.is_contiguous())
 
 
 def _outer_max(cfg: Config | None, name: str) -> float:
@@ -136,6 +133,7 @@ def nvfp4_grouped_matmul(a: dict, a_amax: torch.Tensor, b: dict, b_amax: torch.T
         with torch.cuda.device(dev):
             return nvfp4_grouped_matmul(a, a_amax, b, b_amax, group_start, a_cfg, b_cfg, out,
                                         workspace, status)
+    asc, bsc = a["scales"], b["scales"]
     T, half = _rows_of(ac, "a codes")
     E, N, bhalf = _groups_of(bc, "b codes")
     if half != bhalf:
@@ -143,17 +141,34 @@ def nvfp4_grouped_matmul(a: dict, a_amax: torch.Tensor, b: dict, b_amax: torch.T
     n = a_amax.numel()
     if n != 1 and n != T:
         raise ValueError(f"a_amax holds {n} elements; the call needs 1 or {T}")
-    pa = _OPERAND.pack(_bytes(ac, "a codes", T * half, dev),
-                       _bytes(a["scales"], "a scales", T * half // 8, dev),
-                       _optional(a_amax, "a_amax", n, _F32, dev), n, _outer_max(a_cfg, "a_cfg"))
     if b_amax.numel() != E:
         raise ValueError(f"b_amax holds {b_amax.numel()} elements; the call needs {E}")
-    pb = _OPERAND.pack(_bytes(bc, "b codes", E * N * half, dev),
-                       _bytes(b["scales"], "b scales", E * N * half // 8, dev),
-                       _optional(b_amax, "b_amax", E, _F32, dev), E, _outer_max(b_cfg, "b_cfg"))
+    f32 = torch.float32
+    # one expression for what is usual; what is wrong is looked up only if it fails
+    if not (_encoded(ac, asc, T * half, T * half // 8, dev)
+            and _encoded(bc, bsc, E * N * half, E * N * half // 8, dev)
+            and a_amax.dtype is f32 and b_amax.dtype is f32
+            and a_amax.get_device() == dev == b_amax.get_device()
+            and a_amax.is_contiguous() and b_amax.is_contiguous()):
+        _bytes(ac, "a codes", T * half, dev)
+        _bytes(asc, "a scales", T * half // 8, dev)
+        _bytes(bc, "b codes", E * N * half, dev)
+        _bytes(bsc, "b scales", E * N * half // 8, dev)
+        _optional(a_amax, "a_amax", n, _F32, dev)
+        _optional(b_amax, "b_amax", E, _F32, dev)
+    pa = _OPERAND.pack(ac.data_ptr(), asc.data_ptr(), a_amax.data_ptr(), n,
+                       0.0 if a_cfg is None else _outer_max(a_cfg, "a_cfg"))
+    pb = _OPERAND.pack(bc.data_ptr(), bsc.data_ptr(), b_amax.data_ptr(), E,
+                       0.0 if b_cfg is None else _outer_max(b_cfg, "b_cfg"))
     start = _starts(group_start, E, dev)
-    out, to = _result(out, (T, N), _BF16, ac.device, dev)
-    workspace, ws, ws_bytes = _ws(workspace, ac.device, dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=ac.device)
+        to = out.data_ptr()
+    else:
+        to = _result(out, (T, N), _BF16, dev)
+    if workspace is None:
+        workspace = grouped_matmul_workspace(ac.device)
+    ws, ws_bytes = _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel()
     code = _lib().nvfp4_grouped_matmul(
         pa, pb, T, E, N, 2 * half, start, to, ws, ws_bytes,
         0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
@@ -178,12 +193,23 @@ def nvfp4_mx_grouped_matmul(a: dict, b: dict, group_start: torch.Tensor | None =
     E, N, bk = _groups_of(bc, "b codes")
     if K != bk:
         raise ValueError(f"a has rows of {K} values, b of {bk}")
-    ins = (_bytes(ac, "a codes", T * K, dev), _bytes(a["scales"], "a scales", T * K // 32, dev),
-           _bytes(bc, "b codes", E * N * K, dev),
-           _bytes(b["scales"], "b scales", E * N * K // 32, dev))
+    asc, bsc = a["scales"], b["scales"]
+    if not (_encoded(ac, asc, T * K, T * K // 32, dev)
+            and _encoded(bc, bsc, E * N * K, E * N * K // 32, dev)):
+        _bytes(ac, "a codes", T * K, dev)
+        _bytes(asc, "a scales", T * K // 32, dev)
+        _bytes(bc, "b codes", E * N * K, dev)
+        _bytes(bsc, "b scales", E * N * K // 32, dev)
+    ins = (ac.data_ptr(), asc.data_ptr(), bc.data_ptr(), bsc.data_ptr())
     start = _starts(group_start, E, dev)
-    out, to = _result(out, (T, N), _BF16, ac.device, dev)
-    workspace, ws, ws_bytes = _ws(workspace, ac.device, dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=ac.device)
+        to = out.data_ptr()
+    else:
+        to = _result(out, (T, N), _BF16, dev)
+    if workspace is None:
+        workspace = grouped_matmul_workspace(ac.device)
+    ws, ws_bytes = _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel()
     code = _lib().nvfp4_mx_grouped_matmul(
         *ins, T, E, N, K, start, to, ws, ws_bytes,
         0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
@@ -216,14 +242,25 @@ def nvfp4_mx_grouped_wgrad(g: dict, x: dict, group_start: torch.Tensor | None = 
     E = 1 if group_start is None else group_start.numel() - 1
     if E < 0:
         raise ValueError("group_start must hold groups + 1 entries")
-    ins = (_bytes(gc, "g codes", N * T, dev), _bytes(g["scales"], "g scales", N * T // 32, dev),
-           _bytes(xc, "x codes", K * T, dev), _bytes(x["scales"], "x scales", K * T // 32, dev))
+    gsc, xsc = g["scales"], x["scales"]
+    if not (_encoded(gc, gsc, N * T, N * T // 32, dev)
+            and _encoded(xc, xsc, K * T, K * T // 32, dev)):
+        _bytes(gc, "g codes", N * T, dev)
+        _bytes(gsc, "g scales", N * T // 32, dev)
+        _bytes(xc, "x codes", K * T, dev)
+        _bytes(xsc, "x scales", K * T // 32, dev)
+    ins = (gc.data_ptr(), gsc.data_ptr(), xc.data_ptr(), xsc.data_ptr())
     start = _starts(group_start, E, dev)
-    if out is not None:
-        out_dtype = torch.float32 if out.dtype is torch.float32 else torch.bfloat16
-    f32 = out_dtype is torch.float32
-    out, to = _result(out, (E, N, K), _F32 if f32 else _BF16, gc.device, dev)
-    workspace, ws, ws_bytes = _ws(workspace, gc.device, dev)
+    if out is None:
+        f32 = out_dtype is torch.float32
+        out = torch.empty((E, N, K), dtype=out_dtype, device=gc.device)
+        to = out.data_ptr()
+    else:
+        f32 = out.dtype is torch.float32
+        to = _result(out, (E, N, K), _F32 if f32 else _BF16, dev)
+    if workspace is None:
+        workspace = grouped_matmul_workspace(gc.device)
+    ws, ws_bytes = _optional(workspace, "workspace", 1, _I32, dev), 4 * workspace.numel()
     code = _lib().nvfp4_mx_grouped_wgrad(
         *ins, T, E, N, K, start, to, f32, ws, ws_bytes,
         0 if status is None else _optional(status, "status", 1, _I32, dev), _raw_stream(dev))
