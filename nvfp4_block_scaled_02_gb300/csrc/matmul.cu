@@ -146,8 +146,10 @@ struct Work {
   int k_at;                 // first value of the sum
   int first, steps;         // the sum's first product and the end of its products
   int k0, k1;
-  int tile, part, parts;
+  int item, tile, part, parts;  // part -1: no more work
 };
+constexpr int kWorks = 8;       // pieces of work handed out ahead
+constexpr int kTakers = kEpilogueWarps + 1 + kScaleWarps;
 
 // Fills N slots, then empties and refills them in turn until emptying one fails.
 template <int N, int I = 0, class Fetch>
@@ -191,14 +193,25 @@ struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t raw[3][kMaxStages];     // scales of 128 rows as they lie in memory
   uint64_t acc_full, acc_free, end;
+  uint64_t work_full[kWorks], work_free[kWorks];
   uint32_t tmem;
   volatile int dead;
   int last;
   int scan[kThreads / 32], most[kThreads / 32];
   Geometry geo;
+  Work work[kWorks];
   int tile[kMatmulMaxGroups + 1];  // a group's first tile
   alignas(16) float scale[2][kTileC];  // outer scales of a tile's columns
 };
+
+// The epilogue warps' barrier; whether all of them said yes.
+__device__ __forceinline__ bool all_of(bool yes) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+               "barrier.cta.red.and.pred.aligned q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((uint32_t)yes), "n"(kEpilogueWarps * 32) : "memory");
+  return r != 0;
+}
 
 template <int KIND, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -228,6 +241,9 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       mbar_init(&s.acc_full, 1);
       mbar_init(&s.acc_free, CG * kEpilogueWarps);
       mbar_init(&s.end, 1);
+    } else if (lane - kMaxStages <= kWorks) {
+      mbar_init(&s.work_full[lane - kMaxStages - 1], 1);
+      mbar_init(&s.work_free[lane - kMaxStages - 1], kTakers);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (warp == kCopyWarp && lane < (T::kFp4 && sf_aligned ? 6 : 3)) {
@@ -298,7 +314,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
   // 32-bit unsigned divisions only, and none where there is one of a kind: what a call
   // that fits the SMs once pays before its first copy.
   auto work_of = [&](int item, Work& w) -> bool {
-    w.tile = item;
+    w.item = w.tile = item;
     w.part = 0;
     if (split > 1) {
       w.tile = (int)((uint32_t)item / (uint32_t)split);
@@ -367,13 +383,6 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     }
     return w.part < w.parts && w.cols > 0;
   };
-  // The pair's next piece of work from `item` on; false at the end. Finding one takes some
-  // hundred clocks: where a warp feeds the ring it looks ahead while the ring is full.
-  auto seek = [&](int& item, Work& w) -> bool {
-    for (; item < items; item += pairs)
-      if (work_of(item, w)) return true;
-    return false;
-  };
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
     return mbar_try(b, parity) || wait_long(b, parity, &s.dead, p.status);
   };
@@ -381,6 +390,16 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     return __all_sync(kAll, wait(b, parity));
   };
 
+  // A warp's next piece of work, as the copying warp handed it out; false at the end.
+  auto take = [&](uint32_t& n, Work& w) -> bool {
+    const uint32_t slot = n % kWorks;
+    if (!wait_warp(&s.work_full[slot], (n / kWorks) & 1)) return false;
+    w = s.work[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.work_free[slot]);
+    ++n;
+    return w.part >= 0;
+  };
   // Given up: copies in flight land before the CTA ends (milliseconds are many times enough).
   auto land = [&]() {
     const long long t0 = clock64();
@@ -397,13 +416,14 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     // ==== results ==============================================================
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t acc_lane = tmem + ((uint32_t)quarter << 21);
+    uint32_t taken = 0;
     int done = 0, tiles = 0;
-    for (int item = pair; item < items; item += pairs) {
+    for (;;) {
       Work w;
-      if (!work_of(item, w)) continue;
+      bool go = take(taken, w);
       float* sc = s.scale[tiles++ & 1];
       float gf = 1.0f;
-      if constexpr (T::kFp4) {
+      if (T::kFp4 && go) {
         const SliceScale f = slice_scale(p.f_amax[w.g], p.f_M);
         gf = f.g;
         bool bad = f.bad;
@@ -415,8 +435,9 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         }
         sc[tid] = gc;
         if (bad) flag(p.status, NVFP4_DEV_BAD_AMAX);
-        asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
       }
+      // the columns' scales are there, and the warps go on or end together
+      if (!all_of(go)) break;
       const bool sum = w.k1 > w.k0;  // false: a sum over nothing
       const int buf = done & 1;
       if (sum) {
@@ -426,7 +447,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       }
       const uint32_t acc = acc_lane + (buf ? kAcc1 : 0);
       const int f = w.f0 + quarter * 32 + lane;
-      float* part = p.part + ((int64_t)item * CG + rank) * kMatmulPart + quarter * 32 + lane;
+      float* part = p.part + ((int64_t)w.item * CG + rank) * kMatmulPart + quarter * 32 + lane;
       // the results of columns c .. c + n - 1, for the lane's feature
       auto put = [&](int c, auto& v) {
         constexpr int kN = sizeof(v) / sizeof(float);
@@ -537,15 +558,36 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       }
     }
   } else if (warp == kCopyWarp) {
-    // ==== codes: one lane to a box ==============================================
+    // ==== codes: one lane to a box; pieces of work for all warps =====================
     Place pl;
-    bool ok = true;
+    bool ok = true, ended = false;
     int item = pair;
-    Work ahead;
-    bool more = seek(item, ahead);
-    while (ok && more) {
-      const Work w = ahead;
-      more = false;
+    uint32_t given = 0, at = 0;  // pieces handed out, and which of them is copied now
+    // Finding a piece takes some hundred clocks: it is done between copies, while the ring is
+    // full, and never by a warp that others wait for.
+    auto give = [&](bool now) {
+      if (ended || given >= at + kWorks) return;
+      const uint32_t slot = given % kWorks, parity = ((given / kWorks) & 1) ^ 1;
+      if (now) {
+        if (!(ok = wait_warp(&s.work_free[slot], parity))) return;
+      } else if (!__all_sync(kAll, mbar_test(&s.work_free[slot], parity))) {
+        return;
+      }
+      Work x;
+      for (ended = true; ended && item < items; item += pairs) ended = !work_of(item, x);
+      if (ended) x.part = -1;
+      if (lane == 0) {
+        s.work[slot] = x;
+        mbar_arrive(&s.work_full[slot]);
+      }
+      __syncwarp();
+      ++given;
+    };
+    for (; ok; ++at) {
+      if (at == given) give(true);
+      if (!ok) break;
+      const Work w = s.work[at % kWorks];
+      if (w.part < 0) break;
       const int held = ((w.cols + 15) & ~15) / CG;  // columns of this CTA
       const Boxes boxes(held);
       const uint32_t bytes = kFBytes + boxes.rows() * kStageRow;
@@ -574,26 +616,18 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
           __syncwarp();
           if (lane < boxes.count) tma_load(c_dst, c_box, x, c_row, &s.full[st]);
         }
-        if (k == w.k0) more = seek(item += pairs, ahead);
+        give(false);
       }
-      if (w.k1 <= w.k0) more = seek(item += pairs, ahead);
     }
     if (!ok) land();
   } else if (warp == kMmaWarp) {
     // ==== products ==============================================================
-    uint32_t tiles = 0;
+    uint32_t tiles = 0, taken = 0;
     Place pl;
     bool ok = true;
-    int item = pair;
-    Work ahead;
-    bool more = rank == 0 && seek(item, ahead);
-    while (ok && more) {
-      const Work w = ahead;
-      if (w.k1 <= w.k0) {
-        item += pairs;
-        more = seek(item, ahead);
-        continue;
-      }
+    Work w;
+    while (ok && take(taken, w)) {
+      if (rank != 0 || w.k1 <= w.k0) continue;
       const int n16 = (w.cols + 15) & ~15, blocks = (w.cols + 127) >> 7;
       const uint32_t acc = tmem + (tiles & 1 ? kAcc1 : 0);
       if (tiles > 0 && !(ok = wait_warp(&s.acc_free, (tiles - 1) & 1))) break;
@@ -635,7 +669,6 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
           }
         }
         __syncwarp();
-        if (k == w.k0) more = seek(item += pairs, ahead);
       }
       ++tiles;
     }
@@ -655,12 +688,9 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     // ==== scales: copies, a lane to 128 rows ======================================
     Place pl;
     bool ok = true;
-    int item = pair;
-    Work ahead;
-    bool more = seek(item, ahead);
-    while (ok && more) {
-      const Work w = ahead;
-      more = false;
+    uint32_t taken = 0;
+    Work w;
+    while (ok && take(taken, w)) {
       const Boxes boxes(w.cols);
       const int row = boxes.row(lane - 1), in = lane == 0 ? 0 : 1 + row / 128;  // its 128 rows
       const CUtensorMap* map =
@@ -676,7 +706,6 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         if (lane <= boxes.count)
           tma_load(smem_addr(ring + st * stage_bytes + at), map, k * T::kStageSf, y,
                    &s.raw[in][st]);
-        if (k == w.k0) more = seek(item += pairs, ahead);
       }
     }
     if (!ok) land();
@@ -691,15 +720,13 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     const int piece = lane & 1;
     Place pl;
     bool ok = true;
-    int item = pair;
-    Work ahead;
-    bool more = !sf_aligned && block <= c_blocks && seek(item, ahead);
-    while (ok && more) {
-      const Work w = ahead;
+    uint32_t taken = 0;
+    Work w;
+    while (ok && take(taken, w)) {
+      if (sf_aligned || block > c_blocks) continue;
       const int64_t row0 = (int64_t)(block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) +
                            (lane >> 1);
       const bool any = block == 0 || 128 * (block - 1) < w.cols;
-      more = false;
       for (int k = w.k0; k < w.k1; k += 2) {
         const bool both = k + 1 < w.k1;
         Place next = pl;
@@ -731,7 +758,6 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
           pl = next;
         }
         pl.next(stages);
-        if (k == w.k0) more = seek(item += pairs, ahead);
       }
     }
     cp_async_commit();
@@ -742,12 +768,9 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     const uint32_t base = (uint32_t)(uintptr_t)(block == 0 ? p.f_sf : p.c_sf);
     Place pl;
     bool ok = true;
-    int item = pair;
-    Work ahead;
-    bool more = seek(item, ahead);
-    while (ok && more) {
-      const Work w = ahead;
-      more = false;
+    uint32_t taken = 0;
+    Work w;
+    while (ok && take(taken, w)) {
       // where a row's bytes begin in its first piece
       const uint32_t row = (uint32_t)(block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + lane;
       const uint32_t stride = (uint32_t)p.sf_stride, off = base + row * stride;
@@ -775,7 +798,6 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         }
         __syncwarp();
         if (lane == 0) arrive_first(&s.full[st]);
-        if (k == w.k0) more = seek(item += pairs, ahead);
       }
     }
   } else {
@@ -797,9 +819,10 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       constexpr int kWords = T::kStageSf / 4;            // scale words of a row in a stage
       const int piece = lane % kQ, line = line0 + lane / kQ;
       const uint8_t* end = base + rows * p.sf_stride;
-      int item = pair, k = 0;  // the fetch that comes next
+      int k = 0;  // the fetch that comes next
+      uint32_t taken = 0;
       Work w{};
-      bool have = false;
+      bool have = false, ended = false;
       uint4 lo[kAhead][kB][4], hi[kAligned ? 1 : kAhead][kB][4];
       uint32_t off[kAhead];            // low bits of the lane's first address
       // the end of a fetch's stages (0: no more), their begin, bytes of the lane's piece
@@ -809,9 +832,12 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         constexpr int kSlot = decltype(slot_c)::value;
         count[kSlot] = 0;
         while (!have || k >= w.k1) {
-          if (have) item += pairs;
-          have = seek(item, w);
-          if (!have) return;
+          if (ended) return;
+          have = take(taken, w);
+          if (!have) {
+            ended = true;
+            return;
+          }
           k = w.k0;
           // (a weights' gradient may begin inside 16 aligned bytes)
           if (kAligned && T::kWgrad) k -= (int)(w.k_at / T::kStageK + k) % T::kFetch;
