@@ -117,15 +117,21 @@ struct Geometry {
   int split, items;
   int c_blocks, sf_at, stage_bytes, stages;
 };
-// total tiles of at most `most` columns, for so many CTAs or pairs of CTAs
+// total tiles of at most `most` columns and `stages` stages, for so many CTAs or pairs of CTAs.
+// A sum is cut where that saves more than joining its parts costs: a stage takes a CTA about
+// 250 ns and 1 ns a column (loads and products of its own tile), the join 4.5 us and 50 ns a
+// column (8 rows, 2432 x 16384: 12.5 us cut in 8, 19 whole; 512 rows, 2048 x 7168: 22 us
+// cut in 4, 17 whole).
 template <int KIND, int CG>
-__host__ __device__ __forceinline__ Geometry geometry(int total, int most, int pairs,
+__host__ __device__ __forceinline__ Geometry geometry(int total, int most, int stages, int pairs,
                                                       bool aligned) {
   Geometry g;
   g.split = 1;
   if (total > 0 && 2 * total <= pairs) {
-    g.split = (int)((uint32_t)pairs / (uint32_t)total);
-    if (g.split > 16) g.split = 16;
+    int split = (int)((uint32_t)pairs / (uint32_t)total);
+    if (split > 16) split = 16;
+    const int saved = (int)((uint32_t)(stages * (split - 1)) / (uint32_t)split);
+    if ((int64_t)saved * (250 + most) > 4500 + 50 * (int64_t)most) g.split = split;
   }
   g.items = total * g.split;
   g.c_blocks = (most + 127) / 128;
@@ -302,7 +308,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     for (int e = e0; e < e1; ++e) s.tile[e] += before;
     if (tid == 0) {
       s.tile[p.E] = total;
-      s.geo = geometry<KIND, CG>(total, most, pairs, sf_aligned);
+      s.geo = geometry<KIND, CG>(total, most, (int)((p.K + T::kStageK - 1) / T::kStageK), pairs,
+                                 sf_aligned);
     }
     __syncthreads();
   }
@@ -1012,8 +1019,10 @@ cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   MatmulParams q = p;
   q.tiles = c_tiles * ((p.N + kTileF * CG - 1) / (kTileF * CG));
   q.by_tiles = make_fastdiv((uint32_t)std::max(q.tiles, 1));
+  const int64_t sum = KIND == kMatmulMxWgrad ? p.K / p.E : p.K;
+  const int stages = (int)((sum + Kind<KIND>::kStageK - 1) / Kind<KIND>::kStageK);
   const Geometry geo = geometry<KIND, CG>(q.tiles * (KIND == kMatmulMxWgrad ? p.E : 1),
-                                          (cols + c_tiles - 1) / std::max(c_tiles, 1),
+                                          (cols + c_tiles - 1) / std::max(c_tiles, 1), stages,
                                           (int)lc.gridDim.x / CG, p.sf_stride % 16 == 0);
   return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, m, q, geo);
 }
