@@ -277,7 +277,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         if (blockIdx.x == 0) flag(p.status, NVFP4_DEV_BAD_INDEX);
         a = b = 0;
       }
-      const int cols = (int)(b - a), c_tiles = (cols + kTileC - 1) / kTileC;
+      const int cols = (int)(b - a), c_tiles = (cols + p.c_tile - 1) >> p.c_shift;
       if (c_tiles > 0)
         most = max(most, c_tiles == 1 ? cols
                                       : (int)((uint32_t)(cols + c_tiles - 1) / (uint32_t)c_tiles));
@@ -353,8 +353,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     const int cols = T::kWgrad ? p.C : rows;
     w.c0 = 0;
     w.cols = cols;
-    if (cols > kTileC) {
-      const uint32_t c_tiles = (uint32_t)(cols + kTileC - 1) / kTileC;
+    if (cols > p.c_tile) {
+      const uint32_t c_tiles = (uint32_t)(cols + p.c_tile - 1) >> p.c_shift;
       const uint32_t size = ((uint32_t)cols + c_tiles - 1) / c_tiles;
       // bands of column tiles, a band's columns first
       uint32_t band = 0, in = (uint32_t)ft, wide = c_tiles;
@@ -1015,7 +1015,7 @@ cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   lc.attrs = at;
   lc.numAttrs = CG;
   const int cols = KIND == kMatmulMxWgrad ? p.C : (int)p.c_rows;
-  const int c_tiles = (cols + kTileC - 1) / kTileC;
+  const int c_tiles = (cols + p.c_tile - 1) / p.c_tile;
   MatmulParams q = p;
   q.tiles = c_tiles * ((p.N + kTileF * CG - 1) / (kTileF * CG));
   q.by_tiles = make_fastdiv((uint32_t)std::max(q.tiles, 1));
@@ -1026,11 +1026,30 @@ cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
                                           (int)lc.gridDim.x / CG, p.sf_stride % 16 == 0);
   return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, m, q, geo);
 }
+// Pairs of CTAs on 256 features by up to 256 columns where there is about one such tile for
+// each pair; else single CTAs, with columns that are cut finer while half of the SMs would be
+// without work (512 rows, 2048 x 7168: pairs 17.0 us, tiles of 256 columns 18.8, of 128 14.4, of
+// 64 13.2; cut finer up to all SMs: 8 x 300 rows, 512 x 512 8.3 us where this takes 7.3).
 template <int KIND>
-cudaError_t launch_k(const MatmulParams& p, const Maps& m, cudaStream_t st) {
-  const int64_t cols = KIND == kMatmulMxWgrad ? p.C : p.c_rows / p.E;
-  return p.N > kTileF && cols >= kPairCols ? launch_t<KIND, 2>(p, m, st)
-                                           : launch_t<KIND, 1>(p, m, st);
+cudaError_t launch_k(MatmulParams p, const Maps& m, cudaStream_t st) {
+  constexpr bool kWgrad = KIND == kMatmulMxWgrad;
+  const int64_t cols = kWgrad ? p.C : p.c_rows / p.E;  // of a group, on average
+  // tiles of c columns in all groups: ragged ones end half a tile early
+  auto c_tiles = [&](int64_t c) {
+    return kWgrad ? p.E * ((p.C + c - 1) / c)
+                  : p.E == 1 ? (p.c_rows + c - 1) / c : p.c_rows / c + std::min<int64_t>(p.E, p.c_rows) / 2;
+  };
+  const int64_t f_tiles = (p.N + kTileF - 1) / kTileF, sms = sm_count();
+  auto tile = [&](int c, int shift) {
+    p.c_tile = c;
+    p.c_shift = shift;
+  };
+  tile(256, 8);
+  if (p.N > kTileF && cols >= kPairCols && (f_tiles + 1) / 2 * c_tiles(256) * 4 >= sms / 2 * 3)
+    return launch_t<KIND, 2>(p, m, st);
+  if (f_tiles * c_tiles(256) * 2 < sms) tile(128, 7);
+  if (f_tiles * c_tiles(128) * 2 < sms) tile(64, 6);
+  return launch_t<KIND, 1>(p, m, st);
 }
 
 }  // namespace

@@ -17,6 +17,7 @@ struct MatmulParams {
   int32_t C;                    // weights' gradient: columns of a group
   int64_t K;                    // values of a row (weights' gradient: rows to sum over)
   int32_t E;
+  int32_t c_tile, c_shift;      // columns of a tile at most, a power of two, and its logarithm
   int32_t tiles;                // of a group, where that is the same for all (by_tiles divides)
   FastDiv by_tiles;
   const int32_t* start;         // [E + 1], or null: one group of all rows
