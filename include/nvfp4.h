@@ -579,8 +579,8 @@ typedef struct {
  * device only, so that the same inputs give the same bits. Rows that no group
  * owns are not written.
  * workspace: device memory, >= nvfp4_grouped_matmul_ws_bytes() bytes, 16-byte
- * aligned, ALL ZERO before its first use; every call leaves its counters zero
- * again. It serves one call (of any of the three products) at a time.
+ * aligned, its first 4096 bytes ZERO before its first use; every call leaves them
+ * zero again. It serves one call (of any of the three products) at a time.
  * Data errors: NVFP4_DEV_BAD_INDEX for group_start out of order or outside [0,
  * rows] (such a group is left out), NVFP4_DEV_BAD_AMAX, NVFP4_DEV_TIMEOUT
  * (results and workspace are then not valid). NaN scale bytes give NaN.

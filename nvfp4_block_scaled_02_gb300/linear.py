@@ -14,7 +14,7 @@ import struct
 import torch
 
 from . import (Config, SCALE_E4M3, TARGET_MXFP8, TARGET_NVFP4, _check, _i32, _i64, _Out, _vp)
-from .kv import _BF16, _I32, _lib, _optional, _refuse, _typed, _workspace
+from .kv import _BF16, _I32, _lib, _optional, _refuse, _typed
 
 _F32 = (torch.float32,)
 _U8 = (torch.uint8, torch.int8)
@@ -53,9 +53,12 @@ def declare(L: C.CDLL) -> None:
 
 
 def grouped_matmul_workspace(device) -> torch.Tensor:
-    """A zeroed workspace (89 MB) for the three grouped products, for calls of any
-    size: it serves one call at a time and is allocated and cleared once."""
-    return _workspace(_lib().nvfp4_grouped_matmul_ws_bytes(), device)
+    """A workspace (89 MB, its counters cleared) for the three grouped products, for
+    calls of any size: it serves one call at a time and is allocated and cleared once."""
+    t = torch.empty((_lib().nvfp4_grouped_matmul_ws_bytes() + 3) // 4, dtype=torch.int32,
+                    device=device)
+    t[:1024].zero_()
+    return t
 
 
 def _bytes(t: torch.Tensor, name: str, n: int, dev: int) -> int:
