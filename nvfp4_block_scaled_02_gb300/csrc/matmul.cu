@@ -1,4 +1,51 @@
 // matmul.cu -- products of block-scaled matrices on tcgen05, grouped by expert.
+//
+//   NVFP4, MXFP8:        out[t][n] = sum over k of a[t][k] b[e][n][k], e the group of row t
+//   weights' gradient:   out[e][n][k] = sum over the rows t of group e of g[n][t] x[k][t]
+//
+// both as C = F X^T along the operands' rows: 128 rows of F ("features": the weights, or x)
+// are the M of a product, up to 256 rows of X ("columns": tokens, or g) its N, any multiple of
+// 16, so that a group's last few rows cost what they are and a call of one row reads the weights
+// alone. Codes and scales go to the tensor cores as the encoders wrote them; the products apply
+// the block scales, the outer scales are applied to the fp32 sums.
+//
+// One CTA (or a pair) to an SM, 16 warps with a job each: one copies codes by tensor map (and
+// hands out the work), one issues the products, six bring the scales, eight take the results. A
+// stage of the ring is 128 bytes of codes of every row (256 NVFP4 or 128 MXFP8 values, one
+// swizzle line) with its scales; two accumulators that share 64 columns let a tile's products
+// begin while the last one's results leave.
+//
+// Scales. tcgen05 takes them from tensor memory in a layout of its own (32 lines of four rows
+// each) that a copy from shared memory fills 512 bytes at a time; in memory a row's scales follow
+// one another. NVFP4: a tensor map copies a stage's 16 bytes of 128 rows in one box, and a warp
+// turns them in place (a lane reads 16 bytes of its line's four rows and writes them back,
+// transposed word by word). Loads by threads, which were there first, cost more than everything
+// else together: every 16 bytes are a line of their own to the load unit (dense 8192^3: 303 us;
+// 64 bytes of a row at a time 229; by asynchronous copies 256; by tensor map 199). MXFP8 has a
+// quarter of them: a lane loads 16 bytes (four stages) of its line's rows, three loads ahead,
+// which costs 2%. Rows of scales that are not whole 16 bytes come in two aligned pieces, cut at
+// their use, or, where the sum is long enough, are copied to whole ones first.
+//
+// What bounds it. A 256 x 256 tile of a pair loads 16 KB of F and 16 KB of X per CTA and stage,
+// which its products take 512 clocks for (at 16384 NVFP4 or 8192 MXFP8 operations a clock and SM);
+// the way from L2 gives an SM about 50 bytes a clock, 660 clocks, and both share the port of shared
+// memory. A single CTA's 128 x 256 tile needs 48 KB a stage (NVFP4 8192^3: 205 us without any
+// products, pairs 184). Measured, operations a second in the device's time: dense 8192^3 NVFP4
+// 5.9 PFLOP/s (3.0 times the measured cuBLAS bf16 rate), MXFP8 3.5 (1.8 times). Where columns are
+// few the weights' bytes bound it: 64 experts of 2048 x 7168, 90 rows, 62 us, 83% of the copy
+// rate; 16384 ragged rows 127 us (77% of the copy rate, 3.8 PFLOP/s). Weights' gradients write as
+// much as they read and their sums are short: 16 experts of 2048 x 7168, 16384 rows, 202 us (2.4
+// PFLOP/s), of which the change of accumulators is 650 clocks a tile of 8 stages. Small calls
+// take 6 to 13 us, most of it the way to the first copy (cold code and constants, 2 us), DRAM
+// latency and the results.
+//
+// Tried: results turned in shared memory by stmatrix for 16-byte stores (weights' gradient 218 ->
+// 248 us: shared memory has no time to spare); every warp finding its own work (220 -> 202 when
+// one does it for all); a cluster-scope release for each arrival at the pair's barriers (a stage
+// then took 2000 clocks); bands of 1 to 16 column tiles (within 1%).
+//
+// Every wait has a limit: when it runs out the CTA sets NVFP4_DEV_TIMEOUT, its other waits return
+// at once, and it frees its tensor memory and ends.
 #include "matmul.h"
 #include "tcgen05.cuh"
 
@@ -22,7 +69,9 @@ constexpr int kSmem = kRing + 1024;            // and its alignment
 // Tensor memory: two accumulators of 256 columns that share 64, then the scales of a stage.
 constexpr int kAcc1 = 192, kScales = 448;
 constexpr int kBand = 8;                       // column tiles of a band
-constexpr int kPairCols = 96;                  // columns of a group from which pairs of CTAs pay
+// Columns of a group from which pairs of CTAs pay: 64 experts of 64 rows 91 us alone and 94 in
+// pairs, of 96 rows 93 both, of 256 rows 119 and 111.
+constexpr int kPairCols = 96;
 constexpr double kPadGain = 0.3;               // see launch_matmul
 constexpr long long kWaitCycles = 2000000000;  // about a second
 
@@ -252,9 +301,9 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       mbar_init(&s.work_free[lane - kMaxStages - 1], kTakers);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  } else if (warp == kCopyWarp && lane < (T::kFp4 && sf_aligned ? 6 : 3)) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const CUtensorMap*>(&maps) + lane)
-                 : "memory");
+  } else if (warp == kCopyWarp && p.sf_stride > 0 && lane < (T::kFp4 && sf_aligned ? 6 : 3)) {
+    const CUtensorMap* map = reinterpret_cast<const CUtensorMap*>(&maps) + lane;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
   } else if (warp == kMmaWarp) {
     if constexpr (CG == 2) tmem_alloc_pair(&s.tmem, 512);
     else tmem_alloc(&s.tmem, 512);
@@ -644,6 +693,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         if (!(ok = wait_warp(&s.full[st], pl.turn))) break;
         fence_after();
         if (elect_one()) {
+          // (copies to tensor memory and products of one thread run in order: the scales' columns
+          // serve every stage)
           const uint32_t at = smem_addr(ring + st * stage_bytes);
           const uint32_t sf = tmem + kScales;
           const uint32_t sf16 = (at + sf_at) >> 4;
@@ -653,7 +704,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
             copy_scales<CG>(sf + 4 * j, scale_desc(sf16 + j * 32));
             copy_scales<CG>(sf + 16 + 8 * j, scale_desc(sf16 + T::kSfBlock / 16 + j * 32));
             if (blocks > 1)
-              copy_scales<CG>(sf + 16 + 8 * j + 4, scale_desc(sf16 + 2 * T::kSfBlock / 16 + j * 32));
+              copy_scales<CG>(sf + 16 + 8 * j + 4,
+                              scale_desc(sf16 + 2 * T::kSfBlock / 16 + j * 32));
           }
           const uint64_t df = smem_desc(at >> 4, 16), dc = smem_desc((at + kFBytes) >> 4, 16);
 #pragma unroll
@@ -665,7 +717,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
               mma_nvfp4<CG>(acc, df + 2 * j, dc + 2 * j, nvfp4_mma_desc(CG, n16), sf + 4 * j,
                         sf + 16 + 8 * j, add);
             else
-              mma_mxfp8<CG>(acc, df + 2 * j, dc + 2 * j, mxfp8_mma_desc(CG, n16, j), sf, sf + 16, add);
+              mma_mxfp8<CG>(acc, df + 2 * j, dc + 2 * j, mxfp8_mma_desc(CG, n16, j), sf, sf + 16,
+                            add);
           }
           if constexpr (CG == 2) {
             mma_commit_pair(&s.empty[st]);
@@ -753,7 +806,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
             q -= off;
             // (nothing is read at the array's end or after it)
             const int lo = in ? (int)min((int64_t)16, (int64_t)(end - q)) : 0;
-            const int hi = in && off + valid > 16 ? (int)min((int64_t)16, (int64_t)(end - q) - 16) : 0;
+            const int hi =
+                in && off + valid > 16 ? (int)min((int64_t)16, (int64_t)(end - q) - 16) : 0;
             cp_async16_zfill(dst + 256 * i, q, lo);
             cp_async16_zfill(dst + (1 + c_blocks) * T::kSfBlock + 256 * i, hi > 0 ? q + 16 : base,
                              hi);
@@ -807,34 +861,30 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         if (lane == 0) arrive_first(&s.full[st]);
       }
     }
-  } else {
-    // ==== scales: two warps to 128 rows ==========================================
+  } else if constexpr (!T::kFp4) {
+    // ==== MXFP8 scales: two warps to 128 rows =======================================
     // A line of the layout that tensor memory takes holds rows l, l + 32, l + 64 and
-    // l + 96; a warp has 16 of the 32 lines. A lane fetches 16 bytes of its line's four
-    // rows, kQ lanes side by side pieces that follow one another, several fetches ahead.
+    // l + 96; a warp has 16 of the 32 lines. A lane fetches 16 bytes (four stages) of its
+    // line's four rows, the lane beside it the next 16, several fetches ahead.
     const int block = (warp - kScaleWarp) >> 1;  // 0 features, 1 and 2 columns
-    const int line0 = ((warp - kScaleWarp) & 1) * 16;
+    const int line = ((warp - kScaleWarp) & 1) * 16 + (lane >> 1), piece = lane & 1;
     const uint8_t* base = block == 0 ? p.f_sf : p.c_sf;
     const int64_t rows = block == 0 ? p.f_rows : p.c_rows;
+    constexpr int kStages = 2 * T::kFetch;  // of a fetch
     // Where the 16 bytes are aligned they stay as they came; else two aligned pieces are
     // kept and cut at their use.
-    auto feed = [&](auto aligned_c, auto ahead_c, auto q_c) {
+    auto feed = [&](auto aligned_c, auto ahead_c) {
       constexpr bool kAligned = decltype(aligned_c)::value;
-      constexpr int kAhead = decltype(ahead_c)::value, kQ = decltype(q_c)::value;
-      constexpr int kB = kQ / 2, kLines = 32 / kQ;       // line groups of a warp, their lines
-      constexpr int kStages = kQ * T::kFetch;            // stages of a fetch
-      constexpr int kWords = T::kStageSf / 4;            // scale words of a row in a stage
-      const int piece = lane % kQ, line = line0 + lane / kQ;
+      constexpr int kAhead = decltype(ahead_c)::value;
       const uint8_t* end = base + rows * p.sf_stride;
+      const uint32_t row_step = (uint32_t)(32 * p.sf_stride);
       int k = 0;  // the fetch that comes next
       uint32_t taken = 0;
       Work w{};
       bool have = false, ended = false;
-      uint4 lo[kAhead][kB][4], hi[kAligned ? 1 : kAhead][kB][4];
+      uint4 lo[kAhead][4], hi[kAligned ? 1 : kAhead][4];
       uint32_t off[kAhead];            // low bits of the lane's first address
-      // the end of a fetch's stages (0: no more), their begin, bytes of the lane's piece
-      int count[kAhead], lead[kAhead], valid[kAhead];
-      const uint32_t row_step = (uint32_t)(32 * p.sf_stride), line_step = (uint32_t)(kLines * p.sf_stride);
+      int count[kAhead], lead[kAhead];  // the end of a fetch's stages (0: no more), their begin
       auto fetch = [&](auto slot_c) {
         constexpr int kSlot = decltype(slot_c)::value;
         count[kSlot] = 0;
@@ -847,34 +897,31 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
           }
           k = w.k0;
           // (a weights' gradient may begin inside 16 aligned bytes)
-          if (kAligned && T::kWgrad) k -= (int)(w.k_at / T::kStageK + k) % T::kFetch;
+          if (kAligned && T::kWgrad) k -= (w.k_at / T::kStageK + k) % T::kFetch;
         }
-        const int64_t row0 = (int64_t)(block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + line;
+        const int64_t row0 =
+            (int64_t)(block == 0 ? w.f_row : w.c_row + 128 * (block - 1)) + line;
         const int at = w.k_at / 32 + k * T::kStageSf + 16 * piece;
         const bool any = (block == 0 || 128 * (block - 1) < w.cols) &&
                          piece * T::kFetch < w.k1 - k;
+        const int valid = min((int)p.sf_stride - at, 16);  // bytes of the row in the piece
         count[kSlot] = min(kStages, w.k1 - k);
         lead[kSlot] = max(w.k0 - k, 0);
-        valid[kSlot] = max(0, min((int)p.sf_stride - at, 16));
         k += kStages;
         const uint8_t* first = base + row0 * p.sf_stride + at;
         off[kSlot] = (uint32_t)(uintptr_t)first;
 #pragma unroll
-        for (int b = 0; b < kB; ++b) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = any && row0 + 32 * i + kLines * b < rows;
-            const uint8_t* q = first + i * 32 * p.sf_stride + b * kLines * p.sf_stride;
-            if constexpr (kAligned) {
-              lo[kSlot][b][i] =
-                  in ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
-            } else {
-              const uint32_t o = (uint32_t)(uintptr_t)q & 15;
-              q -= o;
-              lo[kSlot][b][i] = in ? bytes16(q, end) : make_uint4(0, 0, 0, 0);
-              hi[kSlot][b][i] =
-                  in && o + valid[kSlot] > 16 ? bytes16(q + 16, end) : make_uint4(0, 0, 0, 0);
-            }
+        for (int i = 0; i < 4; ++i) {
+          const bool in = any && row0 + 32 * i < rows;
+          const uint8_t* q = first + i * 32 * p.sf_stride;
+          const uint4 none = make_uint4(0, 0, 0, 0);
+          if constexpr (kAligned) {
+            lo[kSlot][i] = in ? __ldg(reinterpret_cast<const uint4*>(q)) : none;
+          } else {
+            const int o = (int)((uintptr_t)q & 15);
+            q -= o;
+            lo[kSlot][i] = in ? bytes16(q, end) : none;
+            hi[kSlot][i] = in && o + valid > 16 ? bytes16(q + 16, end) : none;
           }
         }
       };
@@ -883,18 +930,13 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       auto store = [&](auto slot_c) -> bool {
         constexpr int kSlot = decltype(slot_c)::value;
         if (count[kSlot] == 0) return false;
-        uint32_t x[kB][4][4];
+        uint32_t x[4][4];
 #pragma unroll
-        for (int b = 0; b < kB; ++b) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 v = lo[kSlot][b][i];
-            if constexpr (!kAligned)
-              v = first_bytes(window16(v, hi[kSlot][b][i],
-                                       (off[kSlot] + i * row_step + b * line_step) & 15),
-                              valid[kSlot]);
-            x[b][i][0] = v.x, x[b][i][1] = v.y, x[b][i][2] = v.z, x[b][i][3] = v.w;
-          }
+        for (int i = 0; i < 4; ++i) {
+          uint4 v = lo[kSlot][i];
+          if constexpr (!kAligned)
+            v = window16(v, hi[kSlot][i], (off[kSlot] + i * row_step) & 15);
+          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
         }
 #pragma unroll
         for (int c = 0; c < kStages; ++c) {
@@ -905,14 +947,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
           if (block <= c_blocks && piece == c / T::kFetch) {
             uint4* dst = reinterpret_cast<uint4*>(ring + st * stage_bytes + sf_at +
                                                   block * T::kSfBlock) + line;
-            const int word = c % T::kFetch * kWords;
-#pragma unroll
-            for (int b = 0; b < kB; ++b) {
-#pragma unroll
-              for (int j = 0; j < kWords; ++j)
-                dst[32 * j + kLines * b] = make_uint4(x[b][0][word + j], x[b][1][word + j],
-                                                      x[b][2][word + j], x[b][3][word + j]);
-            }
+            constexpr int kLast = T::kFetch - 1;
+            *dst = make_uint4(x[0][c & kLast], x[1][c & kLast], x[2][c & kLast], x[3][c & kLast]);
             fence_smem_async();
           }
           __syncwarp();
@@ -923,11 +959,10 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       };
       ring_of<kAhead>(fetch, store);
     };
-    constexpr std::integral_constant<int, 2> two{};
     if (sf_aligned)
-      feed(std::true_type{}, std::integral_constant<int, 3>{}, two);
+      feed(std::true_type{}, std::integral_constant<int, 3>{});
     else
-      feed(std::false_type{}, two, two);
+      feed(std::false_type{}, std::integral_constant<int, 2>{});
   }
   __syncwarp();
   fence_before();
@@ -988,7 +1023,8 @@ bool make_map(CUtensorMap* m, const uint8_t* at, int64_t bytes, int64_t rows, in
               int box_rows) {
   const EncodeTiled f = encode_tiled();
   if (!f) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bytes};
+  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)bytes};
   const cuuint32_t sizes[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows}, steps[2] = {1, 1};
   return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(at), dims, strides, sizes,
            steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1037,7 +1073,8 @@ cudaError_t launch_k(MatmulParams p, const Maps& m, cudaStream_t st) {
   // tiles of c columns in all groups: ragged ones end half a tile early
   auto c_tiles = [&](int64_t c) {
     return kWgrad ? p.E * ((p.C + c - 1) / c)
-                  : p.E == 1 ? (p.c_rows + c - 1) / c : p.c_rows / c + std::min<int64_t>(p.E, p.c_rows) / 2;
+           : p.E == 1 ? (p.c_rows + c - 1) / c
+                      : p.c_rows / c + std::min<int64_t>(p.E, p.c_rows) / 2;
   };
   const int64_t f_tiles = (p.N + kTileF - 1) / kTileF, sms = sm_count();
   auto tile = [&](int c, int shift) {
@@ -1058,7 +1095,9 @@ cudaError_t launch_matmul(int kind, const MatmulParams& given, const uint8_t* f_
                           const uint8_t* c_codes, cudaStream_t st) {
   MatmulParams p = given;
   // Rows of scales that are not whole 16 bytes take the kernel longer, a stage by about kPadGain
-  // microseconds; copying them first takes a launch and their bytes twice.
+  // microseconds; copying them first takes a launch and their bytes twice (8 experts of 1024
+  // rows, 2048 x 7136: 114 us as they are, 80 copied first; 5 experts of 140 rows, 1000 x 416
+  // in MXFP8: 8.3 and 9.4).
   const int64_t units = (p.sf_stride + 15) / 16, padded = 16 * units;
   if (p.sf_stride % 16 != 0 && (p.f_rows + p.c_rows) * padded <= (int64_t)kMatmulPadBytes) {
     const bool wgrad = kind == kMatmulMxWgrad;

@@ -9,6 +9,11 @@
 // y / r = h w, whose products of two bf16 are exact in fp32, has y's codes and
 // block scales, and r goes into the row's amax. The codes then do not depend on
 // the order of the sum of squares.
+//
+// Both passes are bound by DRAM: 8192 x 4096 with a residual, in MXFP8, 37 us
+// (94% of the measured copy rate), the gradient 47 us (84%; 32768 rows 96%: about
+// 8 us do not depend on the rows, 3 of them the sum over CTAs in a launch of its
+// own). 32 rows take 2.6 us on the device, the host four to five times as long.
 #include "encode.cuh"
 #include "norm.h"
 #include "tcgen05.cuh"
@@ -29,7 +34,8 @@ __device__ __forceinline__ uint4 add8(uint4 a, uint4 b) {
   unpack8(b, v);
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(__fadd_rn(u[i].x, v[i].x), __fadd_rn(u[i].y, v[i].y));
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack_bf16x2(__fadd_rn(u[i].x, v[i].x), __fadd_rn(u[i].y, v[i].y));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 __device__ __forceinline__ uint4 pack8(const f2 (&v)[4]) {
@@ -187,8 +193,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
         }
       } else {
         const uint4 none = make_uint4(0, 0, 0, 0);
-        const BlockResult q = encode_block_f<0, false, FOS>(v[0], v[1], bm, ss,
-                                                            DirectScales<0>{ss.g}, none, none, false);
+        const BlockResult q = encode_block_f<0, false, FOS>(
+            v[0], v[1], bm, ss, DirectScales<0>{ss.g}, none, none, false);
         if (ok) {
           __stcs(reinterpret_cast<uint2*>(p.codes) + at, make_uint2(q.codes[0], q.codes[1]));
           p.scales[at] = (uint8_t)q.scale;
@@ -216,8 +222,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
 
 // Gradient. u = gy w: gx = r (u - h r^2 mean(u h)) + gh, and the weight's gradient is the
 // sum over rows of gy h r. Rows come by bulk copies into a ring in shared memory, so that
-// several are on their way whatever the registers hold; a thread keeps the weight gradients
-// of its values over the CTA's rows, and a second kernel adds the CTAs' sums in order.
+// several are on their way whatever the registers hold (8192 x 4096: 58 us with the next row
+// in registers, 48 so); a thread keeps the weight gradients of its values over the CTA's rows,
+// and a second kernel adds the CTAs' sums in order. Two rows between two barriers took 58 us.
 constexpr long long kWaitCycles = 2000000000;  // about a second
 constexpr int kMaxDepth = 8;
 constexpr int kRingBwd = 200 * 1024;  // bytes of shared memory for rows on an SM

@@ -7,7 +7,7 @@ E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
 def fp4_values(codes, scales, amax, M=448.0):
-    """fp64 values of an NVFP4 row encoding [..., rows, cols/2]; amax broadcasts over [..., rows]."""
+    """fp64 values of an NVFP4 row encoding [..., rows, cols/2]; amax broadcasts over its rows."""
     lut = torch.tensor(E2M1 + tuple(-m for m in E2M1), dtype=torch.float64, device=codes.device)
     x = torch.stack([lut[(codes & 15).long()], lut[(codes >> 4).long()]], -1).flatten(-2)
     amax = amax.double()

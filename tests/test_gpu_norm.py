@@ -80,7 +80,8 @@ def test_per_row_encoding_is_that_of_the_weighted_sum(rows, cols, fos, residual)
     amax32 = r["row_amax"]
     g = torch.where(amax32 > 0, divided(amax32, 6 * M), torch.ones_like(amax32))
     d = r["scales"].view(torch.float8_e4m3fn).float() * g[:, None]
-    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6], device="cuda")
+    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6],
+                       device="cuda")
     q = torch.stack([lut[(r["codes"] & 15).int()], lut[(r["codes"] >> 4).int()]], -1).flatten(-2)
     assert torch.equal(r["dequant"], (q * d.repeat_interleave(16, 1)).to(BF16))
     assert status.item() == 0

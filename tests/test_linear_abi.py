@@ -167,7 +167,8 @@ def test_the_binding_refuses_shapes():
         nv.nvfp4_add_rms_norm(x[None], w)
     with pytest.raises(ValueError):
         nv.nvfp4_add_rms_norm_bwd(x[None], x[None], w)
-    flat = {"codes": torch.zeros(64, dtype=torch.uint8), "scales": torch.zeros(4, dtype=torch.uint8)}
+    flat = {"codes": torch.zeros(64, dtype=torch.uint8),
+            "scales": torch.zeros(4, dtype=torch.uint8)}
     enc = {"codes": torch.zeros(4, 32, dtype=torch.uint8),
            "scales": torch.zeros(4, 4, dtype=torch.uint8)}
     with pytest.raises(ValueError):
