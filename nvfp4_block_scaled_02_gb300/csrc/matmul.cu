@@ -511,10 +511,10 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
 #pragma unroll
           for (int i = 0; i < kN; i += 4) {
             const float4 g = *reinterpret_cast<const float4*>(sc + c + i);
-            v[i] = __fmul_rn(__fmul_rn(v[i], g.x), gf);
-            v[i + 1] = __fmul_rn(__fmul_rn(v[i + 1], g.y), gf);
-            v[i + 2] = __fmul_rn(__fmul_rn(v[i + 2], g.z), gf);
-            v[i + 3] = __fmul_rn(__fmul_rn(v[i + 3], g.w), gf);
+            const f2 gff = make_float2(gf, gf);
+            const f2 a = f2_mul(f2_mul(make_float2(v[i], v[i + 1]), make_float2(g.x, g.y)), gff);
+            const f2 b = f2_mul(f2_mul(make_float2(v[i + 2], v[i + 3]), make_float2(g.z, g.w)), gff);
+            v[i] = a.x, v[i + 1] = a.y, v[i + 2] = b.x, v[i + 3] = b.y;
           }
         }
         const int64_t row0 = T::kWgrad ? (int64_t)w.g * p.C + w.c0 : (int64_t)w.c_row;
