@@ -301,8 +301,10 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       mbar_init(&s.work_free[lane - kMaxStages - 1], kTakers);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  } else if (warp == kCopyWarp && p.sf_stride > 0 && lane < (T::kFp4 && sf_aligned ? 6 : 3)) {
-    const CUtensorMap* map = reinterpret_cast<const CUtensorMap*>(&maps) + lane;
+  } else if (warp == kCopyWarp && p.sf_stride > 0 && lane < (T::kFp4 && sf_aligned ? 4 : 2)) {
+    // (the large boxes' maps need not be there)
+    const CUtensorMap* map =
+        lane == 0 ? &maps.f : lane == 1 ? &maps.c_small : lane == 2 ? &maps.fs : &maps.cs_small;
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
   } else if (warp == kMmaWarp) {
     if constexpr (CG == 2) tmem_alloc_pair(&s.tmem, 512);
@@ -1125,13 +1127,16 @@ cudaError_t launch_matmul(int kind, const MatmulParams& given, const uint8_t* f_
   Maps m{};
   const int64_t bytes = kind == kMatmulNvfp4 ? p.K / 2 : p.K;
   // without rows to sum over no copy is made: a weights' gradient of zeros
-  if (bytes > 0 && (!make_map(&m.f, f_codes, bytes, p.f_rows, kStageRow, kTileF) ||
-                    !make_map(&m.c, c_codes, bytes, p.c_rows, kStageRow, kBox) ||
-                    !make_map(&m.c_small, c_codes, bytes, p.c_rows, kStageRow, kBoxSmall)))
+  // and where all columns fit half a large box none is used
+  const bool large = (kind == kMatmulMxWgrad ? p.C : p.c_rows) > kBox / 2;
+  if (bytes > 0 &&
+      (!make_map(&m.f, f_codes, bytes, p.f_rows, kStageRow, kTileF) ||
+       (large && !make_map(&m.c, c_codes, bytes, p.c_rows, kStageRow, kBox)) ||
+       !make_map(&m.c_small, c_codes, bytes, p.c_rows, kStageRow, kBoxSmall)))
     return cudaErrorInvalidValue;
   if (kind == kMatmulNvfp4 && p.sf_stride % 16 == 0 &&
       (!make_map(&m.fs, p.f_sf, p.sf_stride, p.f_rows, 16, kTileF) ||
-       !make_map(&m.cs, p.c_sf, p.sf_stride, p.c_rows, 16, kBox) ||
+       (large && !make_map(&m.cs, p.c_sf, p.sf_stride, p.c_rows, 16, kBox)) ||
        !make_map(&m.cs_small, p.c_sf, p.sf_stride, p.c_rows, 16, kBoxSmall)))
     return cudaErrorInvalidValue;
   switch (kind) {

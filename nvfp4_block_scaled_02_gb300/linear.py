@@ -72,19 +72,23 @@ def _bytes(t: torch.Tensor, name: str, n: int, dev: int) -> int:
 
 def _rows_of(t: torch.Tensor, name: str) -> tuple[int, int]:
     """Rows and bytes per row of an encoding's codes."""
-    if t.dim() < 2:
+    shape = t.shape
+    if len(shape) == 2:
+        return shape
+    if len(shape) < 2:
         raise ValueError(f"{name} must be [rows, bytes] or [slices, rows, bytes]")
-    width = t.shape[-1]
+    width = shape[-1]
     return (t.numel() // width if width else 0), width
 
 
 def _groups_of(t: torch.Tensor, name: str) -> tuple[int, int, int]:
     """Groups, rows of a group and bytes per row of the weights' codes."""
-    if t.dim() == 2:
-        return 1, t.shape[0], t.shape[1]
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) == 3:
+        return shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be [rows, bytes] or [groups, rows, bytes]")
-    return tuple(t.shape)
+    return 1, shape[0], shape[1]
 
 
 def _starts(start: torch.Tensor | None, groups: int, dev: int) -> int:
@@ -100,13 +104,6 @@ def _result(out, shape, dtypes, dev: int) -> int:
             out.is_contiguous()):
         return out.data_ptr()
     return _refuse(out, "out", shape, dtypes, dev)
-
-
-def _encoded(codes, scales, n: int, m: int, dev: int) -> bool:
-    """Whether codes and scales are byte arrays of n and m elements on the device."""
-    return (codes.dtype in _U8 and scales.dtype in _U8 and codes.numel() == n
-            and scales.numel() == m and codes.get_device() == dev == scales.get_device()
-            and dev >= 0 and codes.is_contiguous() and scales.is_contiguous())
 
 
 def _outer_max(cfg: Config | None, name: str) -> float:
@@ -139,20 +136,22 @@ def nvfp4_grouped_matmul(a: dict, a_amax: torch.Tensor, b: dict, b_amax: torch.T
     asc, bsc = a["scales"], b["scales"]
     T, half = _rows_of(ac, "a codes")
     E, N, bhalf = _groups_of(bc, "b codes")
-    if half != bhalf:
-        raise ValueError(f"a has rows of {2 * half} values, b of {2 * bhalf}")
-    n = a_amax.numel()
-    if n != 1 and n != T:
-        raise ValueError(f"a_amax holds {n} elements; the call needs 1 or {T}")
-    if b_amax.numel() != E:
-        raise ValueError(f"b_amax holds {b_amax.numel()} elements; the call needs {E}")
-    f32 = torch.float32
+    n, f32 = a_amax.numel(), torch.float32
     # one expression for what is usual; what is wrong is looked up only if it fails
-    if not (_encoded(ac, asc, T * half, T * half // 8, dev)
-            and _encoded(bc, bsc, E * N * half, E * N * half // 8, dev)
+    if not (half == bhalf and (n == 1 or n == T) and b_amax.numel() == E
+            and asc.numel() * 8 == T * half and bsc.numel() * 8 == E * N * half
+            and ac.dtype in _U8 and asc.dtype in _U8 and bc.dtype in _U8 and bsc.dtype in _U8
             and a_amax.dtype is f32 and b_amax.dtype is f32
-            and a_amax.get_device() == dev == b_amax.get_device()
-            and a_amax.is_contiguous() and b_amax.is_contiguous()):
+            and dev == asc.get_device() == bc.get_device() == bsc.get_device() >= 0
+            and dev == a_amax.get_device() == b_amax.get_device()
+            and ac.is_contiguous() and asc.is_contiguous() and bc.is_contiguous()
+            and bsc.is_contiguous() and a_amax.is_contiguous() and b_amax.is_contiguous()):
+        if half != bhalf:
+            raise ValueError(f"a has rows of {2 * half} values, b of {2 * bhalf}")
+        if n != 1 and n != T:
+            raise ValueError(f"a_amax holds {n} elements; the call needs 1 or {T}")
+        if b_amax.numel() != E:
+            raise ValueError(f"b_amax holds {b_amax.numel()} elements; the call needs {E}")
         _bytes(ac, "a codes", T * half, dev)
         _bytes(asc, "a scales", T * half // 8, dev)
         _bytes(bc, "b codes", E * N * half, dev)
@@ -197,8 +196,11 @@ def nvfp4_mx_grouped_matmul(a: dict, b: dict, group_start: torch.Tensor | None =
     if K != bk:
         raise ValueError(f"a has rows of {K} values, b of {bk}")
     asc, bsc = a["scales"], b["scales"]
-    if not (_encoded(ac, asc, T * K, T * K // 32, dev)
-            and _encoded(bc, bsc, E * N * K, E * N * K // 32, dev)):
+    if not (asc.numel() * 32 == T * K and bsc.numel() * 32 == E * N * K
+            and ac.dtype in _U8 and asc.dtype in _U8 and bc.dtype in _U8 and bsc.dtype in _U8
+            and dev == asc.get_device() == bc.get_device() == bsc.get_device() >= 0
+            and ac.is_contiguous() and asc.is_contiguous() and bc.is_contiguous()
+            and bsc.is_contiguous()):
         _bytes(ac, "a codes", T * K, dev)
         _bytes(asc, "a scales", T * K // 32, dev)
         _bytes(bc, "b codes", E * N * K, dev)
@@ -246,8 +248,11 @@ def nvfp4_mx_grouped_wgrad(g: dict, x: dict, group_start: torch.Tensor | None = 
     if E < 0:
         raise ValueError("group_start must hold groups + 1 entries")
     gsc, xsc = g["scales"], x["scales"]
-    if not (_encoded(gc, gsc, N * T, N * T // 32, dev)
-            and _encoded(xc, xsc, K * T, K * T // 32, dev)):
+    if not (gsc.numel() * 32 == N * T and xsc.numel() * 32 == K * T
+            and gc.dtype in _U8 and gsc.dtype in _U8 and xc.dtype in _U8 and xsc.dtype in _U8
+            and dev == gsc.get_device() == xc.get_device() == xsc.get_device() >= 0
+            and gc.is_contiguous() and gsc.is_contiguous() and xc.is_contiguous()
+            and xsc.is_contiguous()):
         _bytes(gc, "g codes", N * T, dev)
         _bytes(gsc, "g scales", N * T // 32, dev)
         _bytes(xc, "x codes", K * T, dev)

@@ -48,7 +48,9 @@ SIZES = [(1, 1, 1, 32), (1, 1, 128, 256), (1, 16, 128, 512), (1, 5, 130, 96), (1
          (7, 40, 77, 160), (1, 33, 64, 7168), (1, 300, 128, 4096), (64, 90, 2048, 1024),
          (2, 3000, 1536, 320), (1, 2000, 4096, 512), (300, 900, 136, 64),
          # rows of scales that are not whole 16 bytes, in sums long enough to be copied first
-         (4, 3000, 1536, 7136), (24, 200, 1500, 7136)]
+         (4, 3000, 1536, 7136), (24, 200, 1500, 7136),
+         # pairs of CTAs with groups of few rows, and with features that end inside a pair
+         (40, 6000, 512, 288), (40, 6000, 333, 256), (30, 4500, 650, 512)]
 
 
 @pytest.mark.parametrize("E,T,N,K", SIZES)
