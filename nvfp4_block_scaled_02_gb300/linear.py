@@ -325,7 +325,7 @@ def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor,
             raise ValueError("h is x itself without a residual")
         h, h_at = x, 0
     elif h is None:
-        h = torch.empty_like(x)
+        h = empty(shape, dtype=x.dtype, device=device)
         h_at = h.data_ptr()
     else:
         h_at = _matrix(h, "h", shape, dev)
@@ -404,7 +404,7 @@ def nvfp4_add_rms_norm_bwd(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
         _matrix(weight, "weight", (Cc,), dev)
         _matrix(gh, "gh", shape, dev)
     if gx is None:
-        gx = torch.empty_like(h)
+        gx = torch.empty(shape, dtype=h.dtype, device=h.device)
         gx_at = gx.data_ptr()
     else:
         gx_at = _matrix(gx, "gx", shape, dev)
