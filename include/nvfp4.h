@@ -584,8 +584,8 @@ typedef struct {
  * Data errors: NVFP4_DEV_BAD_INDEX for group_start out of order or outside [0,
  * rows] (such a group is left out), NVFP4_DEV_BAD_AMAX, NVFP4_DEV_TIMEOUT
  * (results and workspace are then not valid). NaN scale bytes give NaN.
- * Errors: NULL pointers, sizes out of range (rows, groups * out_cols and cols up
- * to 2^31 - 4097, 2^26 tiles of 256 x 128 results), cols % 32, amax_count,
+ * Errors: NULL pointers, sizes out of range (rows and groups * out_cols up to 2^31
+ * - 4097, cols up to 2^25, 2^26 tiles of 256 x 128 results), cols % 32, amax_count,
  * scale_max negative or not finite (NVFP4_ERR_ENUM), buffers that are not
  * 16-byte aligned (amax, group_start, status: 4), and those of the workspace (as
  * nvfp4_amax_ws). */
@@ -608,8 +608,8 @@ NVFP4_API nvfp4_status nvfp4_mx_grouped_matmul(const uint8_t* a_codes, const uin
 
 /* WGRAD: out[e][n][k] = sum over the rows t of group e of g[n][t] * x[k][t], with
  * g [out_rows][rows] and x [out_cols][rows] in MXFP8 (column encodings of the
- * output's gradient and of the activations: blocks of 32 along the rows). rows
- * % 32 == 0 and every entry of group_start a multiple of 32 (pad an expert's rows
+ * output's gradient and of the activations: blocks of 32 along the rows). rows up
+ * to 2^25, rows % 32 == 0 and every entry of group_start a multiple of 32 (pad an expert's rows
  * with zeros): another one is NVFP4_DEV_BAD_INDEX, and its groups' results are
  * not written. A group without rows gets zeros. out: bf16, or fp32 with out_fp32
  * = 1, [groups][out_rows][out_cols]. Otherwise as nvfp4_mx_grouped_matmul. */
@@ -634,8 +634,9 @@ NVFP4_API nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint
  * each row has its own outer scale and row_amax (fp32 [rows]) receives r *
  * max|h * weight|; codes and block scales are those of nvfp4_quantize_per_token's
  * steps on h * weight, to which r is a common factor: they do not depend on how
- * the sum of squares rounds. out->choice (may be NULL) receives ceil(cols/512)
- * words a row; out->dequant (may be NULL) the values that the codes stand for.
+ * the sum of squares rounds (and lose bits where h * weight is below 2^-126).
+ * out->choice (may be NULL) receives ceil(cols/512) words a row; out->dequant (may
+ * be NULL) the values that the codes stand for.
  * cfg: blocks NVFP4_BLOCKS_ROW, rounding NVFP4_ROUND_RNE.
  * Data errors: NVFP4_DEV_NONFINITE_INPUT (also for a sum of squares or a product
  * h * weight past fp32), NVFP4_DEV_BAD_AMAX. A row whose mean square and eps are 0

@@ -12,10 +12,12 @@ bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0;
 nvfp4_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 constexpr int64_t kMaxI32 = INT32_MAX;
 
-// Sizes of a product: coordinates, tiles and the rows of all groups are counted in 32 bits.
-bool sizes_ok(int64_t rows, int64_t groups, int64_t n, int64_t k) {
+// Sizes of a product: coordinates, tiles and the rows of all groups are counted in 32 bits, and
+// a sum is of `sum` values at most.
+bool sizes_ok(int64_t rows, int64_t groups, int64_t n, int64_t k, int64_t sum) {
   if (rows < 0 || groups < 0 || n < 0 || k < 0 || rows > kMaxI32 - 4096 || n > kMaxI32 - 4096 ||
-      k > kMaxI32 - 4096 || groups > nvfp4::kMatmulMaxGroups || groups * n > kMaxI32 - 4096)
+      k > kMaxI32 - 4096 || groups > nvfp4::kMatmulMaxGroups || groups * n > kMaxI32 - 4096 ||
+      sum > nvfp4::kMatmulMaxSum)
     return false;
   return true;
 }
@@ -60,7 +62,7 @@ nvfp4_status nvfp4_grouped_matmul(const nvfp4_operand* a, const nvfp4_operand* b
                                   const int32_t* group_start, void* out, void* workspace,
                                   size_t ws_bytes, int32_t* status, void* stream) {
   if (!a || !b) return NVFP4_ERR_NULL;
-  if (!sizes_ok(rows, groups, out_cols, cols) || cols % 32 != 0 ||
+  if (!sizes_ok(rows, groups, out_cols, cols, cols) || cols % 32 != 0 ||
       !tiles_ok((rows / 256 + groups + 1) * (out_cols / 128 + 1)))
     return NVFP4_ERR_SHAPE;
   for (const nvfp4_operand* o : {a, b})
@@ -102,7 +104,7 @@ nvfp4_status nvfp4_mx_grouped_matmul(const uint8_t* a_codes, const uint8_t* a_sc
                                      int64_t groups, int64_t out_cols, int64_t cols,
                                      const int32_t* group_start, void* out, void* workspace,
                                      size_t ws_bytes, int32_t* status, void* stream) {
-  if (!sizes_ok(rows, groups, out_cols, cols) || cols % 32 != 0 ||
+  if (!sizes_ok(rows, groups, out_cols, cols, cols) || cols % 32 != 0 ||
       !tiles_ok((rows / 256 + groups + 1) * (out_cols / 128 + 1)))
     return NVFP4_ERR_SHAPE;
   if (rows == 0 || groups == 0 || out_cols == 0) return NVFP4_OK;
@@ -133,7 +135,7 @@ nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint8_t* g_sca
                                     const int32_t* group_start, void* out, int32_t out_fp32,
                                     void* workspace, size_t ws_bytes, int32_t* status,
                                     void* stream) {
-  if (!sizes_ok(rows, groups, out_rows, out_cols) || rows % 32 != 0 ||
+  if (!sizes_ok(rows, groups, out_rows, out_cols, rows) || rows % 32 != 0 ||
       !tiles_ok(groups * (out_rows / 256 + 1) * (out_cols / 128 + 1)))
     return NVFP4_ERR_SHAPE;
   if (out_fp32 != 0 && out_fp32 != 1) return NVFP4_ERR_ENUM;

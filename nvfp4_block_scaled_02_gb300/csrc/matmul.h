@@ -35,6 +35,9 @@ struct MatmulParams {
 enum { kMatmulNvfp4 = 0, kMatmulMx = 1, kMatmulMxWgrad = 2 };
 
 constexpr int kMatmulMaxGroups = 1024;
+// The longest sum: one CTA takes at most 2^18 stages of 128 values for a tile, a quarter of a
+// second at 1 us each, and the waits' limit is one.
+constexpr int64_t kMatmulMaxSum = 1 << 25;
 constexpr int kMatmulMaxCtas = 192;
 constexpr int kMatmulPart = 256 * 128;  // floats of a partial result
 constexpr size_t kMatmulPadBytes = (size_t)64 << 20;  // scales in rows of whole 16 bytes

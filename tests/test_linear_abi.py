@@ -93,6 +93,18 @@ def test_mx_grouped_wgrad_argument_errors(L):
         assert call(**{**dict(out=None, ws=None), **empty}) == OK
 
 
+def test_sums_too_long_for_the_waits(L):
+    size, most = L.nvfp4_grouped_matmul_ws_bytes(), 1 << 25
+    a = operand()
+    for k, want in ((most + 32, SHAPE), (most, NULL)):  # (NULL: past the sizes, no workspace)
+        assert L.nvfp4_grouped_matmul(C.byref(a), C.byref(a), 1, 1, 16, k, None, FAKE, None, size,
+                                      None, None) == want
+        assert L.nvfp4_mx_grouped_matmul(FAKE, FAKE, FAKE, FAKE, 1, 1, 16, k, None, FAKE, None,
+                                         size, None, None) == want
+        assert L.nvfp4_mx_grouped_wgrad(FAKE, FAKE, FAKE, FAKE, k, 1, 16, 16, None, FAKE, 0, None,
+                                        size, None, None) == want
+
+
 def cfg(**kw):
     return nv.Config(**kw).c()
 
