@@ -319,6 +319,10 @@ def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor,
     fp4 = target == TARGET_NVFP4
     if not fp4 and target != TARGET_MXFP8:
         raise ValueError("target must be TARGET_MXFP8 or TARGET_NVFP4")
+    if dequant and not fp4:
+        raise ValueError("dequant is of the NVFP4 target")
+    if row_amax is not None and (global_amax is not None or not fp4):
+        raise ValueError("row_amax is written for the NVFP4 target without global_amax")
     empty, device = torch.empty, x.device
     if residual is None:
         if h is not None and h is not x:

@@ -298,6 +298,27 @@ def test_past_32_bits(ws):
     assert not out[37, -1].any()
 
 
+def test_a_matrix_with_itself(ws):
+    """One encoding, and one outer scale, as both operands."""
+    x = randn(1, 300, 416)
+    amax = nv.nvfp4_amax(x)
+    q = nv.nvfp4_quantize(x, amax, nv.Config(), dequant=False)["row"]
+    out = nv.nvfp4_grouped_matmul(q, amax, q, amax, workspace=ws)
+    v = fp4_values(q["codes"].view(300, -1), q["scales"].view(300, -1), amax.expand(300))
+    ref = v @ v.T
+    assert ((out.double() - ref).abs() <= product_bound(v, v, ref)).all()
+    m = nv.nvfp4_mx_quantize(x, nv.Config(blocks=nv.BLOCKS_ROW))["row"]
+    out = nv.nvfp4_mx_grouped_matmul(m, m, workspace=ws)
+    v = mx_values(m["codes"], m["scales"])[0]
+    ref = v @ v.T
+    assert ((out.double() - ref).abs() <= product_bound(v, v, ref)).all()
+    m = nv.nvfp4_mx_quantize(x[:288], nv.Config(blocks=nv.BLOCKS_COL))["col"]
+    out = nv.nvfp4_mx_grouped_wgrad(m, m, out_dtype=torch.float32, workspace=ws)
+    v = mx_values(m["codes"], m["scales"])[0]
+    ref = v @ v.T
+    assert ((out[0].double() - ref).abs() <= product_bound(v, v, ref, True)).all()
+
+
 def test_on_inputs_device_and_refusals():
     a, aa, b, ba, _, _ = fp4_operands(8, 2, 40, 64)
     st = torch.tensor([0, 4, 8], **I32)

@@ -291,3 +291,42 @@ def test_empty():
     assert r["codes"].shape == (0, 32) and r["row_amax"].shape == (0,)
     b = nv.nvfp4_add_rms_norm_bwd(x, x, w)
     assert b["gx"].shape == (0, 64) and not b["gw"].any()
+
+
+def test_what_would_not_be_written_is_refused():
+    x, w, one = randn(1, 4, 64), weight(2, 64), torch.ones(1, device="cuda")
+    rows = torch.zeros(4, device="cuda")
+    for kw in (dict(target=nv.TARGET_MXFP8, dequant=True),
+               dict(target=nv.TARGET_MXFP8, row_amax=rows), dict(global_amax=one, row_amax=rows)):
+        with pytest.raises(ValueError):
+            nv.nvfp4_add_rms_norm(x, w, **kw)
+    assert nv.nvfp4_add_rms_norm(x, w, row_amax=rows)["row_amax"] is rows and rows.all()
+
+
+def test_two_streams_at_once():
+    """Forward and gradient on two streams, each with its workspace, give the bits of a call
+    alone."""
+    w = weight(1, 1056)
+    cases = [(randn(i, r, 1056), randn(10 + i, r, 1056), randn(20 + i, r, 1056))
+             for i, r in enumerate((5, 1021, 3000))]
+    spaces = [nv.add_rms_norm_workspace("cuda") for _ in range(2)]
+
+    def step(case, ws):
+        x, res, gy = case
+        f = nv.nvfp4_add_rms_norm(x, w, res)
+        b = nv.nvfp4_add_rms_norm_bwd(gy, f["h"], w, res, workspace=ws)
+        return f["h"], f["codes"], f["scales"], f["row_amax"], b["gx"], b["gw"]
+
+    alone = [step(c, spaces[0]) for c in cases]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for s in (0, 1):
+            with torch.cuda.stream(side[s]):
+                for c in cases[::1 - 2 * s]:
+                    got[s].append(step(c, spaces[s]))
+    torch.cuda.synchronize()
+    for s in (0, 1):
+        for i, r in enumerate(got[s]):
+            assert all(torch.equal(a, b) for a, b in zip(r, alone[::1 - 2 * s][i % 3]))
