@@ -150,13 +150,16 @@ nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint8_t* g_sca
     if (!aligned(q, 16)) return NVFP4_ERR_ALIGN;
   if (!aligned(group_start, 4) || !aligned(status, 4)) return NVFP4_ERR_ALIGN;
   nvfp4::MatmulParams p{};
-  p.f_sf = x_scales;
-  p.c_sf = g_scales;
-  p.f_rows = out_cols;
-  p.c_rows = out_rows;
+  // The product's lanes are features. With g's rows there a lane holds a piece of a result's row
+  // of bf16, whole 32 bytes of which leave at a time; else x's rows, whose lanes hold neighbours.
+  p.turn = !out_fp32 && out_cols % 16 == 0 && aligned(out, 32);
+  p.f_sf = p.turn ? g_scales : x_scales;
+  p.c_sf = p.turn ? x_scales : g_scales;
+  p.f_rows = p.turn ? out_rows : out_cols;
+  p.c_rows = p.turn ? out_cols : out_rows;
   p.sf_stride = rows / 32;
-  p.N = (int32_t)out_cols;
-  p.C = (int32_t)out_rows;
+  p.N = (int32_t)p.f_rows;
+  p.C = (int32_t)p.c_rows;
   p.K = rows;
   p.E = (int32_t)groups;
   p.start = group_start;
@@ -164,7 +167,8 @@ nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint8_t* g_sca
   p.out_f32 = out_fp32;
   p.status = status;
   fill_ws(p, workspace);
-  return cuda_status(nvfp4::launch_matmul(nvfp4::kMatmulMxWgrad, p, x_codes, g_codes,
+  return cuda_status(nvfp4::launch_matmul(nvfp4::kMatmulMxWgrad, p,
+                                          p.turn ? g_codes : x_codes, p.turn ? x_codes : g_codes,
                                           static_cast<cudaStream_t>(stream)));
 }
 

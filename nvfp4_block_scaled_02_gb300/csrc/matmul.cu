@@ -34,10 +34,19 @@
 // 5.9 PFLOP/s (3.0 times the measured cuBLAS bf16 rate), MXFP8 3.5 (1.8 times). Where columns are
 // few the weights' bytes bound it: 64 experts of 2048 x 7168, 90 rows, 62 us, 83% of the copy
 // rate; 16384 ragged rows 127 us (77% of the copy rate, 3.8 PFLOP/s). Weights' gradients write as
-// much as they read and their sums are short: 16 experts of 2048 x 7168, 16384 rows, 202 us (2.4
-// PFLOP/s), of which the change of accumulators is 650 clocks a tile of 8 stages. Small calls
-// take 6 to 13 us, most of it the way to the first copy (cold code and constants, 2 us), DRAM
-// latency and the results.
+// much as they read and their sums are short: 16 experts of 2048 x 7168, 16384 rows, 189 us (2.5
+// PFLOP/s), of which the change of accumulators is 700 to 1000 clocks a tile of 8 stages and the
+// results' way out 20 us. Small calls take 6 to 13 us, most of it the way to the first copy (cold
+// code and constants, 2 us), DRAM latency and the results.
+//
+// Results. A lane holds a feature's. Of a product over tokens the features are neighbours in
+// memory: lanes swap halves with a shuffle and store 4 bytes. That is nine instructions for two
+// values, which a tile of 8 stages has no time for (5800 of its 6700 clocks). A weights' gradient's
+// features may be either operand's rows: g's, so that a lane's results are a row's, which go to
+// shared memory 16 bytes at a time and leave by tensor map, for one stage of the ring less (202 us
+// to 189; 1000 x 544 8.5 to 7.5; sums of 32 stages 147 to 148). Stored from the lanes they took 213
+// us in pieces of 32 bytes and 294 of 16; tokens' results by tensor map gain nothing (126 us, MXFP8
+// 173 to 175). fp32 results and rows that are not whole 32 bytes go the other way.
 //
 // Tried: results turned in shared memory by stmatrix for 16-byte stores (weights' gradient 218 ->
 // 248 us: shared memory has no time to spare); every warp finding its own work (220 -> 202 when
@@ -64,8 +73,8 @@ constexpr int kStageRow = 128;                 // code bytes of a row in a stage
 constexpr int kFBytes = kTileF * kStageRow;
 constexpr int kBox = 128, kBoxSmall = 32;      // rows of one copy
 constexpr int kMaxStages = 12;
-constexpr int kRing = 216 * 1024;              // bytes of the ring of stages
-constexpr int kSmem = kRing + 1024;            // and its alignment
+constexpr int kSmem = 217 * 1024;              // the ring of stages, 1 KB for its alignment
+constexpr int kTurn = 2048;                    // bytes of a warp's results on their way out
 // Tensor memory: two accumulators of 256 columns that share 64, then the scales of a stage.
 constexpr int kAcc1 = 192, kScales = 448;
 constexpr int kBand = 8;                       // column tiles of a band
@@ -133,6 +142,13 @@ __device__ __forceinline__ uint4 first_bytes(uint4 x, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 32 bytes, 32-byte aligned
+__device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // Copies of n columns: large boxes as far as they fill, then one more or, for up to half
 // of it, small ones.
 struct Boxes {
@@ -157,6 +173,8 @@ struct Kind {
   static constexpr int kStageSf = kFp4 ? 16 : 4;    // scale bytes of a row in a stage
   static constexpr int kSfBlock = 128 * kStageSf;   // scale bytes of 128 rows in a stage
   static constexpr int kFetch = 16 / kStageSf;      // stages whose scales are fetched together
+  // bytes of the ring of stages (a weights' gradient's results leave through the rest)
+  static constexpr int kRing = kSmem - 1024 - (kWgrad ? kEpilogueWarps * kTurn : 0);
 };
 
 // How a call is cut: tiles, parts of a tile's sum (where there are more CTAs than tiles), and
@@ -188,7 +206,7 @@ __host__ __device__ __forceinline__ Geometry geometry(int total, int most, int s
   // (NVFP4 scales that are not aligned come as two aligned pieces)
   const int sf = (1 + g.c_blocks) * Kind<KIND>::kSfBlock * (Kind<KIND>::kFp4 && !aligned ? 2 : 1);
   g.stage_bytes = (g.sf_at + sf + 1023) & ~1023;
-  g.stages = (int)((uint32_t)kRing / (uint32_t)g.stage_bytes);
+  g.stages = (int)((uint32_t)Kind<KIND>::kRing / (uint32_t)g.stage_bytes);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   return g;
 }
@@ -242,6 +260,7 @@ struct Place {
 struct Maps {
   CUtensorMap f, c, c_small;     // codes of the features' and the columns' rows
   CUtensorMap fs, cs, cs_small;  // their scales
+  CUtensorMap out;               // a weights' gradient's results
 };
 
 struct Shared {
@@ -406,7 +425,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
     w.cols = cols;
     if (cols > p.c_tile) {
       const uint32_t c_tiles = (uint32_t)(cols + p.c_tile - 1) >> p.c_shift;
-      const uint32_t size = ((uint32_t)cols + c_tiles - 1) / c_tiles;
+      uint32_t size = ((uint32_t)cols + c_tiles - 1) / c_tiles;
+      if (T::kWgrad) size = (size + 31) & ~31u;  // (a box of results is of one tile)
       // bands of column tiles, a band's columns first
       uint32_t band = 0, in = (uint32_t)ft, wide = c_tiles;
       if (c_tiles > kBand) {
@@ -519,6 +539,32 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
             v[i] = a.x, v[i + 1] = a.y, v[i + 2] = b.x, v[i + 3] = b.y;
           }
         }
+        if (T::kWgrad && p.turn) {
+          if constexpr (kN == 32) {
+            // a lane's 64 bytes of a row to shared memory, swizzled so that eight rows meet no
+            // bank twice, and the warp's box to its place
+            if (f - lane >= p.N) return;
+            if (lane == 0) bulk_wait_read();  // the last box has left
+            __syncwarp();
+            uint8_t* at = ring + T::kRing + warp * kTurn;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(at + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
+                             pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                             pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                             pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+            fence_smem_async();
+            __syncwarp();
+            if (lane == 0) tma_store(&maps.out, w.c0 + c, f, w.g, smem_addr(at));
+          } else if (f < p.N) {  // a sum's parts: 16 columns
+            uint32_t x[kN / 2];
+#pragma unroll
+            for (int j = 0; j < kN / 2; ++j) x[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            store32(static_cast<uint16_t*>(p.out) + ((int64_t)w.g * p.N + f) * p.C + w.c0 + c, x);
+          }
+          return;
+        }
         const int64_t row0 = T::kWgrad ? (int64_t)w.g * p.C + w.c0 : (int64_t)w.c_row;
         // every lane has a feature, every column is there: no checks
         const bool whole = c + kN <= w.cols && f - lane + 32 <= p.N;
@@ -615,6 +661,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         }
       }
     }
+    if (T::kWgrad && lane == 0) bulk_wait_read();
   } else if (warp == kCopyWarp) {
     // ==== codes: one lane to a box; pieces of work for all warps =====================
     Place pl;
@@ -1034,6 +1081,19 @@ bool make_map(CUtensorMap* m, const uint8_t* at, int64_t bytes, int64_t rows, in
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// a weights' gradient's bf16 results [E][N][C], boxes of 32 x 32
+bool make_out_map(CUtensorMap* m, const MatmulParams& p) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t row = 2 * (cuuint64_t)p.C;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.C, (cuuint64_t)p.N, (cuuint64_t)p.E};
+  const cuuint64_t strides[2] = {row, row * p.N};
+  const cuuint32_t sizes[3] = {32, 32, 1}, steps[3] = {1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.out, dims, strides, sizes, steps,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int KIND, int CG>
 cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
@@ -1057,11 +1117,13 @@ cudaError_t launch_t(const MatmulParams& p, const Maps& m, cudaStream_t st) {
   MatmulParams q = p;
   q.tiles = c_tiles * ((p.N + kTileF * CG - 1) / (kTileF * CG));
   q.by_tiles = make_fastdiv((uint32_t)std::max(q.tiles, 1));
+  int most = (cols + c_tiles - 1) / std::max(c_tiles, 1);
+  if (KIND == kMatmulMxWgrad && c_tiles > 1) most = (most + 31) & ~31;
   const int64_t sum = KIND == kMatmulMxWgrad ? p.K / p.E : p.K;
   const int stages = (int)((sum + Kind<KIND>::kStageK - 1) / Kind<KIND>::kStageK);
   const Geometry geo = geometry<KIND, CG>(q.tiles * (KIND == kMatmulMxWgrad ? p.E : 1),
-                                          (cols + c_tiles - 1) / std::max(c_tiles, 1), stages,
-                                          (int)lc.gridDim.x / CG, p.sf_stride % 16 == 0);
+                                          most, stages, (int)lc.gridDim.x / CG,
+                                          p.sf_stride % 16 == 0);
   return cudaLaunchKernelEx(&lc, matmul_kernel<KIND, CG>, m, q, geo);
 }
 // Pairs of CTAs on 256 features by up to 256 columns where there is about one such tile for
@@ -1139,6 +1201,7 @@ cudaError_t launch_matmul(int kind, const MatmulParams& given, const uint8_t* f_
        (large && !make_map(&m.cs, p.c_sf, p.sf_stride, p.c_rows, 16, kBox)) ||
        !make_map(&m.cs_small, p.c_sf, p.sf_stride, p.c_rows, 16, kBoxSmall)))
     return cudaErrorInvalidValue;
+  if (p.turn && !make_out_map(&m.out, p)) return cudaErrorInvalidValue;
   switch (kind) {
     case kMatmulNvfp4: return launch_k<kMatmulNvfp4>(p, m, st);
     case kMatmulMx: return launch_k<kMatmulMx>(p, m, st);

@@ -26,6 +26,8 @@ struct MatmulParams {
   float c_M, f_M;
   void* out;
   int32_t out_f32;
+  int32_t turn;                 // weights' gradient: the features are rows of the results, which
+                                // leave by tensor map
   uint32_t* tickets;
   float* part;
   uint8_t* padded;              // kMatmulPadBytes

@@ -278,4 +278,16 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int
                : "memory");
 }
 
+// A box of shared memory to global memory, a group of copies of its own.
+__device__ __forceinline__ void tma_store(const void* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group "
+               "[%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The thread's groups have read shared memory.
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 }  // namespace nvfp4

@@ -298,6 +298,24 @@ def test_past_32_bits(ws):
     assert not out[37, -1].any()
 
 
+@pytest.mark.parametrize("E,T,N,K", [(5, 320, 33, 64), (3, 96, 130, 304), (2, 4096, 96, 272),
+                                     (8, 2048, 500, 1040)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradients_stay_in_their_place(ws, E, T, N, K, dtype):
+    """Results at 16-byte and at 32-byte boundaries of a larger buffer: the same bits, nothing
+    around them."""
+    g, x, _, _ = columns(T, N, K)
+    start = starts(ragged(np.random.default_rng(N), E, T, unit=32))
+    want = nv.nvfp4_mx_grouped_wgrad(g, x, start, out_dtype=dtype, workspace=ws)
+    n = E * N * K
+    for at in (8, 16, 32):
+        buf = torch.full((n + 64,), 7.0, dtype=dtype, device="cuda")
+        out = buf[at:at + n].view(E, N, K)
+        nv.nvfp4_mx_grouped_wgrad(g, x, start, out=out, workspace=ws)
+        assert torch.equal(out, want)
+        assert (buf[:at] == 7).all() and (buf[at + n:] == 7).all()
+
+
 def test_a_matrix_with_itself(ws):
     """One encoding, and one outer scale, as both operands."""
     x = randn(1, 300, 416)
