@@ -35,8 +35,8 @@
 // few the weights' bytes bound it: 64 experts of 2048 x 7168, 90 rows, 62 us, 83% of the copy
 // rate; 16384 ragged rows 127 us (77% of the copy rate, 3.8 PFLOP/s). Weights' gradients write as
 // much as they read and their sums are short: 16 experts of 2048 x 7168, 16384 rows, 189 us (2.5
-// PFLOP/s), of which the change of accumulators is 700 to 1000 clocks a tile of 8 stages and the
-// results' way out 20 us. Small calls take 6 to 13 us, most of it the way to the first copy (cold
+// PFLOP/s), of which the results' way out is 20 us (the change of accumulators is 700 to 1000
+// clocks a tile of 8 stages, but products that do not wait for it gain 3 us). Small calls take 6 to 13 us, most of it the way to the first copy (cold
 // code and constants, 2 us), DRAM latency and the results.
 //
 // Results. A lane holds a feature's. Of a product over tokens the features are neighbours in
