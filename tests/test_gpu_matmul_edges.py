@@ -316,6 +316,38 @@ def test_gradients_stay_in_their_place(ws, E, T, N, K, dtype):
         assert (buf[:at] == 7).all() and (buf[at + n:] == 7).all()
 
 
+@pytest.mark.parametrize("N,K", [(130, 80), (300, 528), (32, 16)])
+def test_rows_of_gradients_of_nothing_and_of_bad_groups(ws, N, K):
+    """Results that leave row by row: groups without rows and calls without rows give zeros, bad
+    groups leave theirs, in a graph as well."""
+    g, x, gv, xv = columns(96, N, K)
+    out = torch.full((6, N, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, **I32)
+    start = torch.tensor([0, 0, 32, 48, 64, 32, 96], **I32)  # 48 no border, 64 .. 32 backwards
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        nv.nvfp4_mx_grouped_wgrad(g, x, start, out=out, workspace=ws, status=status)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        nv.nvfp4_mx_grouped_wgrad(g, x, start, out=out, workspace=ws, status=status)
+    for _ in range(2):
+        assert status.item() == nv.DEV_BAD_INDEX
+        assert not out[0].any() and (out[2:5] == 7).all()
+        for e, a, b in ((1, 0, 32), (5, 32, 96)):
+            ref = gv[:, a:b] @ xv[:, a:b].T
+            assert ((out[e].double() - ref).abs()
+                    <= product_bound(gv[:, a:b], xv[:, a:b], ref)).all()
+        out.fill_(7)
+        status.zero_()
+        graph.replay()
+    none = [{"codes": torch.empty(n, 0, dtype=torch.uint8, device="cuda"),
+             "scales": torch.empty(n, 0, dtype=torch.uint8, device="cuda")} for n in (N, K)]
+    nv.nvfp4_mx_grouped_wgrad(*none, torch.zeros(7, **I32), out=out, workspace=ws)
+    assert not out.any()
+
+
 def test_a_matrix_with_itself(ws):
     """One encoding, and one outer scale, as both operands."""
     x = randn(1, 300, 416)
