@@ -149,9 +149,7 @@ def _act(g, rows, cols, size=1.0):
 def _fp4(x, amax, fp8_max=448.0):
     """NVFP4 code bytes, scale bytes and values of x [..., cols]; amax (of the outer scale)
     broadcasts against x."""
-    # (divided by a tensor: a division by a number is a product with its reciprocal)
-    g = amax / torch.full_like(amax, 6 * fp8_max)
-    g = torch.where(amax > 0, g, torch.ones_like(amax)).unsqueeze(-1)
+    g = torch.where(amax > 0, amax / (6 * fp8_max), torch.ones_like(amax)).unsqueeze(-1)
     b = x.float().unflatten(-1, (-1, 16))
     t = b.abs().amax(-1, keepdim=True) * (1 / (6 * g))
     s8 = t.clamp(max=448.0).to(torch.float8_e4m3fn)
@@ -399,8 +397,7 @@ def _exact_linear(s):
     # (6 g, its reciprocal, the products with it): ties would fall elsewhere in 64
     v = (h * s["w"].double()).float().unflatten(1, (-1, 16))
     top = v.abs().amax(2, keepdim=True)
-    g = top.amax(1, keepdim=True)
-    g = g / torch.full_like(g, 2688)  # a division, not a product with 1 / 2688
+    g = top.amax(1, keepdim=True) / 2688
     e4m3 = torch.arange(127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).double()
     mags = torch.tensor(E2M1, dtype=torch.float64, device="cuda")
     d = _nearest((top * (6 * g).reciprocal()).double().clamp(max=448), e4m3)
