@@ -931,14 +931,21 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       uint32_t taken = 0;
       Work w{};
       bool have = false, ended = false;
+      int held = 0;  // fetches that are not stored yet
       uint4 lo[kAhead][4], hi[kAligned ? 1 : kAhead][4];
       uint32_t off[kAhead];            // low bits of the lane's first address
-      int count[kAhead], lead[kAhead];  // the end of a fetch's stages (0: no more), their begin
+      int count[kAhead], lead[kAhead];  // the end of a fetch's stages (0: none), their begin
       auto fetch = [&](auto slot_c) {
         constexpr int kSlot = decltype(slot_c)::value;
         count[kSlot] = 0;
         while (!have || k >= w.k1) {
           if (ended) return;
+          // Work ahead is not waited for while scales are held here: pieces without stages (groups
+          // without rows) may fill all that can be handed out until the products of the held
+          // scales have run. The slot then stays empty for this turn.
+          if (held > 0 && !__all_sync(kAll, mbar_test(&s.work_full[taken % kWorks],
+                                                      (taken / kWorks) & 1)))
+            return;
           have = take(taken, w);
           if (!have) {
             ended = true;
@@ -955,6 +962,7 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
                          piece * T::kFetch < w.k1 - k;
         const int valid = min((int)p.sf_stride - at, 16);  // bytes of the row in the piece
         count[kSlot] = min(kStages, w.k1 - k);
+        ++held;
         lead[kSlot] = max(w.k0 - k, 0);
         k += kStages;
         const uint8_t* first = base + row0 * p.sf_stride + at;
@@ -978,7 +986,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
       // the stages of a fetch, to shared memory; false at the end
       auto store = [&](auto slot_c) -> bool {
         constexpr int kSlot = decltype(slot_c)::value;
-        if (count[kSlot] == 0) return false;
+        if (count[kSlot] == 0) return !ended || held > 0;
+        --held;
         uint32_t x[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -390,3 +390,36 @@ def test_on_inputs_device_and_refusals():
         good(workspace=torch.zeros(16, **I32))
     with pytest.raises(ValueError):
         good(b={"codes": b["codes"].cpu(), "scales": b["scales"]})
+
+
+# rows of each group: few or many rows, then a dozen and more groups without any for every CTA,
+# then rows again; rows of scales of whole 16 bytes (multiples of 512 rows) and not
+GAPS = [[64] + [0] * 20 + [448], [160] + [0] * 20 + [96], [0] * 3 + [2048] + [0] * 20 + [512],
+        [0] * 20 + [1000 * 32] + [0] * 20 + [32], [32, 0, 0, 96] * 4 + [0] * 30 + [32, 0] * 5]
+
+
+@pytest.mark.parametrize("rows", GAPS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("wide", [True, False])
+def test_many_groups_without_rows_between_others(ws, rows, dtype, wide):
+    """Tiles without sums between tiles with sums, by pairs of CTAs (wide results) and by single
+    ones: every result is there, and no wait runs out."""
+    n, k = (1024, 2048) if wide else (96, 8192)
+    if not wide:  # more groups, for as many pieces of a CTA
+        rows = [r for r in rows for _ in range(1 if r else 3)]
+    total = sum(rows)
+    g, x, gv, xv = columns(total, n, k, seed=total)
+    status = torch.zeros(1, **I32)
+    out = torch.full((len(rows), n, k), 7.0, dtype=dtype, device="cuda")
+    nv.nvfp4_mx_grouped_wgrad(g, x, starts(rows), out=out, workspace=ws, status=status)
+    assert status.item() == 0 and not ws[:384].any()
+    at = np.concatenate([[0], np.cumsum(rows)])
+    for e, r in enumerate(rows):
+        if r == 0:
+            assert not out[e].any(), e
+        else:
+            ga, xa = gv[:, at[e]:at[e + 1]], xv[:, at[e]:at[e + 1]]
+            ref = ga @ xa.T
+            off = (out[e].double() - ref).abs() - product_bound(ga, xa, ref,
+                                                                dtype == torch.float32)
+            assert not (off > 0).any() and out[e].isfinite().all(), e
