@@ -371,13 +371,14 @@ __global__ void __launch_bounds__(kSumWarps * 32) column_sum_kernel(const float*
   }
 }
 
-// CTAs of `kernel` with so many threads on an SM; `fit` keeps the answers by warps.
+// CTAs of `kernel` with so many threads and bytes of shared memory on an SM; `fit` keeps the answer
+// for just these.
 template <class Kernel>
-int ctas_per_sm(Kernel kernel, int threads, std::atomic<int>* fit, size_t smem = 0) {
-  int n = fit[threads / 32].load(std::memory_order_relaxed);
+int ctas_per_sm(Kernel kernel, int threads, std::atomic<int>& fit, size_t smem = 0) {
+  int n = fit.load(std::memory_order_relaxed);
   if (n == 0) {
     n = resident_ctas(kernel, threads, smem);
-    fit[threads / 32].store(n, std::memory_order_relaxed);
+    fit.store(n, std::memory_order_relaxed);
   }
   return n;
 }
@@ -385,7 +386,7 @@ int ctas_per_sm(Kernel kernel, int threads, std::atomic<int>* fit, size_t smem =
 template <int MODE, bool FOS, int K>
 cudaError_t run(const NormParams& p, int threads, cudaStream_t st) {
   static std::atomic<int> fit[kMaxThreads / 32 + 1];
-  const int per_sm = ctas_per_sm(norm_kernel<MODE, FOS, K>, threads, fit);
+  const int per_sm = ctas_per_sm(norm_kernel<MODE, FOS, K>, threads, fit[threads / 32]);
   const int64_t grid = std::min<int64_t>(p.R, (int64_t)sm_count() * per_sm);
   return launch_pdl(norm_kernel<MODE, FOS, K>, dim3((unsigned)grid), dim3(threads), st, p);
 }
@@ -407,8 +408,11 @@ cudaError_t run_bwd(const NormBwdParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(norm_bwd_kernel<K>, kRingBwd, ready);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> fit[kMaxThreads / 32 + 1];
-  const int per_sm = ctas_per_sm(norm_bwd_kernel<K>, threads, fit, (size_t)depth * row);
+  // (by the width, which shared memory goes by: the grid decides how gw's sum is grouped, and the
+  // same call has to give the same bits whatever was called before it)
+  static std::atomic<int> fit[kNormMaxCols / 16 + 1];
+  const int per_sm =
+      ctas_per_sm(norm_bwd_kernel<K>, threads, fit[p.C / 16], (size_t)depth * row);
   const int64_t grid = std::min<int64_t>(
       std::min<int64_t>(p.R, (int64_t)sm_count() * per_sm), std::max<int64_t>(1, kNormPart / p.C));
   e = launch_pdl_smem(norm_bwd_kernel<K>, dim3((unsigned)grid), dim3(threads),

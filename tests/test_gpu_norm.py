@@ -1,9 +1,13 @@
 """The residual norm with its encodings and its gradient against plain forms in 64 bits, byte for
 byte where the codes do not depend on how a sum rounds."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import nvfp4_block_scaled_02_gb300 as nv
+from conftest import ROOT
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -330,3 +334,26 @@ def test_two_streams_at_once():
     for s in (0, 1):
         for i, r in enumerate(got[s]):
             assert all(torch.equal(a, b) for a, b in zip(r, alone[::1 - 2 * s][i % 3]))
+
+
+BITS = """
+import hashlib, sys, torch
+import nvfp4_block_scaled_02_gb300 as nv
+for cols in map(int, sys.argv[1:]):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(cols)
+    gy, h = (torch.randn(8192, cols, generator=g, device="cuda").bfloat16() for _ in range(2))
+    gw = nv.nvfp4_add_rms_norm_bwd(gy, h, h[0].clone())["gw"]
+    print(cols, hashlib.sha256(gw.cpu().numpy().tobytes()).hexdigest())
+"""
+
+
+def test_weight_gradients_bits_do_not_depend_on_earlier_calls():
+    """Widths of one number of warps in either order, each order in a process of its own."""
+    lines = []
+    for order in (["64", "128", "192", "256"], ["256", "192", "128", "64"]):
+        r = subprocess.run([sys.executable, "-c", BITS, *order], cwd=ROOT, capture_output=True,
+                           text=True, timeout=300)
+        assert r.returncode == 0, r.stderr
+        lines.append(sorted(r.stdout.splitlines()))
+    assert len(lines[0]) == 4 and lines[0] == lines[1]
