@@ -151,8 +151,10 @@ nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint8_t* g_sca
   if (!aligned(group_start, 4) || !aligned(status, 4)) return NVFP4_ERR_ALIGN;
   nvfp4::MatmulParams p{};
   // The product's lanes are features. With g's rows there a lane holds a piece of a result's row
-  // of bf16, whole 32 bytes of which leave at a time; else x's rows, whose lanes hold neighbours.
-  p.turn = !out_fp32 && out_cols % 16 == 0 && aligned(out, 32);
+  // of bf16, which leaves by tensor map where rows are whole 32 bytes; else x's rows, whose lanes
+  // hold neighbours. (Not by out's address: the two are cut differently, and the order of a sum
+  // depends on the sizes alone.)
+  p.turn = !out_fp32 && out_cols % 16 == 0;
   p.f_sf = p.turn ? g_scales : x_scales;
   p.c_sf = p.turn ? x_scales : g_scales;
   p.f_rows = p.turn ? out_rows : out_cols;

@@ -142,13 +142,6 @@ __device__ __forceinline__ uint4 first_bytes(uint4 x, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 32 bytes, 32-byte aligned
-__device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
-               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
 // Copies of n columns: large boxes as far as they fill, then one more or, for up to half
 // of it, small ones.
 struct Boxes {
@@ -557,11 +550,15 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
             fence_smem_async();
             __syncwarp();
             if (lane == 0) tma_store(&maps.out, w.c0 + c, f, w.g, smem_addr(at));
-          } else if (f < p.N) {  // a sum's parts: 16 columns
-            uint32_t x[kN / 2];
+          } else if (f < p.N) {  // a sum's parts: 16 columns, at 16 bytes (as the map's base)
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                ((int64_t)w.g * p.N + f) * p.C + w.c0 + c);
 #pragma unroll
-            for (int j = 0; j < kN / 2; ++j) x[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-            store32(static_cast<uint16_t*>(p.out) + ((int64_t)w.g * p.N + f) * p.C + w.c0 + c, x);
+            for (int j = 0; j < kN / 8; ++j)
+              o[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
+                                pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
           }
           return;
         }

@@ -423,3 +423,22 @@ def test_many_groups_without_rows_between_others(ws, rows, dtype, wide):
             off = (out[e].double() - ref).abs() - product_bound(ga, xa, ref,
                                                                 dtype == torch.float32)
             assert not (off > 0).any() and out[e].isfinite().all(), e
+
+
+@pytest.mark.parametrize("E,T,N,K", [(1, 8192, 1000, 64), (1, 4096, 128, 16), (1, 16384, 200, 160),
+                                     (2, 8192, 64, 528), (4, 1024, 1000, 1040)])
+def test_gradients_bits_do_not_depend_on_alignment(ws, E, T, N, K):
+    """Sums that are cut into parts too: the same order at 16-byte as at larger boundaries."""
+    g, x, gv, xv = columns(T, N, K)
+    start = torch.tensor([T // E // 32 * 32 * e for e in range(E)] + [T], **I32)
+    want = nv.nvfp4_mx_grouped_wgrad(g, x, start, workspace=ws)
+    at, n = start.tolist(), E * N * K
+    for e in range(E):
+        ga, xa = gv[:, at[e]:at[e + 1]], xv[:, at[e]:at[e + 1]]
+        ref = ga @ xa.T
+        assert ((want[e].double() - ref).abs() <= product_bound(ga, xa, ref)).all()
+    for first in (8, 16, 24):
+        buf = torch.full((n + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        nv.nvfp4_mx_grouped_wgrad(g, x, start, out=buf[first:first + n].view(E, N, K), workspace=ws)
+        assert torch.equal(buf[first:first + n].view(E, N, K), want)
+        assert (buf[:first] == 7).all() and (buf[first + n:] == 7).all()
