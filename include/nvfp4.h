@@ -639,8 +639,10 @@ NVFP4_API nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint
  * be NULL) the values that the codes stand for.
  * cfg: blocks NVFP4_BLOCKS_ROW, rounding NVFP4_ROUND_RNE.
  * Data errors: NVFP4_DEV_NONFINITE_INPUT (also for a sum of squares or a product
- * h * weight past fp32), NVFP4_DEV_BAD_AMAX. A row whose mean square and eps are 0
- * gives zeros.
+ * h * weight past fp32), NVFP4_DEV_BAD_AMAX. A row with NaN or Inf, or whose sum of
+ * squares is past fp32, gets NaN throughout: y, dequant, row_amax, NVFP4 scales,
+ * MXFP8 codes; a NaN of the weight its blocks (its rows, with row_amax). A row
+ * whose mean square and eps are 0 gives zeros.
  * Errors: NULL required pointers, target, eps negative or not finite, and config
  * fields out of range, dequant with MXFP8 (NVFP4_ERR_ENUM), sizes, misaligned
  * buffers. */
@@ -656,7 +658,9 @@ NVFP4_API nvfp4_status nvfp4_add_rms_norm(const nvfp4_config* cfg, int32_t targe
  *   gx = r * (u - h * r^2 * mean(u * h)) + gh      (of x and of the residual)
  *   gw = sum over the rows of gy * h * r           (fp32 [cols], overwritten)
  * cols % 16 == 0, up to 16384. gx may be gy, h or gh. gw is summed in a fixed
- * order: the same inputs give the same bits on the same device.
+ * order: the same inputs give the same bits on the same device. A row of h with
+ * NaN or Inf, or whose sum of squares is past fp32, gives NaN in its gx and in gw
+ * (NVFP4_DEV_NONFINITE_INPUT).
  * workspace: device memory, >= nvfp4_add_rms_norm_ws_bytes() bytes, 16-byte
  * aligned, of any content; it serves one call at a time.
  * Errors: as nvfp4_add_rms_norm; NVFP4_ERR_SHAPE for a workspace too small. */

@@ -42,14 +42,23 @@ __device__ __forceinline__ uint4 pack8(const f2 (&v)[4]) {
   return make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
                     pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
 }
+__device__ __forceinline__ float nan32() { return __uint_as_float(0x7FFFFFFFu); }
+// The largest magnitude; with NANS, NaN if one is.
+template <bool NANS>
 __device__ __forceinline__ float absmax8(const f2 (&v)[4], float m) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmax3(m, fabsf(v[i].x), fabsf(v[i].y));
+  for (int i = 0; i < 4; ++i) {
+    const float a = fabsf(v[i].x), b = fabsf(v[i].y);
+    if constexpr (NANS) asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(a), "f"(b));
+    else m = fmax3(m, a, b);
+  }
   return m;
 }
-// 1 / sqrt(mean + eps); 0 for a row of zeros without eps
+// 1 / sqrt(mean + eps); 0 for a row of zeros without eps, NaN where the sum is no finite number
+// (NaN or infinite values, squares past fp32), so that the row's results show it
 __device__ __forceinline__ float inv_rms(float sum, int C, float eps) {
   const float m = __fadd_rn(__fdiv_rn(sum, (float)C), eps);
+  if (!(m <= kFltMax)) return nan32();
   return m > 0.0f ? rsqrtf(m) : 0.0f;
 }
 
@@ -113,7 +122,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
           unpack8(wt[k][i], w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = f2_mul(v[j], w[j]);
-          m = absmax8(v, m);
+          m = absmax8<true>(v, m);
         }
       }
     }
@@ -132,22 +141,24 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
     m = s_max[par][0];
     for (int i = 1; i < warps; ++i) {
       sum = __fadd_rn(sum, s_sum[par][i]);
-      m = fmaxf(m, s_max[par][i]);
+      m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(s_max[par][i])));
     }
     const float r = inv_rms(sum, p.C, p.eps);
     SliceScale ss = st;
     float g = 0.0f;  // of the values that the codes stand for
+    bool bad = r != r;
     if constexpr (MODE == kRow) {
+      bad = bad || !(m <= kFltMax);
       ss = slice_scale(m, p.M);
       // (r m may be too small for 32 bits where m is not 0: then the row's values are 0)
-      const float top = m > 0.0f ? fmaxf(__fmul_rn(m, r), __uint_as_float(1u)) : 0.0f;
+      const float top =
+          bad ? nan32() : m > 0.0f ? fmaxf(__fmul_rn(m, r), __uint_as_float(1u)) : 0.0f;
       g = slice_scale(top, p.M).g;
       if (tid == 0) p.row_amax[row] = top;
-      if (tid == 0 && !(m <= kFltMax)) flag(p.status, NVFP4_DEV_NONFINITE_INPUT);
     } else {
       g = ss.g;
     }
-    if (tid == 0 && !(sum <= kFltMax)) flag(p.status, NVFP4_DEV_NONFINITE_INPUT);
+    if (tid == 0 && bad) flag(p.status, NVFP4_DEV_NONFINITE_INPUT);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int b = k * nt + tid;
@@ -174,7 +185,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
           if (p.y && ok) __stcs(p.y + 2 * at + i, pack8(v[i]));
         }
       }
-      float bm = absmax8(v[1], absmax8(v[0], 0.0f));
+      float bm = absmax8<true>(v[1], absmax8<true>(v[0], 0.0f));
+      // A NVFP4 block with a value that is no finite number gets a NaN for its scale; an MXFP8
+      // code can be NaN, and infinities saturate.
+      if (!(bm <= kFltMax)) {
+        flag(p.status, NVFP4_DEV_NONFINITE_INPUT);
+        bm = MODE == kMx ? absmax8<false>(v[1], absmax8<false>(v[0], 0.0f)) : nan32();
+      }
+      if (MODE != kMx && bad) bm = nan32();
       if constexpr (MODE == kMx) {
         // the block of 32 is this thread's 16 values and its neighbour's
         bm = fmaxf(bm, __shfl_xor_sync(kAll, bm, 1));
@@ -199,7 +217,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
           __stcs(reinterpret_cast<uint2*>(p.codes) + at, make_uint2(q.codes[0], q.codes[1]));
           p.scales[at] = (uint8_t)q.scale;
           if (p.dq) {
-            const float d = __fmul_rn(e4m3_value(q.scale), g);
+            const float d = bm == bm ? __fmul_rn(e4m3_value(q.scale), g) : bm;
             f2 t[4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {

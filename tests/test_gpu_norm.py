@@ -357,3 +357,89 @@ def test_weight_gradients_bits_do_not_depend_on_earlier_calls():
         assert r.returncode == 0, r.stderr
         lines.append(sorted(r.stdout.splitlines()))
     assert len(lines[0]) == 4 and lines[0] == lines[1]
+
+
+def is_nan(scales):
+    """Of scale bytes: NaN of E4M3."""
+    return scales == 0x7F
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 1e30])
+@pytest.mark.parametrize("cols", [96, 16384])
+def test_rows_that_are_no_numbers_show_it(bad, cols):
+    """Such a row's results are NaN throughout (1e30: its squares are past fp32), the other rows'
+    as without it; so are the product's rows and the gradients."""
+    rows, w = 5, weight(1, cols)
+    clean = randn(2, rows, cols)
+    rest = [0, 1, 2, 4]
+    weights = randn(7, 1, 40, cols, size=cols ** -0.5)
+    b_amax = nv.nvfp4_amax(weights)
+    b = nv.nvfp4_quantize(weights, b_amax, dequant=False)["row"]
+    one = torch.full((1,), 9.0, device="cuda")
+    for at in (0, cols - 1):
+        x = clean.clone()
+        x[3, at] = bad
+        for fos in (0, 1):
+            cfg = nv.Config(four_over_six=fos)
+            for amax in (None, one):
+                status = torch.zeros(1, dtype=torch.int32, device="cuda")
+                kw = dict(cfg=cfg, global_amax=amax, dequant=True)
+                want = nv.nvfp4_add_rms_norm(clean, w, y=torch.empty_like(x), **kw)
+                r = nv.nvfp4_add_rms_norm(x, w, y=torch.empty_like(x), status=status, **kw)
+                assert status.item() == nv.DEV_NONFINITE_INPUT
+                assert r["y"][3].isnan().all() and r["dequant"][3].isnan().all()
+                assert is_nan(r["scales"][3]).all()
+                for name in ("y", "codes", "scales", "dequant"):
+                    assert torch.equal(r[name][rest], want[name][rest])
+                if amax is None:
+                    assert r["row_amax"][3].isnan()
+                    assert torch.equal(r["row_amax"][rest], want["row_amax"][rest])
+                a = one if amax is not None else r["row_amax"]
+                out = nv.nvfp4_grouped_matmul(r, a, b, b_amax, a_cfg=cfg)
+                assert out[3].isnan().all() and out[rest].isfinite().all()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        want = nv.nvfp4_add_rms_norm(clean, w, target=nv.TARGET_MXFP8)
+        r = nv.nvfp4_add_rms_norm(x, w, target=nv.TARGET_MXFP8, status=status)
+        assert status.item() == nv.DEV_NONFINITE_INPUT
+        assert r["codes"][3].view(torch.float8_e4m3fn).float().isnan().all()
+        assert torch.equal(r["codes"][rest], want["codes"][rest])
+        assert torch.equal(r["scales"][rest], want["scales"][rest])
+        gy, gh = randn(3, rows, cols), randn(4, rows, cols)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        want = nv.nvfp4_add_rms_norm_bwd(gy, clean, w, gh)
+        r = nv.nvfp4_add_rms_norm_bwd(gy, x, w, gh, status=status)
+        assert status.item() == nv.DEV_NONFINITE_INPUT
+        assert r["gx"][3].isnan().all() and torch.equal(r["gx"][rest], want["gx"][rest])
+        assert r["gw"].isnan().all()
+
+
+def test_weights_that_are_no_numbers_show_it():
+    """A NaN of the weight reaches its block of every row under a tensor's scale and its value in
+    MXFP8, every row with a scale of its own; all of it is flagged."""
+    x, w = randn(1, 5, 96), weight(2, 96)
+    bad = w.clone()
+    bad[37] = float("nan")
+    one = torch.full((1,), 9.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = nv.nvfp4_add_rms_norm(x, w, global_amax=one, dequant=True)
+    r = nv.nvfp4_add_rms_norm(x, bad, global_amax=one, dequant=True, status=status)
+    assert status.item() == nv.DEV_NONFINITE_INPUT
+    assert torch.equal(is_nan(r["scales"]), torch.arange(6, device="cuda").eq(2).expand(5, 6))
+    nan = torch.arange(96, device="cuda").div(16, rounding_mode="floor").eq(2).expand(5, 96)
+    assert torch.equal(r["dequant"].isnan(), nan)
+    assert torch.equal(r["dequant"][~nan], want["dequant"][~nan])
+    status.zero_()
+    r = nv.nvfp4_add_rms_norm(x, bad, status=status)
+    assert status.item() == nv.DEV_NONFINITE_INPUT
+    assert is_nan(r["scales"]).all() and r["row_amax"].isnan().all()
+    status.zero_()
+    want = nv.nvfp4_add_rms_norm(x, w, target=nv.TARGET_MXFP8)
+    r = nv.nvfp4_add_rms_norm(x, bad, target=nv.TARGET_MXFP8, status=status)
+    assert status.item() == nv.DEV_NONFINITE_INPUT
+    v = r["codes"].view(torch.float8_e4m3fn).float()
+    nan = torch.arange(96, device="cuda").eq(37).expand(5, 96)
+    assert torch.equal(v.isnan(), nan)
+    keep = torch.tensor([0, 2], device="cuda")  # blocks of 32 without it
+    assert torch.equal(r["scales"][:, keep], want["scales"][:, keep])
+    assert torch.equal(v.view(5, 3, 32)[:, keep],
+                       want["codes"].view(torch.float8_e4m3fn).float().view(5, 3, 32)[:, keep])
