@@ -296,8 +296,9 @@ def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor,
     MXFP8 (target). x, residual: bf16 [rows, cols]; weight: bf16 [cols]. Returns {"h",
     "y", "codes", "scales", "choice", "dequant", "row_amax"}: h is x itself without a
     residual, y (bf16) is written where a buffer is passed, dequant (NVFP4) where asked
-    for. `out`: an encoding of an earlier call. Nothing is recorded for autograd:
-    nvfp4_add_rms_norm_bwd gives the gradient."""
+    for, choice with Four-Over-Six; what a call does not write is None. `out`: an
+    encoding of an earlier call, written where it lies (its dequant too, if it has one).
+    Nothing is recorded for autograd: nvfp4_add_rms_norm_bwd gives the gradient."""
     dev = x.get_device()
     if dev >= 0 and dev != _device():
         with torch.cuda.device(dev):
@@ -346,13 +347,17 @@ def nvfp4_add_rms_norm(x: torch.Tensor, weight: torch.Tensor,
         o = _OUT.pack(codes.data_ptr(), scales.data_ptr(), choice.data_ptr() if fos else 0,
                       0 if dq is None else dq.data_ptr())
     else:
-        codes, scales, choice, dq = (out["codes"], out["scales"], out.get("choice"),
-                                     out.get("dequant"))
+        codes, scales, dq = out["codes"], out["scales"], out.get("dequant")
+        choice = out.get("choice") if fos else None
+        if dequant and dq is None:
+            raise ValueError("dequant is asked for, but out has no buffer for it")
+        if dq is not None and not fp4:
+            raise ValueError("out has a dequant buffer, which is of the NVFP4 target")
         o = _OUT.pack(
             _bytes(codes, "out codes", R * Cc // per, dev),
             _bytes(scales, "out scales", R * Cc // block, dev),
-            _optional(choice, "out choice", R * ((Cc + 511) // 512), _I32, dev) if fos else 0,
-            _optional(dq, "out dequant", R * Cc, _BF16, dev) if fp4 else 0)
+            _optional(choice, "out choice", R * ((Cc + 511) // 512), _I32, dev),
+            _optional(dq, "out dequant", R * Cc, _BF16, dev))
     amax_at = row_at = 0
     if not fp4:
         row_amax = None

@@ -443,3 +443,27 @@ def test_weights_that_are_no_numbers_show_it():
     assert torch.equal(r["scales"][:, keep], want["scales"][:, keep])
     assert torch.equal(v.view(5, 3, 32)[:, keep],
                        want["codes"].view(torch.float8_e4m3fn).float().view(5, 3, 32)[:, keep])
+
+
+def test_an_earlier_calls_encoding_holds_what_this_call_wrote():
+    """Into an encoding of an earlier call: nothing of that call is handed on, and what has no
+    place is refused."""
+    x, w = randn(1, 4, 1056), weight(2, 1056)
+    fos = nv.Config(four_over_six=1)
+    first = nv.nvfp4_add_rms_norm(randn(3, 4, 1056), w, cfg=fos, dequant=True)
+    choice = first["choice"].clone()
+    want = nv.nvfp4_add_rms_norm(x, w, dequant=True)
+    r = nv.nvfp4_add_rms_norm(x, w, out=first)
+    assert r["choice"] is None and torch.equal(first["choice"], choice)
+    for name in ("codes", "scales", "dequant"):
+        assert r[name] is first[name] and torch.equal(r[name], want[name])
+    again = nv.nvfp4_add_rms_norm(x, w, cfg=fos, out=first)
+    assert again["choice"] is first["choice"]
+    assert torch.equal(again["choice"], nv.nvfp4_add_rms_norm(x, w, cfg=fos)["choice"])
+    plain = nv.nvfp4_add_rms_norm(x, w)
+    with pytest.raises(ValueError):
+        nv.nvfp4_add_rms_norm(x, w, out=plain, dequant=True)
+    mx = nv.nvfp4_add_rms_norm(x, w, target=nv.TARGET_MXFP8)
+    assert nv.nvfp4_add_rms_norm(x, w, target=nv.TARGET_MXFP8, out=mx)["codes"] is mx["codes"]
+    with pytest.raises(ValueError):
+        nv.nvfp4_add_rms_norm(x, w, target=nv.TARGET_MXFP8, out={**mx, "dequant": first["dequant"]})
