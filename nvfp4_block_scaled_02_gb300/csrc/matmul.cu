@@ -81,6 +81,9 @@ constexpr int kBand = 8;                       // column tiles of a band
 // Columns of a group from which pairs of CTAs pay: 64 experts of 64 rows 91 us alone and 94 in
 // pairs, of 96 rows 93 both, of 256 rows 119 and 111.
 constexpr int kPairCols = 96;
+// Tiles of a call at most: groups in order have 2^26 (the entry points refuse more), groups out of
+// order may share rows, and their sums stay at this number.
+constexpr int kMaxTiles = 1 << 27;
 constexpr double kPadGain = 0.3;               // see launch_matmul
 constexpr long long kWaitCycles = 2000000000;  // about a second
 
@@ -345,17 +348,18 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
         most = max(most, c_tiles == 1 ? cols
                                       : (int)((uint32_t)(cols + c_tiles - 1) / (uint32_t)c_tiles));
       s.tile[e] = mine;
-      mine += c_tiles * f_tiles;
+      mine = min(mine + c_tiles * f_tiles, kMaxTiles);
     }
     int incl = mine;
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(kAll, incl, d);
-      if (lane >= d) incl += o;
+      if (lane >= d) incl = min(incl + o, kMaxTiles);
     }
+    before = __shfl_up_sync(kAll, incl, 1);
+    if (lane == 0) before = 0;
     most = __reduce_max_sync(kAll, most);
     if (lane == 31) s.scan[warp] = incl;
     if (lane == 0) s.most[warp] = most;
-    before = incl - mine;
   }
   fence_before();
   __syncthreads();
@@ -364,11 +368,11 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
   if (scan) {
     int total = 0, most = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += s.scan[w];
-      total += s.scan[w];
+      if (w < warp) before = min(before + s.scan[w], kMaxTiles);
+      total = min(total + s.scan[w], kMaxTiles);
       most = max(most, s.most[w]);
     }
-    for (int e = e0; e < e1; ++e) s.tile[e] += before;
+    for (int e = e0; e < e1; ++e) s.tile[e] = min(s.tile[e] + before, kMaxTiles);
     if (tid == 0) {
       s.tile[p.E] = total;
       s.geo = geometry<KIND, CG>(total, most, (int)((p.K + T::kStageK - 1) / T::kStageK), pairs,

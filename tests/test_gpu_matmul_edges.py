@@ -442,3 +442,35 @@ def test_gradients_bits_do_not_depend_on_alignment(ws, E, T, N, K):
         nv.nvfp4_mx_grouped_wgrad(g, x, start, out=buf[first:first + n].view(E, N, K), workspace=ws)
         assert torch.equal(buf[first:first + n].view(E, N, K), want)
         assert (buf[:first] == 7).all() and (buf[first + n:] == 7).all()
+
+
+@pytest.mark.parametrize("T", [300, 1 << 30])
+def test_groups_that_share_rows(ws, T):
+    """Borders that go back and forth: every other of 1024 groups has all rows (with 2^30 of them
+    2^31 tiles, past 32 bits), the others are out of order. All have the same weights, so that the
+    results are known; nothing around them is written."""
+    E, K = 1024, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    codes = torch.empty(T, K // 2, dtype=torch.uint8, device="cuda")
+    codes.random_(0, 256, generator=g)
+    scales = torch.empty(T, K // 16, dtype=torch.uint8, device="cuda")
+    scales.random_(0x30, 0x50, generator=g)
+    bc = torch.randint(0, 256, (1, 1, K // 2), generator=g, dtype=torch.uint8, device="cuda")
+    bs = torch.randint(0x30, 0x50, (1, 1, K // 16), generator=g, dtype=torch.uint8, device="cuda")
+    one = torch.full((1,), 2688.0, device="cuda")  # outer scales of 1
+    b = {"codes": bc.expand(E, 1, -1).contiguous(), "scales": bs.expand(E, 1, -1).contiguous()}
+    start = torch.tensor([0, T] * (E // 2) + [0], **I32)
+    status = torch.zeros(1, **I32)
+    buf = torch.full((T + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    nv.nvfp4_grouped_matmul({"codes": codes, "scales": scales}, one, b, one.expand(E).contiguous(),
+                            start, out=buf[32:32 + T].view(T, 1), workspace=ws, status=status)
+    assert status.item() == nv.DEV_BAD_INDEX
+    assert (buf[:32] == 7).all() and (buf[32 + T:] == 7).all()
+    n = min(T, 1 << 20)
+    bv = fp4_values(bc[0], bs[0], one)
+    for at in (0, (T - n) // 2, T - n):
+        av = fp4_values(codes[at:at + n], scales[at:at + n], one.expand(n))
+        ref = av @ bv.T
+        out = buf[32 + at:32 + at + n, None].double()
+        assert ((out - ref).abs() <= product_bound(av, bv, ref)).all()
