@@ -580,7 +580,9 @@ typedef struct {
  * owns are not written.
  * workspace: device memory, >= nvfp4_grouped_matmul_ws_bytes() bytes, 16-byte
  * aligned, its first 4096 bytes ZERO before its first use; every call leaves them
- * zero again. It serves one call (of any of the three products) at a time.
+ * zero again. It serves one call (of any of the three products) at a time. 64 MB
+ * of its 89 are for scale rows that are not whole 16 bytes, which long sums copy
+ * to whole ones first; operands with more of them are read as they are, slower.
  * Data errors: NVFP4_DEV_BAD_INDEX for group_start out of order or outside [0,
  * rows] (such a group is left out), NVFP4_DEV_BAD_AMAX, NVFP4_DEV_TIMEOUT
  * (results and workspace are then not valid). NaN scale bytes give NaN.
@@ -612,7 +614,8 @@ NVFP4_API nvfp4_status nvfp4_mx_grouped_matmul(const uint8_t* a_codes, const uin
  * to 2^25, rows % 32 == 0 and every entry of group_start a multiple of 32 (pad an expert's rows
  * with zeros): another one is NVFP4_DEV_BAD_INDEX, and its groups' results are
  * not written. A group without rows gets zeros. out: bf16, or fp32 with out_fp32
- * = 1, [groups][out_rows][out_cols]. Otherwise as nvfp4_mx_grouped_matmul. */
+ * = 1, [groups][out_rows][out_cols]; fastest in bf16 with out_cols % 16 == 0.
+ * Otherwise as nvfp4_mx_grouped_matmul. */
 NVFP4_API nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint8_t* g_scales,
                                               const uint8_t* x_codes, const uint8_t* x_scales,
                                               int64_t rows, int64_t groups, int64_t out_rows,

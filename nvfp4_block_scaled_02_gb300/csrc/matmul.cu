@@ -31,22 +31,25 @@
 // the way from L2 gives an SM about 50 bytes a clock, 660 clocks, and both share the port of shared
 // memory. A single CTA's 128 x 256 tile needs 48 KB a stage (NVFP4 8192^3: 205 us without any
 // products, pairs 184). Measured, operations a second in the device's time: dense 8192^3 NVFP4
-// 5.9 PFLOP/s (3.0 times the measured cuBLAS bf16 rate), MXFP8 3.5 (1.8 times). Where columns are
-// few the weights' bytes bound it: 64 experts of 2048 x 7168, 90 rows, 62 us, 83% of the copy
-// rate; 16384 ragged rows 127 us (77% of the copy rate, 3.8 PFLOP/s). Weights' gradients write as
-// much as they read and their sums are short: 16 experts of 2048 x 7168, 16384 rows, 189 us (2.5
+// 5.9 PFLOP/s (3.1 times the measured cuBLAS bf16 rate), MXFP8 3.6 (1.9 times). Where columns are
+// few the weights' bytes bound it: 64 experts of 2048 x 7168, 90 rows, 61 us, 84% of the copy
+// rate; 16384 ragged rows 126 us (77% of the copy rate, 3.8 PFLOP/s). Weights' gradients write as
+// much as they read and their sums are short: 16 experts of 2048 x 7168, 16384 rows, 188 us (2.6
 // PFLOP/s), of which the results' way out is 20 us (the change of accumulators is 700 to 1000
-// clocks a tile of 8 stages, but products that do not wait for it gain 3 us). Small calls take 6 to 13 us, most of it the way to the first copy (cold
-// code and constants, 2 us), DRAM latency and the results.
+// clocks a tile of 8 stages, but products that do not wait for it gain 3 us). These are times at
+// the full clock, 2070 MHz: for seconds on end the power limit holds weights' gradients at 1640
+// MHz (213 us) and the ragged NVFP4 rows at 1720 (136). Small calls take 6 to 13 us, most of it
+// the way to the first copy (cold code and constants, 2 us), DRAM latency and the results.
 //
 // Results. A lane holds a feature's. Of a product over tokens the features are neighbours in
 // memory: lanes swap halves with a shuffle and store 4 bytes. That is nine instructions for two
 // values, which a tile of 8 stages has no time for (5800 of its 6700 clocks). A weights' gradient's
 // features may be either operand's rows: g's, so that a lane's results are a row's, which go to
-// shared memory 16 bytes at a time and leave by tensor map, for one stage of the ring less (202 us
+// shared memory 16 bytes at a time and leave by tensor map, for one stage of the ring less (199 us
 // to 189; 1000 x 544 8.5 to 7.5; sums of 32 stages 147 to 148). Stored from the lanes they took 213
 // us in pieces of 32 bytes and 294 of 16; tokens' results by tensor map gain nothing (126 us, MXFP8
-// 173 to 175). fp32 results and rows that are not whole 32 bytes go the other way.
+// 173 to 175). fp32 results and rows that are not whole 32 bytes go the other way (16 equal experts
+// 235 us in fp32, 174 in bf16).
 //
 // Tried: results turned in shared memory by stmatrix for 16-byte stores (weights' gradient 218 ->
 // 248 us: shared memory has no time to spare); every warp finding its own work (220 -> 202 when
@@ -607,6 +610,8 @@ matmul_kernel(const __grid_constant__ Maps maps, const MatmulParams p, const Geo
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
         if (i == 0 && sum) {
+          // (the reads are complete at tmem_wait_ld, and nothing of memory is handed over: an
+          // arrival without cluster scope does for the pair's first CTA as well)
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_first(&s.acc_free);
