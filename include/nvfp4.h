@@ -643,9 +643,11 @@ NVFP4_API nvfp4_status nvfp4_mx_grouped_wgrad(const uint8_t* g_codes, const uint
  * cfg: blocks NVFP4_BLOCKS_ROW, rounding NVFP4_ROUND_RNE.
  * Data errors: NVFP4_DEV_NONFINITE_INPUT (also for a sum of squares or a product
  * h * weight past fp32), NVFP4_DEV_BAD_AMAX. A row with NaN or Inf, or whose sum of
- * squares is past fp32, gets NaN throughout: y, dequant, row_amax, NVFP4 scales,
- * MXFP8 codes; a NaN of the weight its blocks (its rows, with row_amax). A row
- * whose mean square and eps are 0 gives zeros.
+ * squares is past fp32, gets NaN throughout: y, dequant, row_amax, NVFP4 scales
+ * (their codes 0), MXFP8 codes; a NaN of the weight its blocks (its rows, with
+ * row_amax). The products carry NaN scales on; nvfp4_requant_transpose, which reads
+ * every scale byte as a number, finds zeros. A row whose mean square and eps are 0
+ * gives zeros.
  * Errors: NULL required pointers, target, eps negative or not finite, and config
  * fields out of range, dequant with MXFP8 (NVFP4_ERR_ENUM), sizes, misaligned
  * buffers. */

@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
         }
       }
       float bm = absmax8<true>(v[1], absmax8<true>(v[0], 0.0f));
-      // A NVFP4 block with a value that is no finite number gets a NaN for its scale; an MXFP8
-      // code can be NaN, and infinities saturate.
+      // A NVFP4 block with a value that is no finite number gets a NaN for its scale and codes of 0
+      // (nvfp4_requant_transpose knows no NaN scales); an MXFP8 code can be NaN, and infinities
+      // saturate.
       if (!(bm <= kFltMax)) {
         flag(p.status, NVFP4_DEV_NONFINITE_INPUT);
         bm = MODE == kMx ? absmax8<false>(v[1], absmax8<false>(v[0], 0.0f)) : nan32();
@@ -213,8 +214,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
         }
       } else {
         const uint4 none = make_uint4(0, 0, 0, 0);
-        const BlockResult q = encode_block_f<0, false, FOS>(
-            v[0], v[1], bm, ss, DirectScales<0>{ss.g}, none, none, false);
+        BlockResult q = encode_block_f<0, false, FOS>(v[0], v[1], bm, ss, DirectScales<0>{ss.g},
+                                                      none, none, false);
+        if (bm != bm) q.codes[0] = q.codes[1] = 0;
         if (ok) {
           __stcs(reinterpret_cast<uint2*>(p.codes) + at, make_uint2(q.codes[0], q.codes[1]));
           p.scales[at] = (uint8_t)q.scale;

@@ -467,3 +467,28 @@ def test_an_earlier_calls_encoding_holds_what_this_call_wrote():
     assert nv.nvfp4_add_rms_norm(x, w, target=nv.TARGET_MXFP8, out=mx)["codes"] is mx["codes"]
     with pytest.raises(ValueError):
         nv.nvfp4_add_rms_norm(x, w, target=nv.TARGET_MXFP8, out={**mx, "dequant": first["dequant"]})
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 1e30])
+@pytest.mark.parametrize("fos", [0, 1])
+def test_rows_that_are_no_numbers_are_zeros_to_the_transpose(bad, fos):
+    """Re-quantised for a weights' gradient such a row is a row of zeros, whatever its blocks'
+    scales, and the product has NaN in its row alone."""
+    rows, cols, w = 64, 512, weight(1, 512)
+    cfg, amax = nv.Config(four_over_six=fos), torch.full((1,), 9.0, device="cuda")
+    zero = randn(2, rows, cols)
+    zero[37] = 0
+    x = zero.clone()
+    x[37, 100] = bad
+    out = []
+    for v in (zero, x):
+        r = nv.nvfp4_add_rms_norm(v, w, cfg=cfg, global_amax=amax)
+        out.append((r, nv.nvfp4_requant_transpose(r["codes"], r["scales"], amax, cfg, nv.Config())))
+    (a, at), (b, bt) = out
+    assert is_nan(b["scales"][37]).all() and not b["codes"][37].any()
+    assert torch.equal(at["codes"], bt["codes"]) and torch.equal(at["scales"], bt["scales"])
+    p = nv.nvfp4_grouped_matmul(b, amax, a, amax, a_cfg=cfg, b_cfg=cfg)
+    q = nv.nvfp4_grouped_matmul(a, amax, a, amax, a_cfg=cfg, b_cfg=cfg)
+    assert p[37].isnan().all()
+    p[37] = q[37]
+    assert torch.equal(p, q)
